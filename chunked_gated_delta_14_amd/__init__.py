@@ -20,6 +20,10 @@ __all__ = [
     "Problem", "kda_fwd", "kda_bwd", "gdn_fwd", "gdn_bwd", "kda_ckpt", "gdn_ckpt", "kda_ckpt_noalloc",
     "GDR_NOALLOC_SCRATCH_BYTES", "status_string",
     "check_device", "walk_layout_chosen", "timing_enable", "timing_read", "EXPORTED_SYMBOLS",
+    "GDR_BF16", "GDR_F32", "GDR_ACT_NONE", "GDR_ACT_SILU", "GDR_ACT_SIGMOID", "GDR_GATE_SOFTPLUS", "GDR_GATE_SIGMOID",
+    "GDR_RES_NONE", "GDR_RES_BEFORE", "GDR_RES_AFTER", "Plan", "ConvProblem", "conv_fwd", "conv_bwd", "conv_workspace_bytes",
+    "ConvStep", "conv_step", "GateProblem", "gate_fwd", "gate_bwd", "gate_workspace_bytes", "StepProblem", "kda_step",
+    "gdn_step", "NormProblem", "norm_fwd", "norm_bwd", "norm_workspace_bytes",
 ]
 
 GDR_KDA = 0
@@ -36,6 +40,8 @@ EXPORTED_SYMBOLS = (
     "gdr_gdn_bwd", "gdr_kda_ckpt", "gdr_gdn_ckpt", "gdr_check_device", "gdr_status_string",
     "gdr_last_error", "gdr_timing_enable", "gdr_timing_read", "gdr_walk_layout_chosen",
     "gdr_kda_ckpt_noalloc",
+    "gdr_conv_fwd", "gdr_conv_bwd", "gdr_conv_step", "gdr_conv_workspace_bytes", "gdr_gate_fwd", "gdr_gate_bwd",
+    "gdr_gate_workspace_bytes", "gdr_kda_step", "gdr_gdn_step", "gdr_norm_fwd", "gdr_norm_bwd", "gdr_norm_workspace_bytes",
 )
 GDR_NOALLOC_SCRATCH_BYTES = 64 << 20  # the static workspace of gdr_kda_ckpt_noalloc
 
@@ -106,6 +112,7 @@ def lib():
             L.gdr_status_string.restype = ctypes.c_char_p
             L.gdr_last_error.argtypes = []
             L.gdr_last_error.restype = ctypes.c_char_p
+            layer.declare(L)
             _lib = L
     return _lib
 
@@ -139,13 +146,15 @@ def timing_enable(on: bool = True) -> None:
 
 
 def timing_read(reset: bool = True) -> dict:
-    """{kernel name: (total ms, launches)} of the timed launches so far."""
-    names = (ctypes.c_char_p * 4)()
-    ms = (ctypes.c_double * 4)()
-    n_l = (ctypes.c_int64 * 4)()
+    """{kernel name: (total ms, launches)} of the timed launches so far: the recurrence's four
+    kernels always, the layer operators' kernels once they have been launched."""
+    room = 32
+    names = (ctypes.c_char_p * room)()
+    ms = (ctypes.c_double * room)()
+    n_l = (ctypes.c_int64 * room)()
     cnt = ctypes.c_int32()
-    _check(lib().gdr_timing_read(names, ms, n_l, 4, ctypes.byref(cnt), 1 if reset else 0))
-    return {names[i].decode(): (float(ms[i]), int(n_l[i])) for i in range(cnt.value)}
+    _check(lib().gdr_timing_read(names, ms, n_l, room, ctypes.byref(cnt), 1 if reset else 0))
+    return {names[i].decode(): (float(ms[i]), int(n_l[i])) for i in range(cnt.value) if i < 4 or n_l[i]}
 
 
 def plan_chunks(cu_seqlens):
@@ -290,3 +299,12 @@ def kda_ckpt_noalloc(prob, o, ht, dout, dht, dq, dk, dv, dg, dbeta, dh0, stream=
     """gdr_kda_ckpt on the library's static per-device workspace (no workspace argument)."""
     _check(lib().gdr_kda_ckpt_noalloc(prob.cstruct, _ptr(o), _ptr(ht), _ptr(dout), _ptr(dht), _ptr(dq), _ptr(dk),
                                       _ptr(dv), _ptr(dg), _ptr(dbeta), _ptr(dh0), _stream(stream)))
+
+
+from . import layer  # noqa: E402  (the binding of the layer operators uses the names above)
+from .layer import (  # noqa: E402,F401
+    GDR_ACT_NONE, GDR_ACT_SIGMOID, GDR_ACT_SILU, GDR_BF16, GDR_F32, GDR_GATE_SIGMOID, GDR_GATE_SOFTPLUS, GDR_RES_AFTER,
+    GDR_RES_BEFORE, GDR_RES_NONE, ConvProblem, ConvStep, GateProblem, NormProblem, Plan, StepProblem, conv_bwd, conv_fwd,
+    conv_step, conv_workspace_bytes, gate_bwd, gate_fwd, gate_workspace_bytes, gdn_step, kda_step, norm_bwd, norm_fwd,
+    norm_workspace_bytes,
+)

@@ -4,14 +4,16 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libgdr.so")
-SOURCES = ["gdr_api.cpp", "gdr_fwd.hip", "gdr_bwd.hip"]
-HEADERS = ["gdr_device.h", "gdr_kernels.h"]
+SOURCES = ["gdr_api.cpp", "gdr_fwd.hip", "gdr_bwd.hip", "gdr_layer_api.cpp", "gdr_conv.hip", "gdr_gate.hip", "gdr_step.hip",
+           "gdr_norm.hip", "gdr_psum.hip"]
+HEADERS = ["gdr_device.h", "gdr_kernels.h", "gdr_walk.h", "gdr_host.h", "gdr_layer.h", "gdr_vec.h"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -53,13 +55,16 @@ def build(verbose: bool = False) -> str:
     tmp = LIB_PATH + ".tmp%d" % os.getpid()
     cmds = commands(tmp, PKG_DIR)
     try:
-        for cmd in cmds:
-            if verbose:
-                print(" ".join(cmd), flush=True)
-            res = subprocess.run(cmd, capture_output=True, text=True)
-            if res.returncode != 0:
-                sys.stderr.write(res.stdout + res.stderr)
-                raise RuntimeError("hipcc failed building libgdr.so")
+        # the sources compile side by side, then the link
+        for group in (cmds[:-1], cmds[-1:]):
+            with ThreadPoolExecutor(max_workers=min(8, len(group))) as pool:
+                results = list(pool.map(lambda cmd: subprocess.run(cmd, capture_output=True, text=True), group))
+            for cmd, res in zip(group, results):
+                if verbose:
+                    print(" ".join(cmd), flush=True)
+                if res.returncode != 0:
+                    sys.stderr.write(res.stdout + res.stderr)
+                    raise RuntimeError("hipcc failed building libgdr.so")
         os.replace(tmp, LIB_PATH)
     finally:
         for obj in cmds[-1][4:-2]:

@@ -12,6 +12,7 @@
 #include <string>
 #include <vector>
 
+#include "gdr_host.h"
 #include "gdr_kernels.h"
 
 // Workspace of gdr_kda_ckpt_noalloc: one copy per device, held from the
@@ -270,10 +271,12 @@ struct Timing {
   };
   std::vector<Pending> pending;
   std::vector<hipEvent_t> pool;
-  double total_ms[4] = {0, 0, 0, 0};
-  int64_t launches[4] = {0, 0, 0, 0};
+  double total_ms[gdr::TK_COUNT] = {};
+  int64_t launches[gdr::TK_COUNT] = {};
 };
-const char *const kKernelNames[4] = {"fwd_prep", "fwd_walk", "bwd_walk", "bwd_grad"};
+const char *const kKernelNames[gdr::TK_COUNT] = {"fwd_prep", "fwd_walk", "bwd_walk",  "bwd_grad", "conv_fwd",
+                                                 "conv_bwd", "conv_step", "gate_fwd", "gate_bwd", "step",
+                                                 "norm_fwd", "norm_bwd", "param_sum"};
 Timing &timing() {
   static Timing t;
   return t;
@@ -415,6 +418,21 @@ int32_t ckpt_noalloc_impl(const gdr_problem *p, uint16_t *o, float *ht, const ui
 
 }  // namespace
 
+namespace gdr {
+int32_t host_status(int32_t code, const char *msg) {
+  try {
+    g_last_error = code == GDR_OK ? "" : msg;
+  } catch (...) {  // no memory for the message: the status stands without it
+  }
+  return code;
+}
+int32_t host_check_device() { return check_device_impl(); }
+int32_t host_hip(hipError_t e, const char *what) { return hip_status(e, what); }
+hipError_t host_timed(int kernel, hipStream_t st, hipError_t (*launch)(void *), void *ctx) {
+  return timed(kernel, st, [&] { return launch(ctx); });
+}
+}  // namespace gdr
+
 extern "C" {
 
 int32_t gdr_plan_chunks(const int32_t *cu, int32_t N, int32_t *table, int64_t capacity, int32_t *n_chunks_out,
@@ -537,7 +555,7 @@ int32_t gdr_timing_read(const char **names, double *total_ms, int64_t *launches,
     t.pool.push_back(pd.b);
   }
   t.pending.clear();
-  const int32_t n = std::min<int32_t>(capacity, 4);
+  const int32_t n = std::min<int32_t>(capacity, gdr::TK_COUNT);
   for (int32_t i = 0; i < n; ++i) {
     if (names) names[i] = kKernelNames[i];
     if (total_ms) total_ms[i] = t.total_ms[i];
@@ -545,7 +563,7 @@ int32_t gdr_timing_read(const char **names, double *total_ms, int64_t *launches,
   }
   if (count) *count = n;
   if (reset)
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < gdr::TK_COUNT; ++i) {
       t.total_ms[i] = 0;
       t.launches[i] = 0;
     }

@@ -1,0 +1,458 @@
+// Short causal depthwise convolution over packed documents, with bias and SiLU.
+//
+//   z[t,c] = b[c] + sum_{i<W} w[c,i] X[t-(W-1)+i, c],     y = z or z sigma(z)
+//
+// X is the document preceded by W-1 carried-in rows (s0, or zeros).  Backward,
+// with dz = dy act'(z) and dz = 0 past the document's end:
+//   dX[s] = sum_{i<W} w[c,i] dz[s+(W-1)-i] (+ dst on the last W-1 rows of X)
+//   dw[c,i] = sum_t dz[t] X[t-(W-1)+i],   db = sum_t dz[t]
+// dX before the document's first row is ds0.
+#include "gdr_layer.h"
+#include "gdr_vec.h"
+
+namespace gdr {
+namespace {
+
+struct ConvArgs {
+  const void *x, *w, *b, *s0;
+  const int32_t *table;
+  int N, NC, C;
+  int64_t xs;
+  bool silu, wbf;
+  int lx, ly, nchb;
+};
+
+// The lane's first channel; the last group of a row whose width is no multiple of
+// VEC starts early and repeats its neighbour's channels (the same values, written
+// twice), so every access is whole.
+template <int VEC>
+__device__ __forceinline__ int first_channel(int group, int C) {
+  return VEC == 1 ? group : min(group * VEC, C - VEC);
+}
+
+template <int VEC, int W>
+__device__ __forceinline__ void load_taps(const ConvArgs &a, int c, float (&w)[W][VEC], float (&b)[VEC]) {
+  if constexpr (VEC == 1) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i][0] = ld_param(a.w, (int64_t)c * W + i, a.wbf);
+    b[0] = a.b ? ld_param(a.b, c, a.wbf) : 0.f;
+  } else {
+    if (a.wbf) {
+      Raw<u16, VEC * W> r;
+      r.load(static_cast<const u16 *>(a.w) + (int64_t)c * W);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i][e] = r.get(e * W + i);
+    } else {
+      Raw<float, VEC * W> r;
+      r.load(static_cast<const float *>(a.w) + (int64_t)c * W);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i][e] = r.get(e * W + i);
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) b[e] = a.b ? ld_param(a.b, c + e, a.wbf) : 0.f;
+  }
+}
+
+// Row `pos` (-(W-1) <= pos < 0) of the carried-in rows of document `doc`.
+template <class T, int VEC>
+__device__ __forceinline__ void load_carried(const ConvArgs &a, int W, int doc, int pos, int c, Raw<T, VEC> &r) {
+  if (a.s0) r.load(static_cast<const T *>(a.s0) + ((int64_t)doc * (W - 1) + (W - 1) + pos) * a.C + c);
+  else r.zero();
+}
+
+// First token and token count of a document, from its chunks.
+__device__ __forceinline__ void doc_span(const ChunkTable &tb, int doc, int &start, int &len) {
+  const int c0 = tb.doc_ptr[doc], c1 = tb.doc_ptr[doc + 1];
+  start = c0 < c1 ? tb.start[c0] : 0;
+  len = c0 < c1 ? tb.start[c1 - 1] + tb.len[c1 - 1] - start : 0;
+}
+
+// The taps' products: z for one row, `win` holding the W-1 rows before it.
+template <int VEC, int W>
+__device__ __forceinline__ void taps(const float (&w)[W][VEC], const float (&b)[VEC], const float (&win)[W - 1][VEC],
+                                     const float (&x)[VEC], float (&z)[VEC]) {
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    float s = b[e];
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) s = fmaf(w[i][e], win[i][e], s);
+    z[e] = fmaf(w[W - 1][e], x[e], s);
+  }
+}
+template <int VEC, int D>
+__device__ __forceinline__ void push(float (&win)[D][VEC], const float (&x)[VEC]) {
+#pragma unroll
+  for (int i = 0; i + 1 < D; ++i)
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) win[i][e] = win[i + 1][e];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) win[D - 1][e] = x[e];
+}
+
+// Forward: a thread takes R consecutive tokens of one chunk.  Blocks past the
+// `nrb` row blocks write the final rows st instead, LY documents each.
+template <class T, int VEC, int W, int R>
+__global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int nrb, T *__restrict__ y, int64_t ys,
+                                                       T *__restrict__ st) {
+  const int tx = threadIdx.x % a.lx, ty = threadIdx.x / a.lx;
+  const int chb = blockIdx.x % a.nchb, rb = blockIdx.x / a.nchb;
+  const int group = chb * a.lx + tx;
+  if (ty >= a.ly || group >= (a.C + VEC - 1) / VEC) return;
+  const int c = first_channel<VEC>(group, a.C);
+  const ChunkTable tb(a.table, a.NC, a.N);
+  const T *__restrict__ x = static_cast<const T *>(a.x);
+
+  if (rb >= nrb) {
+    const int doc = (rb - nrb) * a.ly + ty;
+    if (doc >= a.N) return;
+    int start, len;
+    doc_span(tb, doc, start, len);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+      const int pos = len - (W - 1) + j;
+      Raw<T, VEC> r;
+      if (pos >= 0) r.load(x + (int64_t)(start + pos) * a.xs + c);
+      else load_carried<T, VEC>(a, W, doc, pos, c, r);
+      r.store(st + ((int64_t)doc * (W - 1) + j) * a.C + c);
+    }
+    return;
+  }
+
+  constexpr int RUNS = 64 / R;
+  const int run = rb * a.ly + ty, chunk = run / RUNS, sub = run % RUNS;
+  if (chunk >= a.NC) return;
+  const int len = min(R, tb.len[chunk] - sub * R);
+  if (len <= 0) return;
+  const int start = tb.start[chunk] + sub * R, doc = tb.doc[chunk];
+  const int pos = (chunk - tb.doc_ptr[doc]) * 64 + sub * R;  // of the run's first token in its document
+
+  Raw<T, VEC> in[R], hist[W - 1];
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) {
+    const int p = pos - (W - 1) + j;
+    if (p >= 0) hist[j].load(x + (int64_t)(start - (W - 1) + j) * a.xs + c);
+    else load_carried<T, VEC>(a, W, doc, p, c, hist[j]);
+  }
+#pragma unroll
+  for (int t = 0; t < R; ++t) in[t].load(x + (int64_t)(start + min(t, len - 1)) * a.xs + c);
+
+  float w[W][VEC], b[VEC], win[W - 1][VEC];
+  load_taps<VEC, W>(a, c, w, b);
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) win[j][e] = hist[j].get(e);
+#pragma unroll
+  for (int t = 0; t < R; ++t) {
+    float xv[VEC], z[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) xv[e] = in[t].get(e);
+    taps<VEC, W>(w, b, win, xv, z);
+    if (a.silu) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) z[e] *= sigmoid<sizeof(T) == 4>(z[e]);
+    }
+    Raw<T, VEC> out;
+    out.set(z);
+    if (t < len) out.store(y + (int64_t)(start + t) * ys + c);
+    push<VEC, W - 1>(win, xv);
+  }
+}
+
+// dz = dy act'(z).
+template <bool EXACT>
+__device__ __forceinline__ float act_grad(float dy, float z, bool silu) {
+  if (!silu) return dy;
+  const float s = sigmoid<EXACT>(z);
+  return dy * (s * fmaf(z, 1.f - s, 1.f));
+}
+
+// Backward: a worker walks its share of the chunks, keeping the last W-1 rows of
+// x and dz in registers; z is formed again from x.  It reads W-1 rows past each
+// chunk's end, whose dz reach back into the chunk.  The parameter terms stay in
+// registers over all the worker's chunks and leave as one partial row per block.  Blocks
+// past the `nwb` worker blocks form ds0, LY documents each.
+template <class T, int VEC, int W>
+__global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int nwb, int workers, const T *__restrict__ dy, int64_t ds,
+                                                       const T *__restrict__ dst, T *__restrict__ dx, int64_t xs_out,
+                                                       T *__restrict__ ds0, float *__restrict__ partial) {
+  constexpr bool EXACT = sizeof(T) == 4;
+  constexpr int B = 8;  // tokens per batch of loads
+  const int tx = threadIdx.x % a.lx, ty = threadIdx.x / a.lx;
+  const int chb = blockIdx.x % a.nchb, wb = blockIdx.x / a.nchb;
+  const int group = chb * a.lx + tx, groups = (a.C + VEC - 1) / VEC;
+  const bool live = ty < a.ly && group < groups;
+  const int c = first_channel<VEC>(min(group, groups - 1), a.C);
+  const ChunkTable tb(a.table, a.NC, a.N);
+  const T *__restrict__ x = static_cast<const T *>(a.x);
+  float w[W][VEC], b[VEC];
+  load_taps<VEC, W>(a, c, w, b);
+
+  if (wb >= nwb) {
+    const int doc = (wb - nwb) * a.ly + ty;
+    if (!live || doc >= a.N) return;
+    int start, len;
+    doc_span(tb, doc, start, len);
+    float win[W - 1][VEC], acc[W - 1][VEC];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+      Raw<T, VEC> r;
+      load_carried<T, VEC>(a, W, doc, j - (W - 1), c, r);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) win[j][e] = r.get(e), acc[j][e] = 0.f;
+      if (dst && j - len >= 0) {  // a document shorter than the history hands it on
+        Raw<T, VEC> d;
+        d.load(dst + ((int64_t)doc * (W - 1) + j - len) * a.C + c);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[j][e] = d.get(e);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < W - 1; ++t) {
+      if (t >= len) break;
+      Raw<T, VEC> rx, rd;
+      rx.load(x + (int64_t)(start + t) * a.xs + c);
+      rd.load(dy + (int64_t)(start + t) * ds + c);
+      float xv[VEC], z[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) xv[e] = rx.get(e);
+      taps<VEC, W>(w, b, win, xv, z);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float dz = act_grad<EXACT>(rd.get(e), z[e], a.silu);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+          if (j >= t) acc[j][e] = fmaf(w[j - t < 0 ? 0 : j - t][e], dz, acc[j][e]);
+      }
+      push<VEC, W - 1>(win, xv);
+    }
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+      Raw<T, VEC> r;
+      r.set(acc[j]);
+      r.store(ds0 + ((int64_t)doc * (W - 1) + j) * a.C + c);
+    }
+    return;
+  }
+
+  const int worker = wb * a.ly + ty;
+  const int first = (int)((int64_t)a.NC * worker / workers);
+  const int last = live ? (int)((int64_t)a.NC * (worker + 1) / workers) : first;
+  float dw[W][VEC], db[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    db[e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) dw[i][e] = 0.f;
+  }
+  for (int chunk = first; chunk < last; ++chunk) {
+    const int start = tb.start[chunk], len = tb.len[chunk], doc = tb.doc[chunk];
+    const int pos = (chunk - tb.doc_ptr[doc]) * 64;
+    // the document's last chunk ends it; others are followed by at least one row
+    const int lastc = tb.doc_ptr[doc + 1] - 1;
+    const int end = chunk == lastc ? len : len + min(W - 1, tb.len[chunk + 1]);
+    // dz rows that reach into this chunk: [0, end) exist, zeros up to len + W - 1
+    const int dlen = (lastc - chunk) * 64 + tb.len[lastc];  // tokens of the document from `start` on
+    float win[W - 1][VEC], dzw[W - 1][VEC];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+      const int p = pos - (W - 1) + j;
+      Raw<T, VEC> r;
+      if (p >= 0) r.load(x + (int64_t)(start - (W - 1) + j) * a.xs + c);
+      else load_carried<T, VEC>(a, W, doc, p, c, r);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) win[j][e] = r.get(e), dzw[j][e] = 0.f;
+    }
+    for (int t0 = 0; t0 < len + W - 1; t0 += B) {
+      Raw<T, VEC> rx[B], rd[B];
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        const int64_t row = start + min(t0 + i, end - 1);
+        rx[i].load(x + row * a.xs + c);
+        rd[i].load(dy + row * ds + c);
+      }
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        const int t = t0 + i;
+        float xv[VEC], z[VEC], dz[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) xv[e] = rx[i].get(e);
+        taps<VEC, W>(w, b, win, xv, z);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) dz[e] = t < end ? act_grad<EXACT>(rd[i].get(e), z[e], a.silu) : 0.f;
+        if (t < len) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            db[e] += dz[e];
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) dw[j][e] = fmaf(dz[e], win[j][e], dw[j][e]);
+            dw[W - 1][e] = fmaf(dz[e], xv[e], dw[W - 1][e]);
+          }
+        }
+        const int s = t - (W - 1);  // dX[s]: dz[s .. s + W - 1] are dzw and dz
+        if (s >= 0 && s < len) {
+          float g[VEC];
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            g[e] = w[0][e] * dz[e];
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) g[e] = fmaf(w[W - 1 - j][e], dzw[j][e], g[e]);
+          }
+          const int q = s - (dlen - (W - 1));
+          if (dst && q >= 0) {
+            Raw<T, VEC> d;
+            d.load(dst + ((int64_t)doc * (W - 1) + q) * a.C + c);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) g[e] += d.get(e);
+          }
+          Raw<T, VEC> out;
+          out.set(g);
+          out.store(dx + (int64_t)(start + s) * xs_out + c);
+        }
+        push<VEC, W - 1>(win, xv);
+        push<VEC, W - 1>(dzw, dz);
+      }
+    }
+  }
+  __shared__ float sums[256 * VEC];
+  float *p = partial + (int64_t)wb * (W + 1) * a.C + c;
+#pragma unroll
+  for (int i = 0; i < W; ++i) block_partial<VEC>(dw[i], sums, tx, ty, a.lx, a.ly, live, p + (int64_t)i * a.C);
+  block_partial<VEC>(db, sums, tx, ty, a.lx, a.ly, live, p + (int64_t)W * a.C);
+}
+
+// One token per sequence: the W-1 rows of the sequence's slot and the new row give
+// y; the slot keeps the last W-1 rows.  Rows whose slot lies outside the pool are
+// left alone.
+template <class T, int VEC, int W>
+__global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a, T *__restrict__ y, int64_t ys, T *state,
+                                                        const int32_t *__restrict__ slots, int n_slots) {
+  const int tx = threadIdx.x % a.lx, ty = threadIdx.x / a.lx;
+  const int chb = blockIdx.x % a.nchb, rb = blockIdx.x / a.nchb;
+  const int group = chb * a.lx + tx, row = rb * a.ly + ty;
+  if (ty >= a.ly || group >= a.C / VEC || row >= a.N) return;
+  const int slot = slots ? slots[row] : row;
+  if (slot < 0 || slot >= n_slots) return;
+  const int c = group * VEC;
+  T *s = state + (int64_t)slot * (W - 1) * a.C + c;
+  Raw<T, VEC> in, hist[W - 1];
+  in.load(static_cast<const T *>(a.x) + (int64_t)row * a.xs + c);
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) hist[j].load(s + (int64_t)j * a.C);
+  float w[W][VEC], b[VEC], win[W - 1][VEC], xv[VEC], z[VEC];
+  load_taps<VEC, W>(a, c, w, b);
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    xv[e] = in.get(e);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) win[j][e] = hist[j].get(e);
+  }
+  taps<VEC, W>(w, b, win, xv, z);
+  if (a.silu) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) z[e] *= sigmoid<sizeof(T) == 4>(z[e]);
+  }
+  Raw<T, VEC> out;
+  out.set(z);
+  out.store(y + (int64_t)row * ys + c);
+#pragma unroll
+  for (int j = 0; j + 1 < W - 1; ++j) hist[j + 1].store(s + (int64_t)j * a.C);
+  in.store(s + (int64_t)(W - 2) * a.C);
+}
+
+ConvArgs args_of(const gdr_conv &p, const Lanes &l) {
+  ConvArgs a{};
+  a.x = p.x; a.w = p.weight; a.b = p.bias; a.s0 = p.s0;
+  a.table = p.chunk_table;
+  a.N = p.N; a.NC = p.n_chunks; a.C = p.C;
+  a.xs = p.x_stride;
+  a.silu = p.activation == GDR_ACT_SILU;
+  a.wbf = p.w_dtype == GDR_BF16;
+  a.lx = l.lx; a.ly = l.ly; a.nchb = l.nchb;
+  return a;
+}
+
+// Calls f(type tag, VEC, W) with the compile-time values of the problem.
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
+template <class T, int VEC, class F>
+hipError_t with_width(int W, F f) {
+  switch (W) {
+    case 2: return f(T(), Int<VEC>(), Int<2>());
+    case 3: return f(T(), Int<VEC>(), Int<3>());
+    case 4: return f(T(), Int<VEC>(), Int<4>());
+    case 5: return f(T(), Int<VEC>(), Int<5>());
+    case 6: return f(T(), Int<VEC>(), Int<6>());
+    case 7: return f(T(), Int<VEC>(), Int<7>());
+    case 8: return f(T(), Int<VEC>(), Int<8>());
+    default: return hipErrorInvalidValue;
+  }
+}
+template <int BYTES, class F>
+hipError_t with_types(const gdr_conv &p, int vec, F f) {
+  if (p.dtype == GDR_BF16)
+    return vec == 1 ? with_width<u16, 1>(p.W, f) : with_width<u16, BYTES / 2>(p.W, f);
+  return vec == 1 ? with_width<float, 1>(p.W, f) : with_width<float, BYTES / 4>(p.W, f);
+}
+
+constexpr int FWD_RUN = 16;  // tokens per thread of the forward
+
+}  // namespace
+
+hipError_t launch_conv_fwd(const gdr_conv &p, void *y, int64_t y_stride, void *st, hipStream_t stream) {
+  const int vec = vec_of(p.C, p.dtype);
+  const Lanes l = lanes_for(groups_of(p.C, vec));
+  const ConvArgs a = args_of(p, l);
+  const int64_t runs = (int64_t)p.n_chunks * (64 / FWD_RUN), nrb = (runs + l.ly - 1) / l.ly;
+  const int64_t blocks = (nrb + (st ? (p.N + l.ly - 1) / l.ly : 0)) * l.nchb;
+  if (blocks == 0) return hipSuccess;
+  if (blocks >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+  return with_types<16>(p, vec, [&](auto t, auto v, auto w) {
+    using T = decltype(t);
+    conv_fwd_kernel<T, decltype(v)::value, decltype(w)::value, FWD_RUN><<<(unsigned)blocks, l.threads, 0, stream>>>(
+        a, (int)nrb, static_cast<T *>(y), y_stride, static_cast<T *>(st));
+    return hipGetLastError();
+  });
+}
+
+hipError_t launch_conv_bwd(const gdr_conv &p, const void *dy, int64_t dy_stride, const void *dst, void *dx,
+                           int64_t dx_stride, void *ds0, float *partial, int workers, hipStream_t stream) {
+  const int vec = vec_of(p.C, p.dtype, CONV_BWD_BYTES);
+  const Lanes l = lanes_for(groups_of(p.C, vec));
+  const ConvArgs a = args_of(p, l);
+  const int nwb = workers / l.ly;  // a multiple
+  const int64_t blocks = ((int64_t)nwb + (ds0 ? (p.N + l.ly - 1) / l.ly : 0)) * l.nchb;
+  if (blocks == 0) return hipSuccess;
+  if (blocks >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+  return with_types<CONV_BWD_BYTES>(p, vec, [&](auto t, auto v, auto w) {
+    using T = decltype(t);
+    conv_bwd_kernel<T, decltype(v)::value, decltype(w)::value><<<(unsigned)blocks, l.threads, 0, stream>>>(
+        a, nwb, workers, static_cast<const T *>(dy), dy_stride, static_cast<const T *>(dst), static_cast<T *>(dx), dx_stride,
+        static_cast<T *>(ds0), partial);
+    return hipGetLastError();
+  });
+}
+
+hipError_t launch_conv_step(const gdr_conv &p, void *y, int64_t y_stride, void *state, const int32_t *slots,
+                            int32_t n_slots, hipStream_t stream) {
+  const int full = vec_of(p.C, p.dtype), vec = p.C % full == 0 ? full : 1;
+  const Lanes l = lanes_for(p.C / vec);
+  ConvArgs a = args_of(p, l);
+  const int64_t blocks = (int64_t)l.nchb * ((p.N + l.ly - 1) / l.ly);
+  if (blocks == 0) return hipSuccess;
+  if (blocks >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+  return with_types<16>(p, vec, [&](auto t, auto v, auto w) {
+    using T = decltype(t);
+    conv_step_kernel<T, decltype(v)::value, decltype(w)::value><<<(unsigned)blocks, l.threads, 0, stream>>>(
+        a, static_cast<T *>(y), y_stride, static_cast<T *>(state), slots, n_slots);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace gdr

@@ -1,0 +1,78 @@
+// Private interface between the C-ABI layer (gdr_layer_api.cpp) and the kernels
+// around the recurrence: the short convolution, the decay gate, the
+// single-token recurrence and the norm with gate and residual.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "gdr.h"
+
+namespace gdr {
+
+// Lane map of the kernels whose rows are C channels wide: a thread owns one group
+// of `vec` neighbouring channels, LX threads span LX groups, LY sets of LX threads
+// take LY different rows (or runs of rows), nchb blocks span all groups.  LX is
+// not rounded to a power of two, so narrow and odd rows leave few lanes idle.
+struct Lanes {
+  int lx, ly, nchb, threads;
+};
+inline Lanes lanes_for(int groups) {
+  Lanes l;
+  l.nchb = (groups + 255) / 256;
+  l.lx = (groups + l.nchb - 1) / l.nchb;
+  l.ly = std::max(1, 256 / l.lx);
+  l.threads = (l.lx * l.ly + 63) / 64 * 64;
+  return l;
+}
+// Channels per thread: 16 bytes of a row, or single channels for rows narrower than that.
+inline int vec_of(int channels, int dtype, int bytes = 16) {
+  const int v = bytes / (dtype == GDR_BF16 ? 2 : 4);
+  return channels >= v ? v : 1;
+}
+inline int groups_of(int channels, int vec) { return (channels + vec - 1) / vec; }
+
+// Row workers of the parameter-gradient sums: each set of LX threads adds its rows'
+// terms in registers, a block adds its LY sets and leaves one partial row, and a
+// second kernel adds the blocks' partials in a fixed order, so the sums do not
+// depend on scheduling.  `target` threads fill the chip.  A multiple of LY.
+inline int workers_for(int64_t rows, const Lanes &l, int64_t target) {
+  const int64_t n = std::max<int64_t>(1, target / ((int64_t)l.nchb * l.lx));
+  const int64_t w = std::min<int64_t>(std::max<int64_t>(rows, 0), n);
+  return (int)((w + l.ly - 1) / l.ly * l.ly);
+}
+
+constexpr int CONV_BWD_BYTES = 16;  // bytes of a row per thread in the convolution's backward
+inline Lanes conv_bwd_lanes(int C, int dtype) { return lanes_for(groups_of(C, vec_of(C, dtype, CONV_BWD_BYTES))); }
+inline int conv_workers(int n_chunks, int C, int dtype) { return workers_for(n_chunks, conv_bwd_lanes(C, dtype), 131072); }
+inline Lanes gate_lanes(int C, int dtype) { return lanes_for(groups_of(C, vec_of(C, dtype))); }
+inline int gate_workers(int64_t T, int C, int dtype) { return workers_for((T + 7) / 8, gate_lanes(C, dtype), 262144); }
+// norm: a worker is a block (see gdr_norm.hip)
+inline int norm_workers(int64_t rows, int D) {
+  return (int)std::min<int64_t>(std::max<int64_t>(rows * D / 4096, rows > 0), 1024);
+}
+
+hipError_t launch_conv_fwd(const gdr_conv &p, void *y, int64_t y_stride, void *st, hipStream_t stream);
+hipError_t launch_conv_bwd(const gdr_conv &p, const void *dy, int64_t dy_stride, const void *dst, void *dx,
+                           int64_t dx_stride, void *ds0, float *partial, int workers, hipStream_t stream);
+hipError_t launch_conv_step(const gdr_conv &p, void *y, int64_t y_stride, void *state, const int32_t *slots,
+                            int32_t n_slots, hipStream_t stream);
+hipError_t launch_gate_fwd(const gdr_gate &p, float *g, hipStream_t stream);
+hipError_t launch_gate_bwd(const gdr_gate &p, const float *dg, void *dx, int64_t dx_stride, float *partial, int workers,
+                           hipStream_t stream);
+hipError_t launch_step(bool gdn, const gdr_step &p, uint16_t *o, hipStream_t stream);
+hipError_t launch_norm_fwd(const gdr_norm &p, void *y, hipStream_t stream);
+hipError_t launch_norm_bwd(const gdr_norm &p, const void *dy, const void *ds, void *dx, int64_t dx_stride, void *dgate,
+                           int64_t dgate_stride, void *dres, float *partial, int workers, hipStream_t stream);
+
+// Sums of `rows` partial rows, in a fixed order.  conv: partial [rows][W + 1][C] ->
+// dw [C][W], dbias [C].  gate: partial [rows][2][H D] -> dbias [H D] and da [H] (the
+// second row summed over each head's D channels; D is 1 or 128).  norm: partial
+// [rows][D] -> dw.  A NULL output is skipped.
+hipError_t launch_conv_sum(const float *partial, int rows, int C, int W, float *dw, float *dbias, hipStream_t stream);
+hipError_t launch_gate_sum(const float *partial, int rows, int H, int D, float *da, float *dbias, hipStream_t stream);
+hipError_t launch_norm_sum(const float *partial, int rows, int D, float *dw, hipStream_t stream);
+
+}  // namespace gdr

@@ -251,6 +251,157 @@ int32_t gdr_kda_ckpt_noalloc(const gdr_problem *p, uint16_t *o, float *ht, const
                              const float *dht, uint16_t *dq, uint16_t *dk, uint16_t *dv, float *dg,
                              void *dbeta, float *dh0, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * The operators around the recurrence in a gated delta-rule layer: the short
+ * causal convolution that makes q, k and v, the decay gate that makes g, the
+ * recurrence for single tokens, and the norm with gate and residual.  PR #8638
+ * and PR #8218 name the convolution, the gate activation and inference kernels as
+ * parts of the training and serving path; they print no formula, so the usual
+ * definitions below are taken.
+ *
+ * The conventions above hold: caller-owned device memory, host-side checks before
+ * anything is enqueued, no allocation and no synchronisation, outputs that do not
+ * alias inputs or the workspace (the pools that a call updates in place excepted).
+ * Here rows may also be strided: an `*_stride` is the distance between the rows of
+ * two tokens in elements, at least the row's width (so a call can read and write
+ * parts of a wider projection buffer); tensors without one are contiguous.  Rows
+ * need no alignment beyond their element's.  Values are held, summed and rounded
+ * in fp32; an output is rounded once.
+ * ------------------------------------------------------------------------- */
+enum gdr_dtype { GDR_BF16 = 0, GDR_F32 = 1 };
+enum gdr_activation { GDR_ACT_NONE = 0, GDR_ACT_SILU = 1, GDR_ACT_SIGMOID = 2 };
+
+/* Short causal depthwise convolution over packed documents:
+ *     z[t,c] = bias[c] + sum_{i<W} weight[c,i] X[t-(W-1)+i, c],   y = z or z * sigmoid(z)
+ * where X is the document's rows preceded by the W-1 rows s0 (zeros when NULL),
+ * the oldest first.  2 <= W <= 8. */
+typedef struct gdr_conv {
+  int32_t T;          /* tokens (rows of x), >= 0 */
+  int32_t N;          /* documents; the single-token call: sequences, N == T */
+  int32_t C;          /* channels, >= 1 */
+  int32_t W;          /* taps */
+  int32_t dtype;      /* gdr_dtype of x, y, s0, st and their gradients */
+  int32_t w_dtype;    /* gdr_dtype of weight and bias */
+  int32_t activation; /* GDR_ACT_NONE or GDR_ACT_SILU */
+  int32_t n_chunks;   /* of chunk_table */
+  int64_t x_stride;
+  const void *x;      /* [T, C] */
+  const void *weight; /* [C, W] */
+  const void *bias;   /* [C], or NULL for zeros */
+  const void *s0;     /* [N, W-1, C] rows before each document, or NULL for zeros */
+  const int32_t *chunk_table; /* device copy of the gdr_plan_chunks table (not read by the single-token call) */
+} gdr_conv;
+
+/* Forward.  y: [T, C].  st: [N, W-1, C], the last W-1 rows of each document with
+ * its carried-in rows before it (an empty document hands s0 on), or NULL to skip. */
+int32_t gdr_conv_fwd(const gdr_conv *p, void *y, int64_t y_stride, void *st, void *stream);
+
+/* Workspace bytes of the backward, or minus a gdr_status. */
+int64_t gdr_conv_workspace_bytes(int32_t n_chunks, int32_t C, int32_t W, int32_t dtype);
+
+/* Backward: gradients of sum(y * dy) + sum(st * dst).  dy: [T, C]; dst: [N, W-1, C]
+ * or NULL (= zeros).  Writes dx [T, C]; dweight fp32 [C, W]; dbias fp32 [C] and ds0
+ * [N, W-1, C] (each NULL to skip; ds0 is the gradient with respect to s0, also
+ * when s0 is NULL).  Recomputes z from x; keeps nothing from the forward. */
+int32_t gdr_conv_bwd(const gdr_conv *p, const void *dy, int64_t dy_stride, const void *dst, void *dx, int64_t dx_stride,
+                     float *dweight, float *dbias, void *ds0, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* One token for each of N sequences.  state: [n_slots, W-1, C], the last rows of
+ * every sequence in the pool, updated in place; slots: device int32 [N], the slot
+ * of each row of x, or NULL for slot n.  Rows whose slot lies outside
+ * [0, n_slots) (padding) are skipped: their y is left as it was.  The slots of the
+ * other rows are distinct; two rows of one slot race. */
+int32_t gdr_conv_step(const gdr_conv *p, void *y, int64_t y_stride, void *state, const int32_t *slots, int32_t n_slots,
+                      void *stream);
+
+/* The log-decay g of the recurrence from its raw projection x:
+ *     u = x + bias,   A = exp(a_log)
+ *     GDR_GATE_SOFTPLUS:  g = max(floor, -A softplus(u))
+ *     GDR_GATE_SIGMOID:   g = floor * sigmoid(A u)
+ * with a_log one value per head and bias one per channel.  floor in [-8, 0): both
+ * kinds then meet the recurrence's precondition on g.  D is 128 for KDA's g and 1
+ * for GDN's. */
+enum gdr_gate_kind { GDR_GATE_SOFTPLUS = 0, GDR_GATE_SIGMOID = 1 };
+typedef struct gdr_gate {
+  int32_t T, H, D;
+  int32_t dtype;      /* gdr_dtype of x and dx */
+  int32_t kind;       /* gdr_gate_kind */
+  float floor;
+  int64_t x_stride;
+  const void *x;      /* [T, H, D] */
+  const float *a_log; /* [H] */
+  const float *bias;  /* [H, D], or NULL for zeros */
+} gdr_gate;
+
+/* g: fp32 [T, H, D]. */
+int32_t gdr_gate_fwd(const gdr_gate *p, float *g, void *stream);
+int64_t gdr_gate_workspace_bytes(int32_t T, int32_t H, int32_t D, int32_t dtype);
+/* dg: fp32 [T, H, D].  Writes dx [T, H, D], da_log fp32 [H], dbias fp32 [H, D]
+ * (NULL to skip).  Where the floor holds g, the gradients are zero. */
+int32_t gdr_gate_bwd(const gdr_gate *p, const float *dg, void *dx, int64_t dx_stride, float *da_log, float *dbias,
+                     void *workspace, int64_t workspace_bytes, void *stream);
+
+/* The recurrence for single tokens and short runs of them (serving), token by
+ * token, on a pool of states that is updated in place.  Sequence n takes tokens
+ * cu_seqlens[n] .. cu_seqlens[n+1] - 1 in order, or token n when cu_seqlens is NULL
+ * (then N == T), from and to the state of slot slots[n] (slot n when NULL).  ht of
+ * the forward is such a state.  Sequences without tokens and sequences whose slot
+ * lies outside [0, n_slots) are skipped: their state and o are left as they were,
+ * and so are rows of o that no sequence covers.  The slots of the other sequences
+ * are distinct; two sequences of one slot race.  cu_seqlens is clipped to [0, T]. */
+typedef struct gdr_step {
+  int32_t T, N, H_qk, H_v, K, V; /* as gdr_problem; KDA: H_qk == H_v */
+  int32_t n_slots;
+  uint32_t input_flags;      /* GDR_IN_* as in gdr_problem */
+  float scale;
+  int64_t q_stride, k_stride, v_stride;
+  const uint16_t *q, *k;     /* bf16 [T, H_qk, K] */
+  const uint16_t *v;         /* bf16 [T, H_v, V] */
+  const float *g;            /* KDA: fp32 [T, H_v, K]; GDN: fp32 [T, H_v] */
+  const void *beta;          /* KDA: bf16 [T, H_v]; GDN: fp32 [T, H_v] */
+  const int32_t *cu_seqlens; /* device int32 [N+1], or NULL */
+  const int32_t *slots;      /* device int32 [N], or NULL */
+  float *state;              /* fp32 [n_slots, H_v, K, V], 16-byte aligned */
+} gdr_step;
+
+/* o: bf16 [T, H_v, V]. */
+int32_t gdr_kda_step(const gdr_step *p, uint16_t *o, void *stream);
+int32_t gdr_gdn_step(const gdr_step *p, uint16_t *o, void *stream);
+
+/* RMS norm before or after a block, with the block's gate and the residual stream:
+ *     n(u) = u / sqrt(mean(u^2) + eps) * weight * act(gate)
+ *     GDR_RES_NONE:    y = n(x)                 (the head norm: D = 128, H heads)
+ *     GDR_RES_BEFORE:  s = residual + scale * x,   y = n(s)
+ *     GDR_RES_AFTER:   y = residual + scale * n(x)
+ * over rows of D values, 1 <= D <= 16384; weight [D] is shared by all rows. */
+enum gdr_residual { GDR_RES_NONE = 0, GDR_RES_BEFORE = 1, GDR_RES_AFTER = 2 };
+typedef struct gdr_norm {
+  int32_t T, H, D;
+  int32_t dtype;      /* gdr_dtype of x, gate, y and their gradients */
+  int32_t res_dtype;  /* gdr_dtype of residual, s, ds and dres, and of y and dy with GDR_RES_AFTER.  fp32, or dtype */
+  int32_t w_dtype;    /* gdr_dtype of weight */
+  int32_t activation; /* GDR_ACT_SILU or GDR_ACT_SIGMOID with a gate, GDR_ACT_NONE without */
+  int32_t placement;  /* gdr_residual */
+  float scale, eps;   /* eps >= 0 */
+  int64_t x_stride, gate_stride;
+  const void *x;        /* [T, H, D]; not read by the backward of GDR_RES_BEFORE (may be NULL there) */
+  const void *weight;   /* [D], or NULL for ones */
+  const void *gate;     /* [T, H, D], or NULL for no gate */
+  const void *residual; /* [T, H, D] with a residual (not read by the backward) */
+  void *s;              /* [T, H, D], GDR_RES_BEFORE: written by the forward, read by the backward */
+} gdr_norm;
+
+/* y: [T, H, D]. */
+int32_t gdr_norm_fwd(const gdr_norm *p, void *y, void *stream);
+int64_t gdr_norm_workspace_bytes(int32_t T, int32_t H, int32_t D);
+/* Backward: gradients of sum(y * dy) + sum(s * ds).  dy: [T, H, D]; ds: [T, H, D]
+ * or NULL (= zeros), GDR_RES_BEFORE only.  Writes dx [T, H, D] (GDR_RES_BEFORE: NULL
+ * to skip), dgate [T, H, D] (with a gate), dres [T, H, D] (GDR_RES_BEFORE; with
+ * GDR_RES_AFTER the residual's gradient is dy itself), dweight fp32 [D] (NULL to skip). */
+int32_t gdr_norm_bwd(const gdr_norm *p, const void *dy, const void *ds, void *dx, int64_t dx_stride, void *dgate,
+                     int64_t dgate_stride, void *dres, float *dweight, void *workspace, int64_t workspace_bytes,
+                     void *stream);
+
 /* Kernel timing (diagnostics).  gdr_timing_enable(1) makes every later call
  * bracket each of its kernel launches with a pair of hipEvents recorded on the
  * call's stream (the events are created on first use and reused; this is the
@@ -258,7 +409,9 @@ int32_t gdr_kda_ckpt_noalloc(const gdr_problem *p, uint16_t *o, float *ht, const
  * waits for the recorded events, adds their elapsed times to per-kernel
  * totals, writes up to `capacity` entries (kernel name, total milliseconds,
  * number of launches) and, with reset != 0, clears the totals.  Kernel names:
- * "fwd_prep", "fwd_walk", "bwd_walk", "bwd_grad".  Not thread-safe with
+ * "fwd_prep", "fwd_walk", "bwd_walk", "bwd_grad", then "conv_fwd", "conv_bwd",
+ * "conv_step", "gate_fwd", "gate_bwd", "step", "norm_fwd", "norm_bwd" and
+ * "param_sum" (the sums of the parameter gradients' partials).  Not thread-safe with
  * respect to concurrent calls that are being timed. */
 int32_t gdr_timing_enable(int32_t on);
 int32_t gdr_timing_read(const char **names, double *total_ms, int64_t *launches, int32_t capacity,

@@ -1,0 +1,604 @@
+"""GPU tests of the operators around the recurrence (convolution, gate, single-token
+recurrence, norm) against fp64 references with derived bounds (layer_ref.py)."""
+import numpy as np
+import pytest
+import torch
+
+import layer_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+DT = {"bf16": BF, "f32": F32}
+
+
+def gdr():
+    import chunked_gated_delta_14_amd as m
+
+    return m
+
+
+def rng(seed):
+    return np.random.default_rng(seed)
+
+
+def dev(a, dtype=F32, pad=0):
+    """The array on the GPU, rounded to dtype; with pad, as rows of a wider buffer filled with NaN."""
+    t = torch.from_numpy(np.ascontiguousarray(a)).to(dtype).cuda()
+    if not pad:
+        return t
+    rows = t.reshape(t.shape[0], -1)
+    wide = torch.full((rows.shape[0], rows.shape[1] + pad), float("nan"), dtype=dtype, device="cuda")
+    wide[:, :rows.shape[1]] = rows
+    v = wide[:, :rows.shape[1]]
+    return v if t.dim() == 2 else v.unflatten(1, tuple(t.shape[1:]))
+
+
+def f64(t):
+    return None if t is None else t.detach().double().cpu().numpy()
+
+
+def nan(shape, dtype, pad=0):
+    shape = tuple(shape)
+    inner = int(np.prod(shape[1:])) if len(shape) > 1 else 1
+    if not pad:
+        return torch.full(shape, float("nan"), dtype=dtype, device="cuda")
+    wide = torch.full((shape[0], inner + pad), float("nan"), dtype=dtype, device="cuda")
+    v = wide[:, :inner]
+    return v if len(shape) == 2 else v.unflatten(1, shape[1:])
+
+
+def padding_untouched(t, width):
+    """The pad columns of a strided output still hold NaN."""
+    base = t._base if t._base is not None else t
+    while base._base is not None:
+        base = base._base
+    if base.shape[1] > width:
+        assert bool(torch.isnan(base[:, width:].float()).all()), "columns beside the rows were written"
+
+
+# ---- convolution ----
+
+CONV = [
+    # docs, C, W, dtype, w dtype, silu, bias, s0, pad
+    ((1,), 1, 2, "bf16", "bf16", True, True, True, 0),
+    ((1, 0, 2, 3, 1), 8, 4, "bf16", "bf16", True, True, True, 0),
+    ((200, 312), 128, 4, "bf16", "bf16", True, False, False, 0),
+    ((1, 63, 64, 65, 130, 7, 0), 264, 4, "bf16", "f32", True, True, True, 8),
+    ((130, 66, 2), 130, 3, "bf16", "bf16", True, True, True, 3),   # rows off 16-byte alignment, odd tail
+    ((3, 129, 1, 64), 7, 5, "bf16", "bf16", False, True, True, 0),  # narrower than a group
+    ((70, 5), 2056, 4, "bf16", "bf16", True, False, True, 0),       # two channel blocks
+    ((64, 1, 127), 36, 2, "f32", "f32", True, True, True, 0),
+    ((300, 0, 5), 131, 8, "f32", "bf16", True, False, True, 5),
+    ((2, 2, 2, 191), 3, 8, "f32", "f32", False, False, False, 1),
+    ((64, 64), 1028, 6, "f32", "f32", True, True, False, 0),
+    ((90, 38), 72, 7, "bf16", "f32", True, True, True, 0),
+]
+
+
+def conv_inputs(docs, C, W, dt, wdt, bias, s0, pad, seed):
+    r, T, N = rng(seed), sum(docs), len(docs)
+    x = dev(r.standard_normal((T, C)), DT[dt], pad)
+    w = dev(0.5 * r.standard_normal((C, W)), DT[wdt])
+    b = dev(0.2 * r.standard_normal(C), DT[wdt]) if bias else None
+    h = dev(r.standard_normal((N, W - 1, C)), DT[dt]) if s0 else None
+    dy = dev(r.standard_normal((T, C)), DT[dt], pad)
+    dst = dev(r.standard_normal((N, W - 1, C)), DT[dt]) if s0 else None
+    return x, w, b, h, dy, dst
+
+
+def cu_of(docs):
+    return np.concatenate([[0], np.cumsum(docs)]).astype(np.int32)
+
+
+@pytest.mark.parametrize("case", CONV, ids=lambda c: "%s_C%d_W%d_%s" % ("-".join(map(str, c[0])), c[1], c[2], c[3]))
+def test_conv(case):
+    docs, C, W, dt, wdt, silu, bias, s0, pad = case
+    g = gdr()
+    x, w, b, h, dy, dst = conv_inputs(docs, C, W, dt, wdt, bias, s0, pad, sum(docs) + C)
+    T, N = sum(docs), len(docs)
+    act = g.GDR_ACT_SILU if silu else g.GDR_ACT_NONE
+    p = g.ConvProblem(x, w, g.Plan(cu_of(docs)), b, h, act)
+    print("[case] conv", case, flush=True)
+    y, st = nan((T, C), DT[dt], pad), nan((N, W - 1, C), DT[dt])
+    g.conv_fwd(p, y, st)
+    ws = p.alloc_workspace().fill_(0xFF)
+    dx, dw, db = nan((T, C), DT[dt], pad), nan((C, W), F32), nan((C,), F32)
+    ds0 = nan((N, W - 1, C), DT[dt])
+    g.conv_bwd(p, dy, dst, dx, dw, db, ds0, ws)
+    torch.cuda.synchronize()
+    f = ref.conv(f64(x), f64(w), f64(b) if bias else 0.0 * f64(w)[:, 0], f64(h), docs, silu)
+    d = ref.conv_grad(f, f64(x), f64(w), docs, f64(dy), f64(dst), silu)
+    ref.close(y, f["y"], f["Ey"], DT[dt], "y")
+    assert np.array_equal(f64(st), f["st"]), "st"
+    for name, t, odt in (("dx", dx, DT[dt]), ("dw", dw, F32), ("db", db, F32), ("ds0", ds0, DT[dt])):
+        ref.close(t, d[name], d["E" + name], odt, name)
+    padding_untouched(y, C)
+    padding_untouched(dx, C)
+    # the optional outputs left out change nothing else, and the sums repeat bit for bit
+    y2, dx2, dw2 = nan((T, C), DT[dt]), nan((T, C), DT[dt]), nan((C, W), F32)
+    g.conv_fwd(p, y2)
+    g.conv_bwd(p, dy, dst, dx2, dw2, None, None, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(y2, y.contiguous()) and torch.equal(dx2, dx.contiguous()) and torch.equal(dw2, dw)
+
+
+def test_conv_empty_batches():
+    """No tokens: final rows are the carried-in ones, parameter gradients zero; no documents: nothing but the zeros."""
+    g = gdr()
+    for docs in ((), (0, 0)):
+        x, w, b, h, dy, dst = conv_inputs(docs, 24, 4, "bf16", "bf16", True, True, 0, 3)
+        p = g.ConvProblem(x, w, g.Plan(cu_of(docs)), b, h)
+        st, ds0 = nan(h.shape, BF), nan(h.shape, BF)
+        y, dx, dw, db = nan((0, 24), BF), nan((0, 24), BF), nan((24, 4), F32), nan((24,), F32)
+        g.conv_fwd(p, y, st)
+        g.conv_bwd(p, dy, dst, dx, dw, db, ds0, p.alloc_workspace())
+        torch.cuda.synchronize()
+        assert torch.equal(st, h) and torch.equal(ds0, dst)
+        assert not dw.any() and not db.any()
+
+
+@pytest.mark.parametrize("N,C,W,dt,pad", [(1, 128, 4, "bf16", 0), (5, 10240, 4, "bf16", 16), (9, 37, 3, "bf16", 0),
+                                          (4, 260, 2, "f32", 3), (3, 6, 8, "f32", 0), (70, 24, 5, "bf16", 0)])
+def test_conv_step(N, C, W, dt, pad):
+    """Three tokens in turn equal the convolution of the sequence; idle and padding slots stay as they were."""
+    g, r = gdr(), rng(N + C)
+    dtype = DT[dt]
+    n_slots = N + 3
+    w, b = dev(0.5 * r.standard_normal((C, W)), dtype), dev(0.2 * r.standard_normal(C), dtype)
+    state = dev(r.standard_normal((n_slots, W - 1, C)), dtype)
+    slots = torch.from_numpy(r.permutation(n_slots)[:N].astype(np.int32)).cuda()
+    if N > 3:
+        slots[1], slots[2] = -1, n_slots  # padding rows
+    live = [n for n in range(N) if 0 <= int(slots[n]) < n_slots]
+    before = state.clone()
+    xs = [dev(r.standard_normal((N, C)), dtype, pad) for _ in range(3)]
+    ys = []
+    print("[case] conv step", N, C, W, dt, flush=True)
+    for x in xs:
+        y = nan((N, C), dtype, pad)
+        g.conv_step(g.ConvStep(x, w, state, slots, b), y)
+        ys.append(y)
+    torch.cuda.synchronize()
+    sl = slots.cpu().numpy()
+    want = f64(before)
+    for n in live:
+        s0 = f64(before)[sl[n]]
+        f = ref.conv(np.stack([f64(x)[n] for x in xs]), f64(w), f64(b), s0[None], (3,), True)
+        ref.close(torch.stack([y[n] for y in ys]), f["y"], f["Ey"], dtype, "y of sequence %d" % n)
+        want[sl[n]] = f["st"][0]
+    assert np.array_equal(f64(state), want), "state"
+    for n in set(range(N)) - set(live):
+        assert all(bool(torch.isnan(y[n].float()).all()) for y in ys), "a padding row was written"
+    # without slots: sequence n in slot n
+    state2, y = before.clone(), nan((N, C), dtype)
+    g.conv_step(g.ConvStep(xs[0], w, state2, None, b), y)
+    torch.cuda.synchronize()
+    f = ref.conv(f64(xs[0]), f64(w), f64(b), f64(before)[:N], (1,) * N, True)
+    ref.close(y, f["y"], f["Ey"], dtype, "y without slots")
+    assert np.array_equal(f64(state2)[:N], f["st"]) and torch.equal(state2[N:], before[N:])
+
+
+# ---- gate ----
+
+GATE = [
+    # T, H, D, kind, dtype, bias, pad
+    (1, 1, 1, "softplus", "f32", True, 0),
+    (1, 1, 128, "sigmoid", "bf16", True, 0),
+    (77, 3, 128, "softplus", "bf16", True, 0),
+    (130, 2, 128, "sigmoid", "f32", False, 4),
+    (300, 48, 1, "softplus", "bf16", True, 0),
+    (65, 5, 1, "softplus", "f32", False, 3),
+    (9, 13, 1, "sigmoid", "bf16", True, 1),
+    (700, 1, 1, "sigmoid", "bf16", True, 0),
+    (40, 17, 128, "softplus", "f32", True, 0),
+]
+
+
+@pytest.mark.parametrize("case", GATE, ids=lambda c: "T%d_H%d_D%d_%s_%s" % c[:5])
+def test_gate(case):
+    T, H, D, kind, dt, bias, pad = case
+    g, r = gdr(), rng(T * H + D)
+    dtype = DT[dt]
+    print("[case] gate", case, flush=True)
+    x = dev(2.0 * r.standard_normal((T, H * D)), dtype, pad)
+    a = dev(0.7 * r.standard_normal(H))
+    b = dev(r.standard_normal(H * D)) if bias else None
+    dg = dev(r.standard_normal((T, H * D)))
+    p = g.GateProblem(x, a, b, g.GDR_GATE_SOFTPLUS if kind == "softplus" else g.GDR_GATE_SIGMOID, -5.0)
+    out, dx = nan((T, H * D), F32), nan((T, H * D), dtype, pad)
+    da, db = nan((H,), F32), nan((H * D,), F32)
+    g.gate_fwd(p, out)
+    g.gate_bwd(p, dg, dx, da, db, p.alloc_workspace().fill_(0xFF))
+    torch.cuda.synchronize()
+    X, B, DG = f64(x).reshape(T, H, D), (f64(b) if bias else np.zeros(H * D)).reshape(H, D), f64(dg).reshape(T, H, D)
+    v, E = ref.gate(X, f64(a), B, kind, -5.0)
+    if kind == "softplus":
+        # a value within its fp32 error of the floor may land on either side of it, where the slope jumps: none here
+        raw = -np.exp(f64(a))[:, None] * np.logaddexp(X + B, 0)
+        assert not (np.abs(raw + 5.0) <= E * ref.U).any()
+        assert (v == -5.0).any() or T < 60 or not bias, "the floor is not exercised"
+    ref.close(out.view(T, H, D), v, E, F32, "g")
+    d = ref.gate_grad(X, f64(a), B, kind, -5.0, DG)
+    ref.close(dx.reshape(T, H, D), d["dx"], d["Edx"], dtype, "dx")
+    ref.close(da, d["da"], d["Eda"], F32, "da")
+    ref.close(db.view(H, D), d["db"], d["Edb"], F32, "db")
+    padding_untouched(dx, H * D)
+    da2, dx2 = nan((H,), F32), nan((T, H * D), dtype)
+    g.gate_bwd(p, dg, dx2, da2, None, p.alloc_workspace())
+    torch.cuda.synchronize()
+    assert torch.equal(da2, da) and torch.equal(dx2, dx.contiguous())
+
+
+def test_gate_extremes():
+    """Infinities, far values and NaN: the limits of the formulas, and zero slopes there."""
+    g = gdr()
+    x = torch.tensor([[float("inf"), -float("inf"), 300.0, -300.0, float("nan"), 0.0]], device="cuda")
+    a = torch.zeros(6, device="cuda")
+    for kind, want in ((g.GDR_GATE_SOFTPLUS, [-5, 0, -5, 0, float("nan"), -np.log(2)]),
+                       (g.GDR_GATE_SIGMOID, [-5, 0, -5, 0, float("nan"), -2.5])):
+        p = g.GateProblem(x, a, None, kind, -5.0)
+        out, dx, da, dg = nan((1, 6), F32), nan((1, 6), F32), nan((6,), F32), torch.ones(1, 6, device="cuda")
+        g.gate_fwd(p, out)
+        g.gate_bwd(p, dg, dx, da, None, p.alloc_workspace())
+        torch.cuda.synchronize()
+        assert np.allclose(f64(out)[0], want, rtol=1e-6, atol=1e-30, equal_nan=True), out
+        slopes = f64(dx)[0]
+        assert np.array_equal(np.isnan(slopes), np.isnan(want)) and np.all(np.abs(slopes[:4]) < 1e-30), dx
+        assert np.array_equal(np.isnan(f64(da)), np.isnan(want)), da
+
+
+def test_gate_empty():
+    g = gdr()
+    p = g.GateProblem(torch.empty(0, 256, dtype=BF, device="cuda"), torch.zeros(2, device="cuda"))
+    da, db = nan((2,), F32), nan((256,), F32)
+    g.gate_fwd(p, torch.empty(0, 256, device="cuda"))
+    g.gate_bwd(p, torch.empty(0, 256, device="cuda"), torch.empty(0, 256, dtype=BF, device="cuda"), da, db, p.alloc_workspace())
+    torch.cuda.synchronize()
+    assert not da.any() and not db.any()
+
+
+# ---- single-token recurrence ----
+
+STEP = [
+    # variant, docs, H_qk, H_v, spare slots, activations, pad
+    ("kda", (1,), 1, 1, 0, False, 0),
+    ("gdn", (1,), 1, 1, 0, True, 0),
+    ("kda", (1, 1, 1), 3, 3, 2, True, 0),
+    ("gdn", (1, 1, 1, 1, 1), 2, 6, 1, False, 8),
+    ("kda", (4, 0, 1, 7), 2, 2, 3, False, 3),
+    ("gdn", (2, 9, 0, 1), 1, 3, 0, True, 0),
+    ("gdn", (33,), 4, 4, 0, False, 0),
+]
+
+
+def step_inputs(variant, docs, hqk, hv, spare, pad, seed, unit=True):
+    r, T = rng(seed), sum(docs)
+
+    def heads(H, u):
+        x = r.standard_normal((T, H, 128))
+        return dev(x / np.linalg.norm(x, axis=-1, keepdims=True) if u else x, BF, pad)
+
+    q, k, v = heads(hqk, unit), heads(hqk, unit), heads(hv, False)
+    g = dev(-5 * r.random((T, hv, 128) if variant == "kda" else (T, hv)))
+    beta = dev(r.standard_normal((T, hv)) if not unit else 1 / (1 + np.exp(-r.standard_normal((T, hv)))),
+               BF if variant == "kda" else F32)
+    state = dev(0.1 * r.standard_normal((len(docs) + spare, hv, 128, 128)))
+    slots = torch.from_numpy(r.permutation(len(docs) + spare)[:len(docs)].astype(np.int32)).cuda()
+    return q, k, v, g, beta, state, slots
+
+
+@pytest.mark.parametrize("case", STEP, ids=lambda c: "%s_%s_h%d_%d" % (c[0], "-".join(map(str, c[1])), c[2], c[3]))
+def test_step(case):
+    variant, docs, hqk, hv, spare, act, pad = case
+    g = gdr()
+    q, k, v, gate, beta, state, slots = step_inputs(variant, docs, hqk, hv, spare, pad, sum(docs) + hv, not act)
+    before = state.clone()
+    single = all(n == 1 for n in docs)
+    cu = None if single else torch.from_numpy(cu_of(docs)).cuda()
+    print("[case] step", case, flush=True)
+    p = g.StepProblem(g.GDR_KDA if variant == "kda" else g.GDR_GDN, q, k, v, gate, beta, state, cu, slots,
+                      input_flags=g.GDR_IN_QK_L2NORM | g.GDR_IN_BETA_SIGMOID if act else 0)
+    o = nan(v.shape, BF)
+    (g.kda_step if variant == "kda" else g.gdn_step)(p, o)
+    torch.cuda.synchronize()
+    ro, Eo, rs, Es = ref.step(f64(q), f64(k), f64(v), f64(gate), f64(beta), f64(before), docs, slots.cpu().numpy(), 128 ** -0.5,
+                              act, act)
+    ref.close(o, ro, Eo, BF, "o")
+    ref.close(state, rs, Es, F32, "state")
+    idle = sorted(set(range(len(before))) - {int(s) for s, n in zip(slots, docs) if n})
+    assert torch.equal(state[idle], before[idle]), "an idle slot was written"
+
+
+def test_step_skips_padding():
+    """Slots outside the pool, empty sequences and rows behind the last sequence are left as they were; a cu_seqlens that
+    runs past T is clipped."""
+    g = gdr()
+    docs = (1, 2, 1, 1)
+    q, k, v, gate, beta, state, slots = step_inputs("gdn", docs, 1, 2, 1, 0, 5)
+    slots[1], slots[2] = -3, 5
+    before = state.clone()
+    cu = torch.tensor([0, 1, 3, 4, 4], dtype=torch.int32, device="cuda")  # the last row belongs to no sequence
+    o = nan(v.shape, BF)
+    g.gdn_step(g.StepProblem(g.GDR_GDN, q, k, v, gate, beta, state, cu, slots), o)
+    torch.cuda.synchronize()
+    ro, Eo, rs, Es = ref.step(f64(q), f64(k), f64(v), f64(gate), f64(beta), f64(before), (1,), [int(slots[0])], 128 ** -0.5, False, False)
+    ref.close(o[:1], ro[:1], Eo[:1], BF, "o")
+    assert bool(torch.isnan(o[1:].float()).all())
+    ref.close(state, rs, Es, F32, "state")
+    state2, o2 = before.clone(), nan(v.shape, BF)
+    past = torch.tensor([0, 1, 3, 4, 9], dtype=torch.int32, device="cuda")
+    g.gdn_step(g.StepProblem(g.GDR_GDN, q, k, v, gate, beta, state2, past, None), o2)
+    torch.cuda.synchronize()
+    ro, Eo, rs, Es = ref.step(f64(q), f64(k), f64(v), f64(gate), f64(beta), f64(before), docs, [0, 1, 2, 3], 128 ** -0.5, False, False)
+    ref.close(o2, ro, Eo, BF, "o")
+    ref.close(state2, rs, Es, F32, "state")
+
+
+# ---- norm ----
+
+NORM = [
+    # T, H, D, placement, dtype, residual dtype, activation, weight dtype, pad
+    (1, 1, 1, "none", "f32", "f32", "none", "f32", 0),
+    (5, 3, 128, "none", "bf16", "bf16", "silu", "f32", 0),
+    (37, 16, 128, "none", "bf16", "bf16", "sigmoid", "bf16", 8),
+    (9, 2, 128, "none", "f32", "f32", "silu", "f32", 3),
+    (7, 5, 64, "none", "bf16", "bf16", "silu", None, 0),
+    (11, 1, 7, "before", "bf16", "f32", "none", "f32", 1),
+    (19, 1, 257, "before", "bf16", "bf16", "none", "bf16", 0),
+    (6, 1, 2048, "before", "bf16", "f32", "none", "f32", 0),
+    (6, 1, 2048, "after", "bf16", "bf16", "silu", "f32", 16),
+    (3, 1, 2049, "after", "f32", "f32", "sigmoid", "f32", 0),
+    (4, 1, 5001, "before", "bf16", "f32", "silu", "bf16", 0),
+    (2, 1, 10240, "after", "bf16", "f32", "none", "f32", 0),
+    (2, 1, 16384, "none", "f32", "f32", "none", "f32", 0),
+    (300, 1, 384, "before", "f32", "f32", "none", None, 4),
+    (1030, 5, 40, "none", "bf16", "bf16", "silu", "f32", 0),
+    (3, 2, 700, "none", "bf16", "bf16", "sigmoid", "f32", 5),
+]
+
+
+@pytest.mark.parametrize("case", NORM, ids=lambda c: "T%d_H%d_D%d_%s_%s_%s_%s" % c[:7])
+def test_norm(case):
+    T, H, D, place, dt, rdt, act, wdt, pad = case
+    g, r = gdr(), rng(T + D)
+    dtype, rtype = DT[dt], DT[rdt]
+    shape = (T, H, D)
+    print("[case] norm", case, flush=True)
+    x = dev(r.standard_normal(shape), dtype, pad)
+    w = dev(1 + 0.2 * r.standard_normal(D), DT[wdt]) if wdt else None
+    z = dev(2 * r.standard_normal(shape), dtype, pad) if act != "none" else None
+    res = dev(r.standard_normal(shape), rtype) if place != "none" else None
+    s = nan(shape, rtype) if place == "before" else None
+    ydt = rtype if place == "after" else dtype
+    dy = dev(r.standard_normal(shape), ydt)
+    ds = dev(r.standard_normal(shape), rtype) if place == "before" else None
+    alpha = 0.5 if place != "none" else 1.0
+    kinds = {"none": (g.GDR_ACT_NONE, g.GDR_RES_NONE), "silu": (g.GDR_ACT_SILU,), "sigmoid": (g.GDR_ACT_SIGMOID,),
+             "before": g.GDR_RES_BEFORE, "after": g.GDR_RES_AFTER}
+    code = g.GDR_RES_NONE if place == "none" else kinds[place]
+    p = g.NormProblem(x, w, z, kinds[act][0], res, s, code, alpha, 1e-6)
+    y, dx, dw = nan(shape, ydt), nan(shape, dtype, pad), nan((D,), F32)
+    dz = nan(shape, dtype, pad) if z is not None else None
+    dres = nan(shape, rtype) if place == "before" else None
+    g.norm_fwd(p, y)
+    g.norm_bwd(p, dy, dx, dw, p.alloc_workspace().fill_(0xFF), dz, ds, dres)
+    torch.cuda.synchronize()
+    W = f64(w) if w is not None else np.ones(D)
+    f = ref.norm(f64(x), W, f64(z), f64(res), place, act, alpha, 1e-6)
+    ref.close(y, f["y"], f["Ey"], ydt, "y")
+    if s is not None:
+        ref.close(s, f["s"], f["Es"], rtype, "s")
+    d = ref.norm_grad(f64(s) if s is not None else f64(x), W, f64(z), f64(dy), f64(ds), place, act, alpha, 1e-6)
+    ref.close(dx, d["dx"], d["Edx"], dtype, "dx")
+    ref.close(dw, d["dw"], d["Edw"], F32, "dw")
+    padding_untouched(dx, H * D)
+    if dz is not None:
+        ref.close(dz, d["dz"], d["Edz"], dtype, "dz")
+        padding_untouched(dz, H * D)
+    if dres is not None:
+        ref.close(dres, d["dres"], d["Edres"], rtype, "dres")
+        # the backward needs only the stream: without x, without dx, ds and dw
+        q = g.NormProblem(None, w, z, kinds[act][0], None, s, code, alpha, 1e-6, dtype=dtype)
+        dres2 = nan(shape, rtype)
+        g.norm_bwd(q, dy, None, None, None, dz, None, dres2)
+        torch.cuda.synchronize()
+        d2 = ref.norm_grad(f64(s), W, f64(z), f64(dy), None, place, act, alpha, 1e-6)
+        ref.close(dres2, d2["dres"], d2["Edres"], rtype, "dres without ds")
+
+
+def test_norm_zero_rows_and_empty():
+    """A row of zeros stays finite; no rows give zero parameter gradients."""
+    g = gdr()
+    x = torch.zeros(3, 2, 128, dtype=BF, device="cuda")
+    w = torch.ones(128, device="cuda")
+    p = g.NormProblem(x, w)
+    y, dx, dw = nan(x.shape, BF), nan(x.shape, BF), nan((128,), F32)
+    g.norm_fwd(p, y)
+    g.norm_bwd(p, torch.ones_like(x), dx, dw, p.alloc_workspace())
+    e = torch.empty(0, 128, dtype=BF, device="cuda")
+    q = g.NormProblem(e, w)
+    dw0 = nan((128,), F32)
+    g.norm_fwd(q, torch.empty_like(e))
+    g.norm_bwd(q, torch.empty_like(e), torch.empty_like(e), dw0, q.alloc_workspace())
+    torch.cuda.synchronize()
+    assert not y.any() and not dw.any() and not dw0.any()
+    assert bool((dx.float() - 1000.0).abs().max() <= 1000 * (2.0 ** -8 + 64 * ref.U))
+
+
+# ---- streams, graphs and the whole layer ----
+
+
+def test_other_stream():
+    """A call on another stream runs in that stream's order."""
+    g = gdr()
+    x, w, b, h, dy, dst = conv_inputs((500, 300), 512, 4, "bf16", "bf16", True, True, 0, 1)
+    p = g.ConvProblem(x, w, g.Plan(cu_of((500, 300))), b, h)
+    want = nan((800, 512), BF)
+    g.conv_fwd(p, want)
+    torch.cuda.synchronize()
+    side, got, keep = torch.cuda.Stream(), nan((800, 512), BF), x.clone()
+    x.zero_()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        x.copy_(keep)
+    g.conv_fwd(p, got, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+
+
+def layer_pass(g, docs, H, W, seed, T_total=None):
+    """Inputs of one KDA layer's core: raw projections of every token."""
+    r, T = rng(seed), sum(docs)
+    C = H * 128
+    return dict(qkv=dev(r.standard_normal((T, 3 * C)), BF), w=dev(0.5 * r.standard_normal((3 * C, W)), BF),
+                graw=dev(0.5 * r.standard_normal((T, C)), BF), a=dev(0.3 * r.standard_normal(H)), gb=dev(r.standard_normal(C)),
+                beta=dev(r.standard_normal((T, H)), BF), z=dev(r.standard_normal((T, C)), BF), nw=dev(1 + 0.1 * r.standard_normal(128)))
+
+
+def run_prompt(g, m, docs, H, W):
+    """Convolution, gate, recurrence and head norm over a packed batch; returns y, the recurrence's and the convolution's states."""
+    T, N, C = sum(docs), len(docs), H * 128
+    cu = cu_of(docs)
+    plan = g.Plan(cu)
+    act, st = nan((T, 3 * C), BF), nan((N, W - 1, 3 * C), BF)
+    g.conv_fwd(g.ConvProblem(m["qkv"], m["w"], plan), act, st)
+    q, k, v = (act[:, i * C:(i + 1) * C].contiguous().view(T, H, 128) for i in range(3))
+    gate = nan((T, H, 128), F32)
+    g.gate_fwd(g.GateProblem(m["graw"], m["a"], m["gb"], g.GDR_GATE_SIGMOID), gate)
+    prob = g.Problem(g.GDR_KDA, q, k, v, gate, m["beta"], cu, input_flags=g.GDR_IN_QK_L2NORM | g.GDR_IN_BETA_SIGMOID)
+    o, ht = nan((T, H, 128), BF), nan((N, H, 128, 128), F32)
+    g.kda_fwd(prob, o, ht, prob.alloc_workspace(0))
+    y = nan((T, H, 128), BF)
+    g.norm_fwd(g.NormProblem(o, m["nw"], m["z"].view(T, H, 128), g.GDR_ACT_SIGMOID), y)
+    return y, ht, st
+
+
+def test_prompt_then_tokens():
+    """A layer's core over prompts and then token by token through the single-token calls equals the core over the whole
+    sequences: the states handed over are the ones the prompt left.
+
+    Both sides round q, k, v and o to bf16 at the same places; the whole-sequence side also rounds the recurrence's chunk
+    products to bf16 (its stated accuracy is 1e-2 relative RMS), so the two agree to that."""
+    g = gdr()
+    H, W, prompts, more = 2, 4, (70, 1, 129), 5
+    C, N = H * 128, len(prompts)
+    whole = tuple(p + more for p in prompts)
+    m = layer_pass(g, whole, H, W, 9)
+    y_all, ht_all, st_all = run_prompt(g, m, whole, H, W)
+    starts = cu_of(whole)[:-1]
+    rows = np.concatenate([np.arange(s, s + p) for s, p in zip(starts, prompts)])
+    part = {k: (t[torch.from_numpy(rows).cuda()].contiguous() if k in ("qkv", "graw", "beta", "z") else t) for k, t in m.items()}
+    y0, state, conv_state = run_prompt(g, part, prompts, H, W)
+    # static buffers of a serving loop, the slots of a larger pool
+    pool, cpool = nan((N + 2, H, 128, 128), F32), nan((N + 2, W - 1, 3 * C), BF)
+    slots = torch.tensor([3, 0, 4], dtype=torch.int32, device="cuda")
+    pool[slots.long()], cpool[slots.long()] = state, conv_state
+    x, act = nan((N, 3 * C), BF), nan((N, 3 * C), BF)
+    graw, gate, beta = nan((N, C), BF), nan((N, H, 128), F32), nan((N, H), BF)
+    z, o, y = nan((N, H, 128), BF), nan((N, H, 128), BF), nan((N, H, 128), BF)
+    heads = [act[:, i * C:(i + 1) * C].unflatten(1, (H, 128)) for i in range(3)]
+    cs = g.ConvStep(x, m["w"], cpool, slots)
+    gp = g.GateProblem(graw, m["a"], m["gb"], g.GDR_GATE_SIGMOID)
+    sp = g.StepProblem(g.GDR_KDA, *heads, gate, beta, pool, None, slots, input_flags=g.GDR_IN_QK_L2NORM | g.GDR_IN_BETA_SIGMOID)
+    npb = g.NormProblem(o, m["nw"], z, g.GDR_ACT_SIGMOID)
+
+    def token():
+        g.conv_step(cs, act)
+        g.gate_fwd(gp, gate)
+        g.kda_step(sp, o)
+        g.norm_fwd(npb, y)
+
+    def feed(i):
+        at = torch.from_numpy(starts + np.array(prompts) + i).long().cuda()
+        x.copy_(m["qkv"][at])
+        graw.copy_(m["graw"][at])
+        beta.copy_(m["beta"][at])
+        z.copy_(m["z"].view(-1, H, 128)[at])
+        return at
+
+    # the loop captured into a graph, replayed for each token with eager work between; the capture runs nothing
+    saved = pool.clone(), cpool.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        feed(0)
+        token()  # loads the kernels before the capture
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    pool.copy_(saved[0])
+    cpool.copy_(saved[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        token()
+    epool, ecpool = saved[0].clone(), saved[1].clone()
+    for i in range(more):
+        at = feed(i)
+        graph.replay()
+        torch.cuda.synchronize()
+        want, got = f64(y_all[at]), f64(y)
+        rel = np.linalg.norm(got - want) / np.linalg.norm(want)
+        assert rel <= 1.5e-2, "token %d: %.3g" % (i, rel)  # 1e-2 on either side, independent: sqrt(2) 1e-2
+        # and the replay equals the eager calls on a state of their own, bit for bit
+        ey = y.clone()
+        keep = pool.clone(), cpool.clone()
+        pool.copy_(epool)
+        cpool.copy_(ecpool)
+        token()
+        torch.cuda.synchronize()
+        assert torch.equal(ey, y) and torch.equal(keep[0][slots.long()], pool[slots.long()])
+        epool, ecpool = pool.clone(), cpool.clone()
+    rel = np.linalg.norm(f64(pool[slots.long()]) - f64(ht_all)) / np.linalg.norm(f64(ht_all))
+    assert rel <= 1.5e-2, rel
+    assert torch.equal(cpool[slots.long()], st_all)
+    for free in (1, 2):
+        assert bool(torch.isnan(pool[free]).all()) and bool(torch.isnan(cpool[free].float()).all())
+
+
+def test_training_graph_replays():
+    """Forward and backward of convolution, gate and norm captured once and replayed on changed inputs, with eager work
+    between, equal the eager calls."""
+    g = gdr()
+    docs = (130, 1, 77)
+    T, H, C, W = sum(docs), 3, 384, 4
+    x, w, b, h, dy, dst = conv_inputs(docs, C, W, "bf16", "bf16", True, True, 0, 2)
+    p = g.ConvProblem(x, w, g.Plan(cu_of(docs)), b, h)
+    graw, a, gb = dev(rng(1).standard_normal((T, C)), BF), dev(rng(2).standard_normal(H)), dev(rng(3).standard_normal(C))
+    gp = g.GateProblem(graw, a, gb)
+    dg = dev(rng(4).standard_normal((T, C)))
+    nw = dev(1 + 0.1 * rng(5).standard_normal(128))
+    s, res = nan((T, H, 128), F32), dev(rng(6).standard_normal((T, H, 128)))
+    y = nan((T, C), BF)
+    npb = g.NormProblem(y.view(T, H, 128), nw, residual=res, s=s, placement=g.GDR_RES_BEFORE)
+    outs = dict(st=nan((3, W - 1, C), BF), gate=nan((T, C), F32), n=nan((T, H, 128), BF), dx=nan((T, C), BF), dw=nan((C, W), F32),
+                db=nan((C,), F32), ds0=nan((3, W - 1, C), BF), dgx=nan((T, C), BF), da=nan((H,), F32), dgb=nan((C,), F32),
+                dres=nan((T, H, 128), F32), dn=nan((T, H, 128), BF), dnw=nan((128,), F32))
+    ws = [q.alloc_workspace() for q in (p, gp, npb)]
+
+    def step():
+        g.conv_fwd(p, y, outs["st"])
+        g.gate_fwd(gp, outs["gate"])
+        g.norm_fwd(npb, outs["n"])
+        g.norm_bwd(npb, outs["n"], outs["dn"], outs["dnw"], ws[2], dres=outs["dres"])
+        g.gate_bwd(gp, dg, outs["dgx"], outs["da"], outs["dgb"], ws[1])
+        g.conv_bwd(p, outs["dn"].view(T, C), dst, outs["dx"], outs["dw"], outs["db"], outs["ds0"], ws[0])
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(3):
+        x.copy_(dev(rng(20 + i).standard_normal((T, C)), BF))
+        graw.copy_(dev(rng(30 + i).standard_normal((T, C)), BF))
+        for t in list(outs.values()) + [s, y]:
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = {k: t.clone() for k, t in outs.items()}
+        for t in list(outs.values()) + [s, y]:
+            t.fill_(float("nan"))
+        step()
+        torch.cuda.synchronize()
+        for k in outs:
+            assert torch.equal(got[k], outs[k]), (i, k)
