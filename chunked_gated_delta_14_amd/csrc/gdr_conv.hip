@@ -18,7 +18,7 @@ struct ConvArgs {
   const int32_t *table;
   int N, NC, C;
   int64_t xs;
-  bool silu, wbf;
+  bool wbf;
   int lx, ly, nchb;
 };
 
@@ -64,6 +64,15 @@ __device__ __forceinline__ void load_carried(const ConvArgs &a, int W, int doc, 
   else r.zero();
 }
 
+// The thread's set within its block.  With UNI a wavefront lies within one set
+// (Lanes::uniform): its rows, their addresses and the document's bounds are then
+// scalar values, and a row's access is one instruction with a scalar base.
+template <bool UNI>
+__device__ __forceinline__ int set_of(int lx) {
+  const int ty = threadIdx.x / lx;
+  return UNI ? __builtin_amdgcn_readfirstlane(ty) : ty;
+}
+
 // First token and token count of a document, from its chunks.
 __device__ __forceinline__ void doc_span(const ChunkTable &tb, int doc, int &start, int &len) {
   const int c0 = tb.doc_ptr[doc], c1 = tb.doc_ptr[doc + 1];
@@ -95,10 +104,10 @@ __device__ __forceinline__ void push(float (&win)[D][VEC], const float (&x)[VEC]
 
 // Forward: a thread takes R consecutive tokens of one chunk.  Blocks past the
 // `nrb` row blocks write the final rows st instead, LY documents each.
-template <class T, int VEC, int W, int R>
+template <class T, int VEC, int W, bool SILU, bool UNI, int R>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int nrb, T *__restrict__ y, int64_t ys,
                                                        T *__restrict__ st) {
-  const int tx = threadIdx.x % a.lx, ty = threadIdx.x / a.lx;
+  const int tx = threadIdx.x % a.lx, ty = set_of<UNI>(a.lx);
   const int chb = blockIdx.x % a.nchb, rb = blockIdx.x / a.nchb;
   const int group = chb * a.lx + tx;
   if (ty >= a.ly || group >= (a.C + VEC - 1) / VEC) return;
@@ -137,8 +146,12 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int nrb, T *_
     if (p >= 0) hist[j].load(x + (int64_t)(start - (W - 1) + j) * a.xs + c);
     else load_carried<T, VEC>(a, W, doc, p, c, hist[j]);
   }
+  const T *__restrict__ px = x + (int64_t)start * a.xs;
 #pragma unroll
-  for (int t = 0; t < R; ++t) in[t].load(x + (int64_t)(start + min(t, len - 1)) * a.xs + c);
+  for (int t = 0; t < R; ++t) {
+    in[t].load(px + c);
+    if (t < len - 1) px += a.xs;  // past the end: the last row again
+  }
 
   float w[W][VEC], b[VEC], win[W - 1][VEC];
   load_taps<VEC, W>(a, c, w, b);
@@ -146,43 +159,46 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int nrb, T *_
   for (int j = 0; j < W - 1; ++j)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) win[j][e] = hist[j].get(e);
+  T *__restrict__ py = y + (int64_t)start * ys;
 #pragma unroll
   for (int t = 0; t < R; ++t) {
     float xv[VEC], z[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) xv[e] = in[t].get(e);
     taps<VEC, W>(w, b, win, xv, z);
-    if (a.silu) {
+    if constexpr (SILU) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) z[e] *= sigmoid<sizeof(T) == 4>(z[e]);
     }
     Raw<T, VEC> out;
     out.set(z);
-    if (t < len) out.store(y + (int64_t)(start + t) * ys + c);
+    if (t < len) out.store(py + c);
+    py += ys;
     push<VEC, W - 1>(win, xv);
   }
 }
 
 // dz = dy act'(z).
-template <bool EXACT>
-__device__ __forceinline__ float act_grad(float dy, float z, bool silu) {
-  if (!silu) return dy;
+template <bool EXACT, bool SILU>
+__device__ __forceinline__ float act_grad(float dy, float z) {
+  if constexpr (!SILU) return dy;
   const float s = sigmoid<EXACT>(z);
   return dy * (s * fmaf(z, 1.f - s, 1.f));
 }
 
-// Backward: a worker walks its share of the chunks, keeping the last W-1 rows of
-// x and dz in registers; z is formed again from x.  It reads W-1 rows past each
-// chunk's end, whose dz reach back into the chunk.  The parameter terms stay in
-// registers over all the worker's chunks and leave as one partial row per block.  Blocks
-// past the `nwb` worker blocks form ds0, LY documents each.
-template <class T, int VEC, int W>
-__global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int nwb, int workers, const T *__restrict__ dy, int64_t ds,
+// Backward: a worker walks its share of the runs of R tokens, keeping the last W-1
+// rows of x and dz in registers; z is formed again from x.  It reads W-1 rows past
+// each run's end, whose dz reach back into the run.  The parameter terms stay in
+// registers over all the worker's runs and leave as one partial row per block.
+// Blocks past the `nwb` worker blocks form ds0, LY documents each.
+template <class T, int VEC, int W, bool SILU, bool UNI>
+__global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int R, int nwb, int workers, const T *__restrict__ dy, int64_t ds,
                                                        const T *__restrict__ dst, T *__restrict__ dx, int64_t xs_out,
                                                        T *__restrict__ ds0, float *__restrict__ partial) {
   constexpr bool EXACT = sizeof(T) == 4;
-  constexpr int B = 8;  // tokens per batch of loads
-  const int tx = threadIdx.x % a.lx, ty = threadIdx.x / a.lx;
+  constexpr int B = 4;  // tokens per batch of loads; the next batch is in flight during one's arithmetic
+  const int RUNS = 64 / R;
+  const int tx = threadIdx.x % a.lx, ty = set_of<UNI>(a.lx);
   const int chb = blockIdx.x % a.nchb, wb = blockIdx.x / a.nchb;
   const int group = chb * a.lx + tx, groups = (a.C + VEC - 1) / VEC;
   const bool live = ty < a.ly && group < groups;
@@ -223,7 +239,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int nwb, int 
       taps<VEC, W>(w, b, win, xv, z);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const float dz = act_grad<EXACT>(rd.get(e), z[e], a.silu);
+        const float dz = act_grad<EXACT, SILU>(rd.get(e), z[e]);
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
           if (j >= t) acc[j][e] = fmaf(w[j - t < 0 ? 0 : j - t][e], dz, acc[j][e]);
@@ -240,8 +256,9 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int nwb, int 
   }
 
   const int worker = wb * a.ly + ty;
-  const int first = (int)((int64_t)a.NC * worker / workers);
-  const int last = live ? (int)((int64_t)a.NC * (worker + 1) / workers) : first;
+  const int64_t runs = (int64_t)a.NC * RUNS;
+  const int first = (int)(runs * worker / workers);
+  const int last = live ? (int)(runs * (worker + 1) / workers) : first;
   float dw[W][VEC], db[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
@@ -249,14 +266,15 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int nwb, int 
 #pragma unroll
     for (int i = 0; i < W; ++i) dw[i][e] = 0.f;
   }
-  for (int chunk = first; chunk < last; ++chunk) {
-    const int start = tb.start[chunk], len = tb.len[chunk], doc = tb.doc[chunk];
-    const int pos = (chunk - tb.doc_ptr[doc]) * 64;
-    // the document's last chunk ends it; others are followed by at least one row
+  for (int run = first; run < last; ++run) {
+    const int chunk = run / RUNS, sub = run % RUNS;
+    const int len = min(R, tb.len[chunk] - sub * R);
+    if (len <= 0) continue;
+    const int start = tb.start[chunk] + sub * R, doc = tb.doc[chunk];
+    const int pos = (chunk - tb.doc_ptr[doc]) * 64 + sub * R;
     const int lastc = tb.doc_ptr[doc + 1] - 1;
-    const int end = chunk == lastc ? len : len + min(W - 1, tb.len[chunk + 1]);
-    // dz rows that reach into this chunk: [0, end) exist, zeros up to len + W - 1
-    const int dlen = (lastc - chunk) * 64 + tb.len[lastc];  // tokens of the document from `start` on
+    const int left = (lastc - chunk) * 64 + tb.len[lastc] - sub * R;  // tokens of the document from `start` on
+    const int end = min(len + W - 1, left);                           // rows whose dz reach into the run
     float win[W - 1][VEC], dzw[W - 1][VEC];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
@@ -267,14 +285,24 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int nwb, int 
 #pragma unroll
       for (int e = 0; e < VEC; ++e) win[j][e] = r.get(e), dzw[j][e] = 0.f;
     }
+    const T *__restrict__ px = x + (int64_t)start * a.xs;
+    const T *__restrict__ pd = dy + (int64_t)start * ds;
+    T *__restrict__ po = dx + (int64_t)start * xs_out;
+    Raw<T, VEC> nx[B], nd[B];
+    auto fetch = [&](int t0) {
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        nx[i].load(px + c);
+        nd[i].load(pd + c);
+        if (t0 + i < end - 1) px += a.xs, pd += ds;  // past the end: the last row again
+      }
+    };
+    fetch(0);
     for (int t0 = 0; t0 < len + W - 1; t0 += B) {
       Raw<T, VEC> rx[B], rd[B];
 #pragma unroll
-      for (int i = 0; i < B; ++i) {
-        const int64_t row = start + min(t0 + i, end - 1);
-        rx[i].load(x + row * a.xs + c);
-        rd[i].load(dy + row * ds + c);
-      }
+      for (int i = 0; i < B; ++i) rx[i] = nx[i], rd[i] = nd[i];
+      if (t0 + B < len + W - 1) fetch(t0 + B);
 #pragma unroll
       for (int i = 0; i < B; ++i) {
         const int t = t0 + i;
@@ -283,7 +311,11 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int nwb, int 
         for (int e = 0; e < VEC; ++e) xv[e] = rx[i].get(e);
         taps<VEC, W>(w, b, win, xv, z);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) dz[e] = t < end ? act_grad<EXACT>(rd[i].get(e), z[e], a.silu) : 0.f;
+        for (int e = 0; e < VEC; ++e) dz[e] = act_grad<EXACT, SILU>(rd[i].get(e), z[e]);
+        if (t >= end) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) dz[e] = 0.f;
+        }
         if (t < len) {
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
@@ -302,7 +334,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int nwb, int 
 #pragma unroll
             for (int j = 0; j < W - 1; ++j) g[e] = fmaf(w[W - 1 - j][e], dzw[j][e], g[e]);
           }
-          const int q = s - (dlen - (W - 1));
+          const int q = s - (left - (W - 1));
           if (dst && q >= 0) {
             Raw<T, VEC> d;
             d.load(dst + ((int64_t)doc * (W - 1) + q) * a.C + c);
@@ -311,7 +343,8 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int nwb, int 
           }
           Raw<T, VEC> out;
           out.set(g);
-          out.store(dx + (int64_t)(start + s) * xs_out + c);
+          out.store(po + c);
+          po += xs_out;
         }
         push<VEC, W - 1>(win, xv);
         push<VEC, W - 1>(dzw, dz);
@@ -328,7 +361,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int nwb, int 
 // One token per sequence: the W-1 rows of the sequence's slot and the new row give
 // y; the slot keeps the last W-1 rows.  Rows whose slot lies outside the pool are
 // left alone.
-template <class T, int VEC, int W>
+template <class T, int VEC, int W, bool SILU>
 __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a, T *__restrict__ y, int64_t ys, T *state,
                                                         const int32_t *__restrict__ slots, int n_slots) {
   const int tx = threadIdx.x % a.lx, ty = threadIdx.x / a.lx;
@@ -352,7 +385,7 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a, T *__restric
     for (int j = 0; j < W - 1; ++j) win[j][e] = hist[j].get(e);
   }
   taps<VEC, W>(w, b, win, xv, z);
-  if (a.silu) {
+  if constexpr (SILU) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) z[e] *= sigmoid<sizeof(T) == 4>(z[e]);
   }
@@ -370,35 +403,43 @@ ConvArgs args_of(const gdr_conv &p, const Lanes &l) {
   a.table = p.chunk_table;
   a.N = p.N; a.NC = p.n_chunks; a.C = p.C;
   a.xs = p.x_stride;
-  a.silu = p.activation == GDR_ACT_SILU;
   a.wbf = p.w_dtype == GDR_BF16;
   a.lx = l.lx; a.ly = l.ly; a.nchb = l.nchb;
   return a;
 }
 
-// Calls f(type tag, VEC, W) with the compile-time values of the problem.
+// Calls f(type tag, VEC, W, SILU, UNI) with the compile-time values of the problem.
 template <int N>
-struct Int {
-  static constexpr int value = N;
-};
-template <class T, int VEC, class F>
+using Int = std::integral_constant<int, N>;
+template <class T, int VEC, bool SILU, bool UNI, class F>
 hipError_t with_width(int W, F f) {
+  const T t{};
+  const Int<VEC> v;
+  const Int<SILU> s;
+  const Int<UNI> u;
   switch (W) {
-    case 2: return f(T(), Int<VEC>(), Int<2>());
-    case 3: return f(T(), Int<VEC>(), Int<3>());
-    case 4: return f(T(), Int<VEC>(), Int<4>());
-    case 5: return f(T(), Int<VEC>(), Int<5>());
-    case 6: return f(T(), Int<VEC>(), Int<6>());
-    case 7: return f(T(), Int<VEC>(), Int<7>());
-    case 8: return f(T(), Int<VEC>(), Int<8>());
+    case 2: return f(t, v, Int<2>(), s, u);
+    case 3: return f(t, v, Int<3>(), s, u);
+    case 4: return f(t, v, Int<4>(), s, u);
+    case 5: return f(t, v, Int<5>(), s, u);
+    case 6: return f(t, v, Int<6>(), s, u);
+    case 7: return f(t, v, Int<7>(), s, u);
+    case 8: return f(t, v, Int<8>(), s, u);
     default: return hipErrorInvalidValue;
   }
 }
-template <int BYTES, class F>
-hipError_t with_types(const gdr_conv &p, int vec, F f) {
-  if (p.dtype == GDR_BF16)
-    return vec == 1 ? with_width<u16, 1>(p.W, f) : with_width<u16, BYTES / 2>(p.W, f);
-  return vec == 1 ? with_width<float, 1>(p.W, f) : with_width<float, BYTES / 4>(p.W, f);
+template <class T, int VEC, class F>
+hipError_t with_flags(const gdr_conv &p, const Lanes &l, F f) {
+  const bool silu = p.activation == GDR_ACT_SILU;
+  if constexpr (VEC > 1) {
+    if (l.uniform) return silu ? with_width<T, VEC, true, true>(p.W, f) : with_width<T, VEC, false, true>(p.W, f);
+  }
+  return silu ? with_width<T, VEC, true, false>(p.W, f) : with_width<T, VEC, false, false>(p.W, f);
+}
+template <int BF_VEC, class F>
+hipError_t with_types(const gdr_conv &p, int vec, const Lanes &l, F f) {
+  if (p.dtype == GDR_BF16) return vec == 1 ? with_flags<u16, 1>(p, l, f) : with_flags<u16, BF_VEC>(p, l, f);
+  return vec == 1 ? with_flags<float, 1>(p, l, f) : with_flags<float, 4>(p, l, f);
 }
 
 constexpr int FWD_RUN = 16;  // tokens per thread of the forward
@@ -413,28 +454,30 @@ hipError_t launch_conv_fwd(const gdr_conv &p, void *y, int64_t y_stride, void *s
   const int64_t blocks = (nrb + (st ? (p.N + l.ly - 1) / l.ly : 0)) * l.nchb;
   if (blocks == 0) return hipSuccess;
   if (blocks >= (int64_t(1) << 31)) return hipErrorInvalidValue;
-  return with_types<16>(p, vec, [&](auto t, auto v, auto w) {
+  return with_types<8>(p, vec, l, [&](auto t, auto v, auto w, auto s, auto u) {
     using T = decltype(t);
-    conv_fwd_kernel<T, decltype(v)::value, decltype(w)::value, FWD_RUN><<<(unsigned)blocks, l.threads, 0, stream>>>(
-        a, (int)nrb, static_cast<T *>(y), y_stride, static_cast<T *>(st));
+    conv_fwd_kernel<T, decltype(v)::value, decltype(w)::value, decltype(s)::value, decltype(u)::value, FWD_RUN>
+        <<<(unsigned)blocks, l.threads, 0, stream>>>(a, (int)nrb, static_cast<T *>(y), y_stride, static_cast<T *>(st));
     return hipGetLastError();
   });
 }
 
 hipError_t launch_conv_bwd(const gdr_conv &p, const void *dy, int64_t dy_stride, const void *dst, void *dx,
-                           int64_t dx_stride, void *ds0, float *partial, int workers, hipStream_t stream) {
-  const int vec = vec_of(p.C, p.dtype, CONV_BWD_BYTES);
-  const Lanes l = lanes_for(groups_of(p.C, vec));
+                           int64_t dx_stride, void *ds0, float *partial, hipStream_t stream) {
+  const int vec = conv_bwd_vec(p.C);
+  const ConvBwdPlan plan = conv_bwd_plan(p.n_chunks, p.C);
+  const Lanes &l = plan.lanes;
   const ConvArgs a = args_of(p, l);
-  const int nwb = workers / l.ly;  // a multiple
+  const int nwb = plan.workers / l.ly;  // a multiple
   const int64_t blocks = ((int64_t)nwb + (ds0 ? (p.N + l.ly - 1) / l.ly : 0)) * l.nchb;
   if (blocks == 0) return hipSuccess;
   if (blocks >= (int64_t(1) << 31)) return hipErrorInvalidValue;
-  return with_types<CONV_BWD_BYTES>(p, vec, [&](auto t, auto v, auto w) {
+  return with_types<4>(p, vec, l, [&](auto t, auto v, auto w, auto s, auto u) {
     using T = decltype(t);
-    conv_bwd_kernel<T, decltype(v)::value, decltype(w)::value><<<(unsigned)blocks, l.threads, 0, stream>>>(
-        a, nwb, workers, static_cast<const T *>(dy), dy_stride, static_cast<const T *>(dst), static_cast<T *>(dx), dx_stride,
-        static_cast<T *>(ds0), partial);
+    conv_bwd_kernel<T, decltype(v)::value, decltype(w)::value, decltype(s)::value, decltype(u)::value>
+        <<<(unsigned)blocks, l.threads, 0, stream>>>(a, plan.run, nwb, plan.workers, static_cast<const T *>(dy), dy_stride,
+                                                     static_cast<const T *>(dst), static_cast<T *>(dx), dx_stride,
+                                                     static_cast<T *>(ds0), partial);
     return hipGetLastError();
   });
 }
@@ -442,14 +485,15 @@ hipError_t launch_conv_bwd(const gdr_conv &p, const void *dy, int64_t dy_stride,
 hipError_t launch_conv_step(const gdr_conv &p, void *y, int64_t y_stride, void *state, const int32_t *slots,
                             int32_t n_slots, hipStream_t stream) {
   const int full = vec_of(p.C, p.dtype), vec = p.C % full == 0 ? full : 1;
-  const Lanes l = lanes_for(p.C / vec);
-  ConvArgs a = args_of(p, l);
+  Lanes l = lanes_for(p.C / vec);
+  l.uniform = false;
+  const ConvArgs a = args_of(p, l);
   const int64_t blocks = (int64_t)l.nchb * ((p.N + l.ly - 1) / l.ly);
   if (blocks == 0) return hipSuccess;
   if (blocks >= (int64_t(1) << 31)) return hipErrorInvalidValue;
-  return with_types<16>(p, vec, [&](auto t, auto v, auto w) {
+  return with_types<8>(p, vec, l, [&](auto t, auto v, auto w, auto s, auto) {
     using T = decltype(t);
-    conv_step_kernel<T, decltype(v)::value, decltype(w)::value><<<(unsigned)blocks, l.threads, 0, stream>>>(
+    conv_step_kernel<T, decltype(v)::value, decltype(w)::value, decltype(s)::value><<<(unsigned)blocks, l.threads, 0, stream>>>(
         a, static_cast<T *>(y), y_stride, static_cast<T *>(state), slots, n_slots);
     return hipGetLastError();
   });

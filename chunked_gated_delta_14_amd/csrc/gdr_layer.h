@@ -14,22 +14,35 @@ namespace gdr {
 
 // Lane map of the kernels whose rows are C channels wide: a thread owns one group
 // of `vec` neighbouring channels, LX threads span LX groups, LY sets of LX threads
-// take LY different rows (or runs of rows), nchb blocks span all groups.  LX is
-// not rounded to a power of two, so narrow and odd rows leave few lanes idle.
+// take LY different rows (or runs of rows), nchb blocks span all groups.  Wide rows
+// take LX in whole wavefronts (`uniform`: a wavefront's rows are scalar values) unless
+// that leaves more than a fifth of the lanes idle; others take LX as it comes, so
+// narrow and odd rows leave few lanes idle.
 struct Lanes {
   int lx, ly, nchb, threads;
+  bool uniform;
 };
 inline Lanes lanes_for(int groups) {
   Lanes l;
-  l.nchb = (groups + 255) / 256;
-  l.lx = (groups + l.nchb - 1) / l.nchb;
+  const int waves = (groups + 63) / 64;
+  l.uniform = groups * 5 >= waves * 64 * 4;
+  if (l.uniform) {
+    // the widest of 4, 3, 2, 1 wavefronts that adds no idle wavefront
+    int k = 4;
+    while (waves % k) --k;
+    l.nchb = waves / k;
+    l.lx = 64 * k;
+  } else {
+    l.nchb = (groups + 255) / 256;
+    l.lx = (groups + l.nchb - 1) / l.nchb;
+  }
   l.ly = std::max(1, 256 / l.lx);
   l.threads = (l.lx * l.ly + 63) / 64 * 64;
   return l;
 }
 // Channels per thread: 16 bytes of a row, or single channels for rows narrower than that.
-inline int vec_of(int channels, int dtype, int bytes = 16) {
-  const int v = bytes / (dtype == GDR_BF16 ? 2 : 4);
+inline int vec_of(int channels, int dtype) {
+  const int v = dtype == GDR_BF16 ? 8 : 4;
   return channels >= v ? v : 1;
 }
 inline int groups_of(int channels, int vec) { return (channels + vec - 1) / vec; }
@@ -44,9 +57,26 @@ inline int workers_for(int64_t rows, const Lanes &l, int64_t target) {
   return (int)((w + l.ly - 1) / l.ly * l.ly);
 }
 
-constexpr int CONV_BWD_BYTES = 16;  // bytes of a row per thread in the convolution's backward
-inline Lanes conv_bwd_lanes(int C, int dtype) { return lanes_for(groups_of(C, vec_of(C, dtype, CONV_BWD_BYTES))); }
-inline int conv_workers(int n_chunks, int C, int dtype) { return workers_for(n_chunks, conv_bwd_lanes(C, dtype), 131072); }
+// The convolution's backward: 4 channels per thread, runs of 64 tokens, or shorter
+// ones where the chunks are too few to fill the chip (each run reads W-1 rows
+// before and after itself again).  Measured with 8 channels per thread (twice the
+// registers, half the wavefronts) and one run per chunk: [16792, 3832] W = 2 117 us,
+// [512, 128] 19 us, [40000, 37] 27 us; as here 94, 14 and 16 us, large packs level.
+struct ConvBwdPlan {
+  Lanes lanes;
+  int run, workers;
+  int rows() const { return workers / lanes.ly; }  // partial rows, one per block
+};
+inline int conv_bwd_vec(int C) { return C >= 4 ? 4 : 1; }
+inline ConvBwdPlan conv_bwd_plan(int n_chunks, int C) {
+  ConvBwdPlan p;
+  p.lanes = lanes_for(groups_of(C, conv_bwd_vec(C)));
+  const int64_t target = 131072, threads = (int64_t)n_chunks * p.lanes.nchb * p.lanes.lx;
+  p.run = 64;
+  while (p.run > 8 && threads * (64 / p.run) < target * 3 / 4) p.run /= 2;
+  p.workers = workers_for((int64_t)n_chunks * (64 / p.run), p.lanes, target);
+  return p;
+}
 inline Lanes gate_lanes(int C, int dtype) { return lanes_for(groups_of(C, vec_of(C, dtype))); }
 inline int gate_workers(int64_t T, int C, int dtype) { return workers_for((T + 7) / 8, gate_lanes(C, dtype), 262144); }
 // norm: a worker is a block (see gdr_norm.hip)
@@ -56,7 +86,7 @@ inline int norm_workers(int64_t rows, int D) {
 
 hipError_t launch_conv_fwd(const gdr_conv &p, void *y, int64_t y_stride, void *st, hipStream_t stream);
 hipError_t launch_conv_bwd(const gdr_conv &p, const void *dy, int64_t dy_stride, const void *dst, void *dx,
-                           int64_t dx_stride, void *ds0, float *partial, int workers, hipStream_t stream);
+                           int64_t dx_stride, void *ds0, float *partial, hipStream_t stream);
 hipError_t launch_conv_step(const gdr_conv &p, void *y, int64_t y_stride, void *state, const int32_t *slots,
                             int32_t n_slots, hipStream_t stream);
 hipError_t launch_gate_fwd(const gdr_gate &p, float *g, hipStream_t stream);

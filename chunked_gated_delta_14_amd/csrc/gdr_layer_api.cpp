@@ -69,9 +69,8 @@ int32_t check_conv(const gdr_conv *p, bool step) {
   if (p->N > 0 && !p->chunk_table) return invalid("chunk_table must be non-NULL");
   return GDR_OK;
 }
-int64_t conv_bytes(int32_t n_chunks, int32_t C, int32_t W, int32_t dtype) {
-  const int64_t rows = gdr::conv_workers(n_chunks, C, dtype) / gdr::conv_bwd_lanes(C, dtype).ly;
-  return round_up(rows * (W + 1) * C * 4);
+int64_t conv_bytes(int32_t n_chunks, int32_t C, int32_t W) {
+  return round_up((int64_t)gdr::conv_bwd_plan(n_chunks, C).rows() * (W + 1) * C * 4);
 }
 
 int32_t conv_fwd(const gdr_conv *p, void *y, int64_t y_stride, void *st, void *stream) {
@@ -97,14 +96,13 @@ int32_t conv_bwd(const gdr_conv *p, const void *dy, int64_t dy_stride, const voi
   if (!element_aligned(dy, p->dtype) || !element_aligned(dst, p->dtype) || !element_aligned(dx, p->dtype) ||
       !element_aligned(ds0, p->dtype) || !element_aligned(dw, GDR_F32) || !element_aligned(dbias, GDR_F32))
     return invalid("gradients must be aligned to their elements");
-  const int64_t need = conv_bytes(p->n_chunks, p->C, p->W, p->dtype);
+  const int64_t need = conv_bytes(p->n_chunks, p->C, p->W);
   if ((rc = check_workspace(ws, ws_bytes, need))) return rc;
   if ((rc = gdr::host_check_device())) return rc;
-  const int workers = gdr::conv_workers(p->n_chunks, p->C, p->dtype);
-  const int rows = workers / gdr::conv_bwd_lanes(p->C, p->dtype).ly;
+  const int rows = gdr::conv_bwd_plan(p->n_chunks, p->C).rows();
   float *partial = static_cast<float *>(ws);
   if ((rc = launch(gdr::TK_CONV_BWD, stream, "convolution gradient launch", [&](hipStream_t s) {
-         return gdr::launch_conv_bwd(*p, dy, dy_stride, dst, dx, dx_stride, ds0, partial, workers, s);
+         return gdr::launch_conv_bwd(*p, dy, dy_stride, dst, dx, dx_stride, ds0, partial, s);
        })))
     return rc;
   if ((rc = launch(gdr::TK_PARAM_SUM, stream, "parameter sum launch",
@@ -313,7 +311,7 @@ int64_t gdr_conv_workspace_bytes(int32_t n_chunks, int32_t C, int32_t W, int32_t
   if (n_chunks < 0 || C < 1 || !is_dtype(dtype)) return -(int64_t)invalid("n_chunks must be >= 0, C positive and dtype known");
   if (W < 2 || W > 8) return -(int64_t)unsupported("W outside 2..8");
   if (C > (1 << 24)) return -(int64_t)unsupported("C above 2^24");
-  return conv_bytes(n_chunks, C, W, dtype);
+  return conv_bytes(n_chunks, C, W);
 }
 int32_t gdr_conv_bwd(const gdr_conv *p, const void *dy, int64_t dy_stride, const void *dst, void *dx, int64_t dx_stride,
                      float *dweight, float *dbias, void *ds0, void *workspace, int64_t workspace_bytes, void *stream) {
