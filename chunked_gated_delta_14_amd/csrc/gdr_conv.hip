@@ -22,14 +22,6 @@ struct ConvArgs {
   int lx, ly, nchb;
 };
 
-// The lane's first channel; the last group of a row whose width is no multiple of
-// VEC starts early and repeats its neighbour's channels (the same values, written
-// twice), so every access is whole.
-template <int VEC>
-__device__ __forceinline__ int first_channel(int group, int C) {
-  return VEC == 1 ? group : min(group * VEC, C - VEC);
-}
-
 template <int VEC, int W>
 __device__ __forceinline__ void load_taps(const ConvArgs &a, int c, float (&w)[W][VEC], float (&b)[VEC]) {
   if constexpr (VEC == 1) {
@@ -62,15 +54,6 @@ template <class T, int VEC>
 __device__ __forceinline__ void load_carried(const ConvArgs &a, int W, int doc, int pos, int c, Raw<T, VEC> &r) {
   if (a.s0) r.load(static_cast<const T *>(a.s0) + ((int64_t)doc * (W - 1) + (W - 1) + pos) * a.C + c);
   else r.zero();
-}
-
-// The thread's set within its block.  With UNI a wavefront lies within one set
-// (Lanes::uniform): its rows, their addresses and the document's bounds are then
-// scalar values, and a row's access is one instruction with a scalar base.
-template <bool UNI>
-__device__ __forceinline__ int set_of(int lx) {
-  const int ty = threadIdx.x / lx;
-  return UNI ? __builtin_amdgcn_readfirstlane(ty) : ty;
 }
 
 // First token and token count of a document, from its chunks.

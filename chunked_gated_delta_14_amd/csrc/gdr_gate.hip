@@ -5,10 +5,10 @@
 //   sigmoid:  g = floor sigma(A u),             dg/du = floor A s(1-s),         dg/da = u dg/du
 //
 // a is one value per head, b one per channel.  softplus(u) = max(u,0) + log(1+e)
-// with e = exp(-|u|) in (0,1], and log(1+e) = 2 artanh(v) = 2 (v + v^3/3 + ...)
-// with v = e/(2+e) <= 1/3: the odd series keeps its relative accuracy for tiny e,
-// where 1 + e would lose it; the first term left out, v^15/15, is at most 1.4e-8 of v,
-// below half an fp32 step.
+// with e = exp(-|u|) in (0,1], and log(1+e) = 2 artanh(v) with v = e/(2+e) <= 1/3:
+// an odd function of v keeps its relative accuracy for tiny e, where 1 + e would
+// lose it.  Bound by HBM; the arithmetic, about 30 lane operations per value, is
+// two thirds of what the vector units do in that time, so it is kept short.
 #include "gdr_layer.h"
 #include "gdr_vec.h"
 
@@ -24,41 +24,51 @@ struct GateArgs {
   int lx, ly, nchb;
 };
 
-__device__ __forceinline__ float log1p01(float e) {  // e in [0, 1]
+// log(1+e) / 2 for e in [0, 1]: artanh(v) = v + v^3 p(v^2), p fitted to degree 3 for
+// v^2 in [0, 1/9] with a relative error of 5e-9, a twelfth of fp32's half step.
+__device__ __forceinline__ float half_log1p(float e) {
   const float v = e * __builtin_amdgcn_rcpf(2.f + e), q = v * v;
-  float s = fmaf(q, 1.f / 13.f, 1.f / 11.f);
-  s = fmaf(s, q, 1.f / 9.f);
-  s = fmaf(s, q, 1.f / 7.f);
-  s = fmaf(s, q, 1.f / 5.f);
-  s = fmaf(s, q, 1.f / 3.f);
-  return 2.f * fmaf(v * q, s, v);
+  float p = fmaf(q, 0.140122339f, 0.139995694f);
+  p = fmaf(p, q, 0.200108498f);
+  p = fmaf(p, q, 0.333332062f);
+  return fmaf(v * q, p, v);
+}
+// e^-|x|, the argument cut at 104 (the result is below fp32's smallest value
+// there), which keeps infinities out of the correction; a NaN passes.
+__device__ __forceinline__ float exp_neg_abs(float x) {
+  float a = __builtin_fabsf(x);
+  a = a > 104.f ? 104.f : a;
+  const float t = a * -1.44269504088896341f, e = __builtin_amdgcn_exp2f(t);
+  return fmaf(e, fmaf(a, -1.44269504088896341f, -t) * 0.693147180559945309f, e);
+}
+// -A softplus(u) from e = exp(-|u|).
+__device__ __forceinline__ float softplus_raw(float u, float e, float A) {
+  return fmaf(-2.f * A, half_log1p(e), -A * fmaxf(u, 0.f));
 }
 
 template <int KIND>
 __device__ __forceinline__ float gate_value(float u, float A, float floor) {
   if constexpr (KIND == GDR_GATE_SOFTPLUS) {
-    const float e = fast_exp<true>(-__builtin_fabsf(u));
-    const float raw = -A * ((u > 0.f ? u : 0.f) + log1p01(e));
-    return raw < floor ? floor : u == u ? raw : u;  // a NaN stays one
+    const float raw = softplus_raw(u, exp_neg_abs(u), A);
+    return raw < floor ? floor : raw;  // a NaN stays one
   } else {
-    return floor * sigmoid<true>(A * u);
+    const float w = A * u, e = exp_neg_abs(w), r = floor * __builtin_amdgcn_rcpf(1.f + e);
+    return w < 0.f ? e * r : r;
   }
 }
 // du = dg/du and da = dg/da at u.
 template <int KIND>
 __device__ __forceinline__ void gate_slopes(float u, float A, float floor, float &du, float &da) {
   if constexpr (KIND == GDR_GATE_SOFTPLUS) {
-    const float e = fast_exp<true>(-__builtin_fabsf(u)), r = __builtin_amdgcn_rcpf(1.f + e);
-    const float raw = -A * ((u > 0.f ? u : 0.f) + log1p01(e));
-    const bool live = !(raw < floor);
-    du = live ? -A * (u >= 0.f ? r : e * r) : 0.f;
-    da = live ? raw : 0.f;
-    if (u != u) du = da = u;
+    const float e = exp_neg_abs(u), r = -A * __builtin_amdgcn_rcpf(1.f + e);
+    const float raw = softplus_raw(u, e, A);
+    const bool held = raw < floor;
+    du = held ? 0.f : u < 0.f ? e * r : r;
+    da = held ? 0.f : raw;
   } else {
-    const float s = sigmoid<true>(A * u), c = sigmoid<true>(-A * u);  // 1 - s keeps its accuracy
-    du = floor * A * (s * c);
-    da = du * u;
-    if (s == 0.f || c == 0.f) da = 0.f;  // the slope vanished: u itself may be infinite
+    const float e = exp_neg_abs(A * u), r = __builtin_amdgcn_rcpf(1.f + e);
+    du = floor * A * (e * r * r);       // s (1 - s) = e / (1 + e)^2 on either side
+    da = du == 0.f ? 0.f : du * u;      // the slope vanished: u itself may be infinite
   }
 }
 
@@ -66,91 +76,103 @@ template <int VEC>
 __device__ __forceinline__ void load_params(const GateArgs &p, int c, float (&A)[VEC], float (&b)[VEC]) {
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
-    A[e] = fast_exp<true>(p.a[(c + e) / p.D]);
+    A[e] = fast_exp<true>(p.a[p.D == 1 ? c + e : (c + e) >> 7]);
     b[e] = p.b ? p.b[c + e] : 0.f;
   }
 }
 
 constexpr int U = 4;  // rows in flight per thread
 
-template <class T, int VEC, int KIND>
+template <class T, int VEC, int KIND, bool UNI>
 __global__ __launch_bounds__(256) void gate_fwd_kernel(GateArgs p, int workers, float *__restrict__ g) {
-  const int tx = threadIdx.x % p.lx, ty = threadIdx.x / p.lx;
+  const int tx = threadIdx.x % p.lx, ty = set_of<UNI>(p.lx);
   const int chb = blockIdx.x % p.nchb, worker = (blockIdx.x / p.nchb) * p.ly + ty;
   const int group = chb * p.lx + tx;
   if (ty >= p.ly || group >= (p.C + VEC - 1) / VEC) return;
-  const int c = VEC == 1 ? group : min(group * VEC, p.C - VEC);
+  const int c = first_channel<VEC>(group, p.C);
   float A[VEC], b[VEC];
   load_params<VEC>(p, c, A, b);
-  const T *__restrict__ x = static_cast<const T *>(p.x) + c;
-  g += c;
-  for (int64_t t0 = worker; t0 < p.T; t0 += (int64_t)U * workers) {
+  const T *__restrict__ x = static_cast<const T *>(p.x) + worker * p.xs;
+  float *__restrict__ out = g + (int64_t)worker * p.C;
+  const int64_t xstep = workers * p.xs, gstep = (int64_t)workers * p.C;
+  for (int64_t t = worker; t < p.T; t += (int64_t)U * workers) {
     Raw<T, VEC> r[U];
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int64_t t = t0 + (int64_t)i * workers;
-      r[i].load(x + (t < p.T ? t : t0) * p.xs);
-    }
+    for (int i = 0; i < U; ++i) r[i].load((t + (int64_t)i * workers < p.T ? x + i * xstep : x) + c);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int64_t t = t0 + (int64_t)i * workers;
       float v[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) v[e] = gate_value<KIND>(r[i].get(e) + b[e], A[e], p.floor);
       Raw<float, VEC> o;
       o.set(v);
-      if (t < p.T) o.store(g + t * p.C);
+      if (t + (int64_t)i * workers < p.T) o.store(out + i * gstep + c);
     }
+    x += U * xstep;
+    out += U * gstep;
   }
 }
 
-template <class T, int VEC, int KIND>
+// A block leaves one partial row: the C sums of dg du, then the sums of dg da, per
+// channel (D = 1) or per thread's VEC channels of one head (D = 128).
+template <class T, int VEC, int KIND, bool UNI>
 __global__ __launch_bounds__(256) void gate_bwd_kernel(GateArgs p, int workers, const float *__restrict__ dg,
                                                        T *__restrict__ dx, int64_t dxs, float *__restrict__ partial) {
-  const int tx = threadIdx.x % p.lx, ty = threadIdx.x / p.lx;
+  const int tx = threadIdx.x % p.lx, ty = set_of<UNI>(p.lx);
   const int chb = blockIdx.x % p.nchb, worker = (blockIdx.x / p.nchb) * p.ly + ty;
-  const int group = chb * p.lx + tx;
-  const bool live = ty < p.ly && group < (p.C + VEC - 1) / VEC;
-  const int c = VEC == 1 ? min(group, p.C - 1) : min(group * VEC, p.C - VEC);
+  const int group = chb * p.lx + tx, groups = (p.C + VEC - 1) / VEC;
+  const bool live = ty < p.ly && group < groups;
+  const int c = first_channel<VEC>(min(group, groups - 1), p.C);
   float A[VEC], b[VEC], sa[VEC], sb[VEC];
   load_params<VEC>(p, c, A, b);
 #pragma unroll
   for (int e = 0; e < VEC; ++e) sa[e] = sb[e] = 0.f;
-  const T *__restrict__ x = static_cast<const T *>(p.x) + c;
-  dg += c;
-  dx += c;
-  for (int64_t t0 = live ? worker : p.T; t0 < p.T; t0 += (int64_t)U * workers) {
+  const T *__restrict__ x = static_cast<const T *>(p.x) + worker * p.xs;
+  const float *__restrict__ d = dg + (int64_t)worker * p.C;
+  T *__restrict__ out = dx + worker * dxs;
+  const int64_t xstep = workers * p.xs, gstep = (int64_t)workers * p.C, ostep = workers * dxs;
+  for (int64_t t = live ? worker : p.T; t < p.T; t += (int64_t)U * workers) {
     Raw<T, VEC> r[U];
-    Raw<float, VEC> d[U];
+    Raw<float, VEC> q[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int64_t t = t0 + (int64_t)i * workers, at = t < p.T ? t : t0;
-      r[i].load(x + at * p.xs);
-      d[i].load(dg + at * p.C);
+      const bool there = t + (int64_t)i * workers < p.T;
+      r[i].load((there ? x + i * xstep : x) + c);
+      q[i].load((there ? d + i * gstep : d) + c);
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int64_t t = t0 + (int64_t)i * workers;
-      if (t < p.T) {
+      if (t + (int64_t)i * workers < p.T) {
         float v[VEC];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           float du, da;
           gate_slopes<KIND>(r[i].get(e) + b[e], A[e], p.floor, du, da);
-          v[e] = d[i].get(e) * du;
+          v[e] = q[i].get(e) * du;
           sb[e] += v[e];
-          sa[e] = fmaf(d[i].get(e), da, sa[e]);
+          sa[e] = fmaf(q[i].get(e), da, sa[e]);
         }
         Raw<T, VEC> o;
         o.set(v);
-        o.store(dx + t * dxs);
+        o.store(out + i * ostep + c);
       }
     }
+    x += U * xstep;
+    d += U * gstep;
+    out += U * ostep;
   }
-  float *q = partial + (int64_t)(blockIdx.x / p.nchb) * 2 * p.C + c;
   __shared__ float sums[256 * VEC];
-  block_partial<VEC>(sb, sums, tx, ty, p.lx, p.ly, live, q);
-  block_partial<VEC>(sa, sums, tx, ty, p.lx, p.ly, live, q + p.C);
+  const int per_row = gate_partial_row(p.C, p.D, VEC);
+  float *q = partial + (int64_t)(blockIdx.x / p.nchb) * per_row;
+  block_partial<VEC>(sb, sums, tx, ty, p.lx, p.ly, live, q + c);
+  if (p.D == 1) {
+    block_partial<VEC>(sa, sums, tx, ty, p.lx, p.ly, live, q + p.C + c);
+  } else {
+    float s[1] = {0.f};
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) s[0] += sa[e];
+    block_partial<1>(s, sums, tx, ty, p.lx, p.ly, live, q + p.C + c / VEC);
+  }
 }
 
 GateArgs args_of(const gdr_gate &p, const Lanes &l) {
@@ -163,43 +185,58 @@ GateArgs args_of(const gdr_gate &p, const Lanes &l) {
   return a;
 }
 
+// Calls f(type tag, VEC, KIND, UNI) with the compile-time values of the problem.
+template <int N>
+using Int = std::integral_constant<int, N>;
 template <class T, int VEC, class F>
-hipError_t with_kind(int kind, F f) {
-  if (kind == GDR_GATE_SOFTPLUS) return f(T(), std::integral_constant<int, VEC>(), std::integral_constant<int, GDR_GATE_SOFTPLUS>());
-  return f(T(), std::integral_constant<int, VEC>(), std::integral_constant<int, GDR_GATE_SIGMOID>());
+hipError_t with_flags(int kind, bool uniform, F f) {
+  const T t{};
+  const Int<VEC> v;
+  if (kind == GDR_GATE_SOFTPLUS)
+    return uniform ? f(t, v, Int<GDR_GATE_SOFTPLUS>(), Int<1>()) : f(t, v, Int<GDR_GATE_SOFTPLUS>(), Int<0>());
+  return uniform ? f(t, v, Int<GDR_GATE_SIGMOID>(), Int<1>()) : f(t, v, Int<GDR_GATE_SIGMOID>(), Int<0>());
 }
-template <class F>
-hipError_t with_types(const gdr_gate &p, int vec, F f) {
-  if (p.dtype == GDR_BF16) return vec == 1 ? with_kind<u16, 1>(p.kind, f) : with_kind<u16, 8>(p.kind, f);
-  return vec == 1 ? with_kind<float, 1>(p.kind, f) : with_kind<float, 4>(p.kind, f);
+template <int BF_VEC, class F>
+hipError_t with_types(const gdr_gate &p, int vec, bool uniform, F f) {
+  if (p.dtype == GDR_BF16) return vec == 1 ? with_flags<u16, 1>(p.kind, uniform, f) : with_flags<u16, BF_VEC>(p.kind, uniform, f);
+  return vec == 1 ? with_flags<float, 1>(p.kind, uniform, f) : with_flags<float, GATE_VEC>(p.kind, uniform, f);
+}
+
+// Channels per thread of the forward.  From bf16, 4: a wavefront's stores then cover
+// whole lines one after the other ([261392, 2048] 646 us, with 8 channels 701 us).
+// From fp32, 8: twice the bytes in flight ([100000, 2048] 324 us, with 4 359 us).
+int fwd_vec(int C, int dtype) {
+  const int v = dtype == GDR_BF16 ? 4 : GATE_VEC;
+  return C >= v ? v : 1;
 }
 
 }  // namespace
 
 hipError_t launch_gate_fwd(const gdr_gate &p, float *g, hipStream_t stream) {
   if (p.T == 0) return hipSuccess;
-  const int C = p.H * p.D, vec = vec_of(C, p.dtype);
+  const int C = p.H * p.D;
+  const int vec = fwd_vec(C, p.dtype);
   const Lanes l = lanes_for(groups_of(C, vec));
   const int workers = workers_for((p.T + U - 1) / U, l, 1 << 21);
   const GateArgs a = args_of(p, l);
-  const unsigned blocks = (unsigned)((workers + l.ly - 1) / l.ly * l.nchb);
-  return with_types(p, vec, [&](auto t, auto v, auto k) {
+  const unsigned blocks = (unsigned)(workers / l.ly * l.nchb);
+  return with_types<4>(p, vec, l.uniform, [&](auto t, auto v, auto k, auto u) {
     using T = decltype(t);
-    gate_fwd_kernel<T, decltype(v)::value, decltype(k)::value><<<blocks, l.threads, 0, stream>>>(a, workers, g);
+    gate_fwd_kernel<T, decltype(v)::value, decltype(k)::value, decltype(u)::value><<<blocks, l.threads, 0, stream>>>(a, workers, g);
     return hipGetLastError();
   });
 }
 
-hipError_t launch_gate_bwd(const gdr_gate &p, const float *dg, void *dx, int64_t dx_stride, float *partial, int workers,
-                           hipStream_t stream) {
+hipError_t launch_gate_bwd(const gdr_gate &p, const float *dg, void *dx, int64_t dx_stride, float *partial, hipStream_t stream) {
   if (p.T == 0) return hipSuccess;
-  const int C = p.H * p.D, vec = vec_of(C, p.dtype);
-  const Lanes l = lanes_for(groups_of(C, vec));
+  const int C = p.H * p.D;
+  const Lanes l = gate_lanes(C);
+  const int workers = gate_rows(p.T, C) * l.ly;
   const GateArgs a = args_of(p, l);
-  const unsigned blocks = (unsigned)((workers + l.ly - 1) / l.ly * l.nchb);
-  return with_types(p, vec, [&](auto t, auto v, auto k) {
+  const unsigned blocks = (unsigned)(workers / l.ly * l.nchb);
+  return with_types<GATE_VEC>(p, gate_vec(C), l.uniform, [&](auto t, auto v, auto k, auto u) {
     using T = decltype(t);
-    gate_bwd_kernel<T, decltype(v)::value, decltype(k)::value><<<blocks, l.threads, 0, stream>>>(
+    gate_bwd_kernel<T, decltype(v)::value, decltype(k)::value, decltype(u)::value><<<blocks, l.threads, 0, stream>>>(
         a, workers, dg, static_cast<T *>(dx), dx_stride, partial);
     return hipGetLastError();
   });

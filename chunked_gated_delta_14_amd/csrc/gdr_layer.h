@@ -77,8 +77,18 @@ inline ConvBwdPlan conv_bwd_plan(int n_chunks, int C) {
   p.workers = workers_for((int64_t)n_chunks * (64 / p.run), p.lanes, target);
   return p;
 }
-inline Lanes gate_lanes(int C, int dtype) { return lanes_for(groups_of(C, vec_of(C, dtype))); }
-inline int gate_workers(int64_t T, int C, int dtype) { return workers_for((T + 7) / 8, gate_lanes(C, dtype), 262144); }
+
+// The gate's backward: 8 channels per thread for either type.  A block's partial row holds
+// the C sums of dbias and the terms of da, one per channel or per thread.
+constexpr int GATE_VEC = 8;
+inline int gate_vec(int C) { return C >= GATE_VEC ? GATE_VEC : 1; }
+inline Lanes gate_lanes(int C) { return lanes_for(groups_of(C, gate_vec(C))); }
+inline int gate_rows(int64_t T, int C) {
+  const Lanes l = gate_lanes(C);
+  return workers_for((T + 7) / 8, l, 131072) / l.ly;
+}
+__host__ __device__ inline int gate_partial_row(int C, int D, int vec) { return C + (D == 1 ? C : C / vec); }
+
 // norm: a worker is a block (see gdr_norm.hip)
 inline int norm_workers(int64_t rows, int D) {
   return (int)std::min<int64_t>(std::max<int64_t>(rows * D / 4096, rows > 0), 1024);
@@ -90,17 +100,15 @@ hipError_t launch_conv_bwd(const gdr_conv &p, const void *dy, int64_t dy_stride,
 hipError_t launch_conv_step(const gdr_conv &p, void *y, int64_t y_stride, void *state, const int32_t *slots,
                             int32_t n_slots, hipStream_t stream);
 hipError_t launch_gate_fwd(const gdr_gate &p, float *g, hipStream_t stream);
-hipError_t launch_gate_bwd(const gdr_gate &p, const float *dg, void *dx, int64_t dx_stride, float *partial, int workers,
-                           hipStream_t stream);
+hipError_t launch_gate_bwd(const gdr_gate &p, const float *dg, void *dx, int64_t dx_stride, float *partial, hipStream_t stream);
 hipError_t launch_step(bool gdn, const gdr_step &p, uint16_t *o, hipStream_t stream);
 hipError_t launch_norm_fwd(const gdr_norm &p, void *y, hipStream_t stream);
 hipError_t launch_norm_bwd(const gdr_norm &p, const void *dy, const void *ds, void *dx, int64_t dx_stride, void *dgate,
                            int64_t dgate_stride, void *dres, float *partial, int workers, hipStream_t stream);
 
 // Sums of `rows` partial rows, in a fixed order.  conv: partial [rows][W + 1][C] ->
-// dw [C][W], dbias [C].  gate: partial [rows][2][H D] -> dbias [H D] and da [H] (the
-// second row summed over each head's D channels; D is 1 or 128).  norm: partial
-// [rows][D] -> dw.  A NULL output is skipped.
+// dw [C][W], dbias [C].  gate: partial [rows][gate_partial_row] -> dbias [H D] and da
+// [H] (D is 1 or 128).  norm: partial [rows][D] -> dw.  A NULL dbias is skipped.
 hipError_t launch_conv_sum(const float *partial, int rows, int C, int W, float *dw, float *dbias, hipStream_t stream);
 hipError_t launch_gate_sum(const float *partial, int rows, int H, int D, float *da, float *dbias, hipStream_t stream);
 hipError_t launch_norm_sum(const float *partial, int rows, int D, float *dw, hipStream_t stream);

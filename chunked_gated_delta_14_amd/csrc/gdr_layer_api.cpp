@@ -149,7 +149,9 @@ int32_t check_gate(const gdr_gate *p) {
     return invalid("x, a_log and bias must be aligned to their elements");
   return GDR_OK;
 }
-int64_t gate_rows(int32_t T, int32_t C, int32_t dtype) { return gdr::gate_workers(T, C, dtype) / gdr::gate_lanes(C, dtype).ly; }
+int64_t gate_bytes(int32_t T, int32_t C, int32_t D) {
+  return round_up((int64_t)gdr::gate_rows(T, C) * gdr::gate_partial_row(C, D, gdr::gate_vec(C)) * 4);
+}
 
 int32_t gate_fwd(const gdr_gate *p, float *g, void *stream) {
   int32_t rc = check_gate(p);
@@ -173,16 +175,15 @@ int32_t gate_bwd(const gdr_gate *p, const float *dg, void *dx, int64_t dx_stride
   if (!element_aligned(dg, GDR_F32) || !element_aligned(dx, p->dtype) || !element_aligned(da, GDR_F32) ||
       !element_aligned(dbias, GDR_F32))
     return invalid("gradients must be aligned to their elements");
-  const int64_t rows = gate_rows(p->T, C, p->dtype);
-  if ((rc = check_workspace(ws, ws_bytes, round_up(rows * 2 * C * 4)))) return rc;
+  if ((rc = check_workspace(ws, ws_bytes, gate_bytes(p->T, C, p->D)))) return rc;
   if ((rc = gdr::host_check_device())) return rc;
   float *partial = static_cast<float *>(ws);
-  const int workers = gdr::gate_workers(p->T, C, p->dtype);
+  const int rows = gdr::gate_rows(p->T, C);
   if ((rc = launch(gdr::TK_GATE_BWD, stream, "gate gradient launch",
-                   [&](hipStream_t s) { return gdr::launch_gate_bwd(*p, dg, dx, dx_stride, partial, workers, s); })))
+                   [&](hipStream_t s) { return gdr::launch_gate_bwd(*p, dg, dx, dx_stride, partial, s); })))
     return rc;
   if ((rc = launch(gdr::TK_PARAM_SUM, stream, "parameter sum launch",
-                   [&](hipStream_t s) { return gdr::launch_gate_sum(partial, (int)rows, p->H, p->D, da, dbias, s); })))
+                   [&](hipStream_t s) { return gdr::launch_gate_sum(partial, rows, p->H, p->D, da, dbias, s); })))
     return rc;
   return host_status(GDR_OK, "");
 }
@@ -326,7 +327,7 @@ int32_t gdr_gate_fwd(const gdr_gate *p, float *g, void *stream) { return gate_fw
 int64_t gdr_gate_workspace_bytes(int32_t T, int32_t H, int32_t D, int32_t dtype) {
   const int32_t rc = check_gate_sizes(T, H, D, dtype);
   if (rc) return -(int64_t)rc;
-  return round_up(gate_rows(T, H * D, dtype) * 2 * H * D * 4);
+  return gate_bytes(T, H * D, D);
 }
 int32_t gdr_gate_bwd(const gdr_gate *p, const float *dg, void *dx, int64_t dx_stride, float *da_log, float *dbias,
                      void *workspace, int64_t workspace_bytes, void *stream) {

@@ -94,6 +94,23 @@ __device__ __forceinline__ float sigmoid(float x) {
   return __builtin_amdgcn_rcpf(1.f + fast_exp<EXACT>(-x));
 }
 
+// The lane's first channel; the last group of a row whose width is no multiple of
+// VEC starts early and repeats its neighbour's channels (the same values, written
+// twice), so every access is whole.
+template <int VEC>
+__device__ __forceinline__ int first_channel(int group, int C) {
+  return VEC == 1 ? group : min(group * VEC, C - VEC);
+}
+
+// The thread's set within its block.  With UNI a wavefront lies within one set
+// (Lanes::uniform): its rows, their addresses and the document's bounds are then
+// scalar values, and a row's access is one instruction with a scalar base.
+template <bool UNI>
+__device__ __forceinline__ int set_of(int lx) {
+  const int ty = threadIdx.x / lx;
+  return UNI ? __builtin_amdgcn_readfirstlane(ty) : ty;
+}
+
 // Adds a block's LY sets of per-thread sums (LX threads, VEC values each) in set
 // order and stores the LX x VEC results at each first-set thread's `out`.  Every
 // thread of the block calls it; `sums` holds 256 x VEC floats.
