@@ -89,9 +89,12 @@ inline int gate_rows(int64_t T, int C) {
 }
 __host__ __device__ inline int gate_partial_row(int C, int D, int vec) { return C + (D == 1 ? C : C / vec); }
 
-// norm: a worker is a block (see gdr_norm.hip)
+// The norm's backward: a worker is a block (gdr_norm.hip); at least 2048 values or 64
+// rows for each and fewer for wide rows, whose blocks are larger, so that the
+// partial rows stay a small part of the traffic.
 inline int norm_workers(int64_t rows, int D) {
-  return (int)std::min<int64_t>(std::max<int64_t>(rows * D / 4096, rows > 0), 1024);
+  const int64_t n = std::max<int64_t>(rows * D / 2048, (rows + 63) / 64);
+  return (int)std::min<int64_t>(n, std::min(1024, (1 << 22) / D));
 }
 
 hipError_t launch_conv_fwd(const gdr_conv &p, void *y, int64_t y_stride, void *st, hipStream_t stream);

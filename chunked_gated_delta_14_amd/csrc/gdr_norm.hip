@@ -25,51 +25,45 @@ struct NormArgs {
   float alpha, eps;
 };
 
-// VEC values of a row from `p`, of which n are there (the rest read as zeros).
-template <class T, int VEC>
-__device__ __forceinline__ void ld(const T *p, int n, float (&f)[VEC]) {
-  Raw<T, VEC> r;
-  if (n >= VEC) {
-    r.load(p);
+// Threads of a block whose rows take LPR threads each.
+constexpr int row_threads(int lpr) { return lpr <= 128 ? 256 : lpr; }
+
+// A thread's groups of VEC values of a row.  Group i starts at column (i LPR + lane)
+// VEC; the last group of a row whose width is no multiple of VEC, and the groups
+// past it, start at D - VEC, so that every load is whole, and `skip` counts the
+// leading values that belong to a group before (VEC: all of them).
+template <int VEC, int LPR>
+struct Cols {
+  int lane, D;
+  __device__ __forceinline__ int nominal(int i) const { return (i * LPR + lane) * VEC; }
+  __device__ __forceinline__ int at(int i) const { return min(nominal(i), D - VEC); }
+  __device__ __forceinline__ int skip(int i) const { return nominal(i) - at(i); }
+  template <class T>
+  __device__ __forceinline__ void store(T *row, int i, const float (&f)[VEC]) const {
+    const int c = at(i), s = skip(i);
+    if (s == 0) {
+      Raw<T, VEC> r;
+      r.set(f);
+      r.store(row + c);
+    } else {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) f[e] = r.get(e);
-  } else {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      Raw<T, 1> one;
-      one.w[0] = 0;
-      if (e < n) one.load(p + e);
-      f[e] = one.get(0);
+      for (int e = 0; e < VEC; ++e)
+        if (e >= s) {
+          Raw<T, 1> one;
+          const float v[1] = {f[e]};
+          one.set(v);
+          one.store(row + c + e);
+        }
     }
   }
-}
-template <class T, int VEC>
-__device__ __forceinline__ void st(T *p, int n, const float (&f)[VEC]) {
-  if (n >= VEC) {
-    Raw<T, VEC> r;
-    r.set(f);
-    r.store(p);
-  } else {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e)
-      if (e < n) {
-        Raw<T, 1> one;
-        const float v[1] = {f[e]};
-        one.set(v);
-        one.store(p + e);
-      }
-  }
-}
+};
 
-template <int N, int VEC>
-__device__ __forceinline__ void load_weight(const NormArgs &a, int lane, int lpr, float (&w)[N][VEC]) {
+template <int N, int VEC, int LPR>
+__device__ __forceinline__ void load_weight(const NormArgs &a, const Cols<VEC, LPR> &cols, float (&w)[N][VEC]) {
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const int c = (i * lpr + lane) * VEC + e;
-      w[i][e] = c < a.D ? (a.w ? ld_param(a.w, c, a.wbf) : 1.f) : 0.f;
-    }
+    for (int e = 0; e < VEC; ++e) w[i][e] = a.w ? ld_param(a.w, cols.at(i) + e, a.wbf) : 1.f;
 }
 
 // Sum of K values over the LPR threads of a row; every thread of the row gets it.
@@ -93,7 +87,7 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float *lds) {
     for (int k = 0; k < K; ++k) {
       float s = 0.f;
 #pragma unroll
-      for (int j = 0; j < WAVES; ++j) s += lds[j * K + k];
+      for (int j = 0; j < WAVES; ++j) s += lds[((int)threadIdx.x / LPR * WAVES + j) * K + k];
       v[k] = s;
     }
   }
@@ -105,142 +99,159 @@ __device__ __forceinline__ int64_t row_at(int64_t row, int64_t stride, int H, in
   return t * stride + (row - t * H) * D;
 }
 
-template <class T, class R, int PLACE, int VEC, int LPR, int N>
-__global__ __launch_bounds__(LPR > 256 ? LPR : 256) void norm_fwd_kernel(NormArgs a) {
-  constexpr int THREADS = LPR > 256 ? LPR : 256, RPB = THREADS / LPR;
+// The row's values are loaded before any is used, and kept as they lie in memory
+// until then: bf16 rows take half the registers.
+template <class T, class R, int PLACE, bool GATE, int VEC, int LPR, int N>
+__global__ __launch_bounds__(row_threads(LPR)) void norm_fwd_kernel(NormArgs a) {
+  constexpr int THREADS = row_threads(LPR), RPB = THREADS / LPR;
   constexpr bool EXACT = sizeof(T) == 4;
   using Y = std::conditional_t<PLACE == GDR_RES_AFTER, R, T>;
-  __shared__ float lds[16];
-  const int lane = threadIdx.x % LPR, sub = threadIdx.x / LPR;
+  __shared__ float lds[THREADS / 64];
+  const Cols<VEC, LPR> cols{(int)threadIdx.x % LPR, a.D};
+  const int sub = threadIdx.x / LPR;
   float w[N][VEC];
-  load_weight<N, VEC>(a, lane, LPR, w);
+  load_weight<N>(a, cols, w);
   const float inv = 1.f / (float)a.D;
   for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < a.rows; row0 += (int64_t)gridDim.x * RPB) {
     const int64_t row = min(row0 + sub, a.rows - 1);
     const bool mine = row0 + sub < a.rows;
     const T *x = static_cast<const T *>(a.x) + row_at(row, a.xs, a.H, a.D);
-    const T *z = a.z ? static_cast<const T *>(a.z) + row_at(row, a.zs, a.H, a.D) : nullptr;
-    float u[N][VEC], zz[N][VEC], res[PLACE == GDR_RES_NONE ? 1 : N][VEC];
+    const T *z = GATE ? static_cast<const T *>(a.z) + row_at(row, a.zs, a.H, a.D) : nullptr;
+    Raw<T, VEC> rx[N], rz[GATE ? N : 1];
+    Raw<R, VEC> rr[PLACE == GDR_RES_NONE ? 1 : N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int c = (i * LPR + lane) * VEC;
-      ld<T, VEC>(x + c, a.D - c, u[i]);
-      if (z) ld<T, VEC>(z + c, a.D - c, zz[i]);
-      if constexpr (PLACE != GDR_RES_NONE) ld<R, VEC>(static_cast<const R *>(a.res) + row * a.D + c, a.D - c, res[i]);
+      const int c = cols.at(i);
+      rx[i].load(x + c);
+      if constexpr (PLACE != GDR_RES_NONE) rr[i].load(static_cast<const R *>(a.res) + row * a.D + c);
+      if constexpr (GATE) rz[i].load(z + c);
     }
     float q[1] = {0.f};
+    float s[PLACE == GDR_RES_BEFORE ? N : 1][VEC];  // the unrounded stream
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if constexpr (PLACE == GDR_RES_BEFORE) {
-        const int c = (i * LPR + lane) * VEC;
+      const int skip = cols.skip(i);
+      float u[VEC];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) u[i][e] = fmaf(a.alpha, u[i][e], res[i][e]);
-        if (mine) st<R, VEC>(static_cast<R *>(a.s) + row * a.D + c, a.D - c, u[i]);
+      for (int e = 0; e < VEC; ++e) {
+        u[e] = rx[i].get(e);
+        if constexpr (PLACE == GDR_RES_BEFORE) s[i][e] = u[e] = fmaf(a.alpha, u[e], rr[i].get(e));
+        q[0] = fmaf(e >= skip ? u[e] : 0.f, u[e], q[0]);
       }
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) q[0] = fmaf(u[i][e], u[i][e], q[0]);
+      if constexpr (PLACE == GDR_RES_BEFORE) {
+        if (mine) cols.store(static_cast<R *>(a.s) + row * a.D, i, u);
+      }
     }
     row_sum<LPR, 1>(q, lds);
     const float rs = __builtin_amdgcn_rsqf(fmaf(q[0], inv, a.eps));
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int c = (i * LPR + lane) * VEC;
       float y[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        y[e] = u[i][e] * rs * w[i][e];
-        if (z) {
-          const float g = sigmoid<EXACT>(zz[i][e]);
-          y[e] *= a.act == GDR_ACT_SILU ? zz[i][e] * g : g;
+        float u = 0.f;
+        if constexpr (PLACE == GDR_RES_BEFORE) u = s[i][e];
+        else u = rx[i].get(e);
+        y[e] = u * rs * w[i][e];
+        if constexpr (GATE) {
+          const float zz = rz[i].get(e), g = sigmoid<EXACT>(zz);
+          y[e] *= a.act == GDR_ACT_SILU ? zz * g : g;
         }
-        if constexpr (PLACE == GDR_RES_AFTER) y[e] = fmaf(a.alpha, y[e], res[i][e]);
+        if constexpr (PLACE == GDR_RES_AFTER) y[e] = fmaf(a.alpha, y[e], rr[i].get(e));
       }
-      if (mine) st<Y, VEC>(static_cast<Y *>(a.y) + row * a.D + c, a.D - c, y);
+      if (mine) cols.store(static_cast<Y *>(a.y) + row * a.D, i, y);
     }
   }
 }
 
-template <class T, class R, int PLACE, int VEC, int LPR, int N>
-__global__ __launch_bounds__(LPR > 256 ? LPR : 256) void norm_bwd_kernel(NormArgs a) {
-  constexpr int THREADS = LPR > 256 ? LPR : 256, RPB = THREADS / LPR;
+template <class T, class R, int PLACE, bool GATE, int VEC, int LPR, int N>
+__global__ __launch_bounds__(row_threads(LPR)) void norm_bwd_kernel(NormArgs a) {
+  constexpr int THREADS = row_threads(LPR), RPB = THREADS / LPR;
   constexpr bool EXACT = sizeof(T) == 4;
   using U = std::conditional_t<PLACE == GDR_RES_BEFORE, R, T>;  // the normed row as stored
   using Y = std::conditional_t<PLACE == GDR_RES_AFTER, R, T>;
-  __shared__ float lds[32];
-  const int lane = threadIdx.x % LPR, sub = threadIdx.x / LPR;
+  __shared__ float lds[2 * THREADS / 64];
+  const Cols<VEC, LPR> cols{(int)threadIdx.x % LPR, a.D};
+  const int sub = threadIdx.x / LPR;
   float w[N][VEC], dw[N][VEC];
-  load_weight<N, VEC>(a, lane, LPR, w);
+  load_weight<N>(a, cols, w);
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) dw[i][e] = 0.f;
   const float inv = 1.f / (float)a.D, ty = PLACE == GDR_RES_AFTER ? a.alpha : 1.f;
+  const bool silu = a.act == GDR_ACT_SILU;
   for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < a.rows; row0 += (int64_t)gridDim.x * RPB) {
     const int64_t row = min(row0 + sub, a.rows - 1);
     const bool mine = row0 + sub < a.rows;
     const U *x = PLACE == GDR_RES_BEFORE ? static_cast<const U *>(a.s) + row * a.D
                                          : static_cast<const U *>(a.x) + row_at(row, a.xs, a.H, a.D);
-    const T *z = a.z ? static_cast<const T *>(a.z) + row_at(row, a.zs, a.H, a.D) : nullptr;
-    float u[N][VEC], t[N][VEC], zz[N][VEC], ds[PLACE == GDR_RES_BEFORE ? N : 1][VEC];
+    const T *z = GATE ? static_cast<const T *>(a.z) + row_at(row, a.zs, a.H, a.D) : nullptr;
+    Raw<U, VEC> ru[N];
+    Raw<Y, VEC> rt[N];
+    Raw<T, VEC> rz[GATE ? N : 1];
+    Raw<R, VEC> rd[PLACE == GDR_RES_BEFORE ? N : 1];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int c = (i * LPR + lane) * VEC;
-      ld<U, VEC>(x + c, a.D - c, u[i]);
-      ld<Y, VEC>(static_cast<const Y *>(a.dy) + row * a.D + c, a.D - c, t[i]);
-      if (z) ld<T, VEC>(z + c, a.D - c, zz[i]);
+      const int c = cols.at(i);
+      ru[i].load(x + c);
+      rt[i].load(static_cast<const Y *>(a.dy) + row * a.D + c);
+      if constexpr (GATE) rz[i].load(z + c);
       if constexpr (PLACE == GDR_RES_BEFORE) {
-        if (a.ds) {
-          ld<R, VEC>(static_cast<const R *>(a.ds) + row * a.D + c, a.D - c, ds[i]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) ds[i][e] = 0.f;
-        }
+        if (a.ds) rd[i].load(static_cast<const R *>(a.ds) + row * a.D + c);
+        else rd[i].zero();
       }
     }
+    // t act(z) and t act'(z), kept where registers allow and formed again otherwise
+    constexpr bool KEEP = GATE && N == 1;
+    float ta[KEEP ? VEC : 1], tz[KEEP ? VEC : 1];
     float q[2] = {0.f, 0.f};  // sum u^2, sum v u
 #pragma unroll
-    for (int i = 0; i < N; ++i)
+    for (int i = 0; i < N; ++i) {
+      const int skip = cols.skip(i);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        t[i][e] *= ty;
-        q[0] = fmaf(u[i][e], u[i][e], q[0]);
-        float v = t[i][e] * w[i][e];
-        if (z) {
-          const float g = sigmoid<EXACT>(zz[i][e]);
-          const bool silu = a.act == GDR_ACT_SILU;
-          const float act = silu ? zz[i][e] * g : g;
-          // dz without rs, which is not known yet
-          zz[i][e] = v * u[i][e] * (silu ? g * fmaf(zz[i][e], 1.f - g, 1.f) : g * (1.f - g));
-          v *= act;
-          t[i][e] *= act;
+        const float u = ru[i].get(e), um = e >= skip ? u : 0.f;
+        float t = rt[i].get(e) * ty;
+        if constexpr (GATE) {
+          const float zz = rz[i].get(e), g = sigmoid<EXACT>(zz);
+          if constexpr (KEEP) tz[e] = t * (silu ? g * fmaf(zz, 1.f - g, 1.f) : g * (1.f - g));
+          t *= silu ? zz * g : g;
+          if constexpr (KEEP) ta[e] = t;
         }
-        q[1] = fmaf(v, u[i][e], q[1]);
+        q[0] = fmaf(um, u, q[0]);
+        q[1] = fmaf(um, t * w[i][e], q[1]);
       }
+    }
     row_sum<LPR, 2>(q, lds);
     const float rs = __builtin_amdgcn_rsqf(fmaf(q[0], inv, a.eps)), m = q[1] * inv * rs * rs;
+    if (!mine) continue;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int c = (i * LPR + lane) * VEC;
-      float d[VEC];
+      float d[VEC], dz[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        if (mine) dw[i][e] = fmaf(t[i][e], u[i][e] * rs, dw[i][e]);
-        d[e] = rs * fmaf(t[i][e], w[i][e], -u[i][e] * m);
-        if constexpr (PLACE == GDR_RES_BEFORE) d[e] += ds[i][e];
+        const float u = ru[i].get(e), n = u * rs;
+        float t = rt[i].get(e) * ty;
+        if constexpr (KEEP) {
+          dz[e] = tz[e] * w[i][e] * n;
+          t = ta[e];
+        } else if constexpr (GATE) {
+          const float zz = rz[i].get(e), g = sigmoid<EXACT>(zz);
+          dz[e] = t * w[i][e] * n * (silu ? g * fmaf(zz, 1.f - g, 1.f) : g * (1.f - g));
+          t *= silu ? zz * g : g;
+        }
+        dw[i][e] = fmaf(t, n, dw[i][e]);
+        d[e] = rs * fmaf(t, w[i][e], -u * m);
+        if constexpr (PLACE == GDR_RES_BEFORE) d[e] += rd[i].get(e);
       }
-      if (!mine) continue;
       if constexpr (PLACE == GDR_RES_BEFORE) {
-        st<R, VEC>(static_cast<R *>(a.dres) + row * a.D + c, a.D - c, d);
+        cols.store(static_cast<R *>(a.dres) + row * a.D, i, d);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) d[e] *= a.alpha;
       }
-      if (PLACE != GDR_RES_BEFORE || a.dx) st<T, VEC>(static_cast<T *>(a.dx) + row_at(row, a.dxs, a.H, a.D) + c, a.D - c, d);
-      if (z) {
-        float dz[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) dz[e] = zz[i][e] * rs;
-        st<T, VEC>(static_cast<T *>(a.dz) + row_at(row, a.dzs, a.H, a.D) + c, a.D - c, dz);
-      }
+      if (PLACE != GDR_RES_BEFORE || a.dx) cols.store(static_cast<T *>(a.dx) + row_at(row, a.dxs, a.H, a.D), i, d);
+      if constexpr (GATE) cols.store(static_cast<T *>(a.dz) + row_at(row, a.dzs, a.H, a.D), i, dz);
     }
   }
   if (!a.partial) return;
@@ -258,10 +269,9 @@ __global__ __launch_bounds__(LPR > 256 ? LPR : 256) void norm_bwd_kernel(NormArg
       if (sub == 0)
         for (int j = 1; j < RPB; ++j)
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) s[e] += sums[(j * LPR + lane) * VEC + e];
+          for (int e = 0; e < VEC; ++e) s[e] += sums[(j * LPR + cols.lane) * VEC + e];
     }
-    const int c = (i * LPR + lane) * VEC;
-    if (sub == 0) st<float, VEC>(a.partial + (int64_t)blockIdx.x * a.D + c, a.D - c, s);
+    if (sub == 0) cols.store(a.partial + (int64_t)blockIdx.x * a.D, i, s);
   }
 }
 
@@ -276,34 +286,51 @@ NormArgs args_of(const gdr_norm &p) {
   return a;
 }
 
-// Threads per row and groups per thread, the smallest that hold a row of D values.
-template <class T, class R, int PLACE, int VEC, class F>
+// Threads per row and groups per thread, the smallest that hold a row of D values:
+// calls f with the kernels' compile-time values.
+template <class T, class R, int PLACE, bool GATE, int VEC, int LPR, int N>
+struct Shape {
+  using Type = T;
+  using Res = R;
+  static constexpr int place = PLACE, vec = VEC, lpr = LPR, n = N, threads = row_threads(LPR);
+  static constexpr bool gate = GATE;
+};
+template <class T, class R, int PLACE, bool GATE, int VEC, class F>
 hipError_t with_rows(int D, F f) {
+  if (D < VEC) return f(Shape<T, R, PLACE, GATE, 1, 16, 1>());
 #define GDR_ROWS(LPR, N) \
-  if (D <= LPR * N * VEC) return f(T(), R(), std::integral_constant<int, PLACE>(), std::integral_constant<int, VEC>(), \
-                                   std::integral_constant<int, LPR>(), std::integral_constant<int, N>())
+  if (D <= LPR * N * VEC) return f(Shape<T, R, PLACE, GATE, VEC, LPR, N>())
   GDR_ROWS(16, 1);
   GDR_ROWS(32, 1);
   GDR_ROWS(64, 1);
+  GDR_ROWS(128, 1);
+  GDR_ROWS(192, 1);
   GDR_ROWS(256, 1);
   GDR_ROWS(256, 2);
-  GDR_ROWS(256, 4);
+  GDR_ROWS(384, 2);
+  GDR_ROWS(512, 2);
+  GDR_ROWS(640, 2);
+  GDR_ROWS(768, 2);
   GDR_ROWS(1024, 2);
-  GDR_ROWS(1024, 4);
 #undef GDR_ROWS
+  if constexpr (VEC == 4) return f(Shape<T, R, PLACE, GATE, 8, 1024, 2>());  // fp32 rows up to 16384
   return hipErrorInvalidValue;
+}
+template <class T, class R, int PLACE, int VEC, class F>
+hipError_t with_gate(const gdr_norm &p, F f) {
+  return p.gate ? with_rows<T, R, PLACE, true, VEC>(p.D, f) : with_rows<T, R, PLACE, false, VEC>(p.D, f);
 }
 template <class F>
 hipError_t with_types(const gdr_norm &p, F f) {
   const bool b = p.dtype == GDR_BF16, rb = p.res_dtype == GDR_BF16;
   switch (p.placement) {
-    case GDR_RES_NONE: return b ? with_rows<u16, u16, GDR_RES_NONE, 8>(p.D, f) : with_rows<float, float, GDR_RES_NONE, 4>(p.D, f);
+    case GDR_RES_NONE: return b ? with_gate<u16, u16, GDR_RES_NONE, 8>(p, f) : with_gate<float, float, GDR_RES_NONE, 4>(p, f);
     case GDR_RES_BEFORE:
-      return b ? (rb ? with_rows<u16, u16, GDR_RES_BEFORE, 8>(p.D, f) : with_rows<u16, float, GDR_RES_BEFORE, 8>(p.D, f))
-               : with_rows<float, float, GDR_RES_BEFORE, 4>(p.D, f);
+      return b ? (rb ? with_gate<u16, u16, GDR_RES_BEFORE, 8>(p, f) : with_gate<u16, float, GDR_RES_BEFORE, 8>(p, f))
+               : with_gate<float, float, GDR_RES_BEFORE, 4>(p, f);
     default:
-      return b ? (rb ? with_rows<u16, u16, GDR_RES_AFTER, 8>(p.D, f) : with_rows<u16, float, GDR_RES_AFTER, 8>(p.D, f))
-               : with_rows<float, float, GDR_RES_AFTER, 4>(p.D, f);
+      return b ? (rb ? with_gate<u16, u16, GDR_RES_AFTER, 8>(p, f) : with_gate<u16, float, GDR_RES_AFTER, 8>(p, f))
+               : with_gate<float, float, GDR_RES_AFTER, 4>(p, f);
   }
 }
 
@@ -313,11 +340,14 @@ hipError_t launch_norm_fwd(const gdr_norm &p, void *y, hipStream_t stream) {
   if (p.T == 0) return hipSuccess;
   NormArgs a = args_of(p);
   a.y = y;
-  return with_types(p, [&](auto t, auto r, auto place, auto vec, auto lpr, auto n) {
-    constexpr int LPR = decltype(lpr)::value, threads = LPR > 256 ? LPR : 256, rpb = threads / LPR;
-    const int64_t blocks = std::min<int64_t>((a.rows + rpb - 1) / rpb, 8192);
-    norm_fwd_kernel<decltype(t), decltype(r), decltype(place)::value, decltype(vec)::value, LPR, decltype(n)::value>
-        <<<(unsigned)blocks, threads, 0, stream>>>(a);
+  return with_types(p, [&](auto s) {
+    using S = decltype(s);
+    constexpr int rpb = S::threads / S::lpr;
+    // as many blocks as the compute units hold at once, so that a block reads the weight
+    // for many rows ([4182272, 128] 605 us, [4000, 10240] 78 us; 8192 blocks: 639 and 112)
+    const int64_t blocks = std::min<int64_t>((a.rows + rpb - 1) / rpb, 524288 / S::threads);
+    norm_fwd_kernel<typename S::Type, typename S::Res, S::place, S::gate, S::vec, S::lpr, S::n>
+        <<<(unsigned)blocks, S::threads, 0, stream>>>(a);
     return hipGetLastError();
   });
 }
@@ -329,10 +359,10 @@ hipError_t launch_norm_bwd(const gdr_norm &p, const void *dy, const void *ds, vo
   a.dy = dy; a.ds = ds; a.dx = dx; a.dz = dgate; a.dres = dres;
   a.dxs = dx_stride; a.dzs = dgate_stride;
   a.partial = partial;
-  return with_types(p, [&](auto t, auto r, auto place, auto vec, auto lpr, auto n) {
-    constexpr int LPR = decltype(lpr)::value, threads = LPR > 256 ? LPR : 256;
-    norm_bwd_kernel<decltype(t), decltype(r), decltype(place)::value, decltype(vec)::value, LPR, decltype(n)::value>
-        <<<workers, threads, 0, stream>>>(a);
+  return with_types(p, [&](auto s) {
+    using S = decltype(s);
+    norm_bwd_kernel<typename S::Type, typename S::Res, S::place, S::gate, S::vec, S::lpr, S::n>
+        <<<workers, S::threads, 0, stream>>>(a);
     return hipGetLastError();
   });
 }
