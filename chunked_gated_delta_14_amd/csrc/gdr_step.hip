@@ -35,42 +35,56 @@ __device__ __forceinline__ float sum_groups(float x) {  // over the 8 lane group
   return x;
 }
 
-template <bool GDN, bool NORM, bool SIGM>
+// One token's operands for a lane's 16 keys and 4 columns, as they lie in memory.
+template <bool GDN>
+struct Token {
+  Raw<u16, 16> k, q;
+  Raw<u16, 4> v;
+  Raw<float, GDN ? 1 : 16> g;
+  float beta;
+  __device__ __forceinline__ void load(const StepArgs &a, int64_t t, int h, int hq, int key, int col) {
+    k.load(a.k + t * a.ks + hq * HD + key);
+    q.load(a.q + t * a.qs + hq * HD + key);
+    v.load(a.v + t * a.vs + h * HD + col);
+    g.load(a.g + (GDN ? t * a.Hv + h : (t * a.Hv + h) * HD + key));
+    beta = ld_param(a.beta, t * a.Hv + h, !GDN);
+  }
+};
+
+// RUN: sequences given by cu_seqlens; otherwise one token each, whose operands do not
+// wait for the slot.  (Reading a run's next token during the current one takes 177
+// registers, two wavefronts per SIMD instead of three: 16 runs at 64 heads 30 us, not 26.)
+template <bool GDN, bool NORM, bool SIGM, bool RUN>
 __global__ __launch_bounds__(256) void step_kernel(StepArgs a) {
   const int lane = threadIdx.x & 63, rg = lane >> 3, qd = lane & 7;
   const int slice = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = blockIdx.x / a.Hv, h = blockIdx.x - n * a.Hv, hq = h / a.group;
-  int t0 = n, t1 = n + 1;
-  if (a.cu) t0 = max(a.cu[n], 0), t1 = min(a.cu[n + 1], a.T);
   const int slot = a.slots ? a.slots[n] : n;
-  if (t0 >= t1 || slot < 0 || slot >= a.n_slots) return;
-  float *sp = a.state + (((int64_t)slot * a.Hv + h) * HD + 16 * rg) * HD + 32 * slice + 4 * qd;
+  int t0 = n, t1 = n + 1;
+  if constexpr (RUN) {
+    t0 = max(a.cu[n], 0), t1 = min(a.cu[n + 1], a.T);
+    if (t0 >= t1) return;
+  }
+  const int key = 16 * rg, col = 32 * slice + 4 * qd;
+  Token<GDN> x;
+  if constexpr (!RUN) x.load(a, t0, h, hq, key, col);
+  if (slot < 0 || slot >= a.n_slots) return;
+  float *sp = a.state + (((int64_t)slot * a.Hv + h) * HD + key) * HD + col;
   f32x4 S[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) S[j] = *reinterpret_cast<const f32x4 *>(sp + j * HD);
 
   for (int t = t0; t < t1; ++t) {
-    Raw<u16, 16> rk, rq;
-    rk.load(a.k + (int64_t)t * a.ks + hq * HD + 16 * rg);
-    rq.load(a.q + (int64_t)t * a.qs + hq * HD + 16 * rg);
-    Raw<u16, 4> rv;
-    rv.load(a.v + (int64_t)t * a.vs + h * HD + 32 * slice + 4 * qd);
+    if constexpr (RUN) x.load(a, t, h, hq, key, col);
     float dec[GDN ? 1 : 16];
-    if constexpr (GDN) {
-      dec[0] = fast_exp<true>(a.g[(int64_t)t * a.Hv + h]);
-    } else {
-      Raw<float, 16> rd;
-      rd.load(a.g + ((int64_t)t * a.Hv + h) * HD + 16 * rg);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) dec[j] = fast_exp<true>(rd.get(j));
-    }
-    float beta = ld_param(a.beta, (int64_t)t * a.Hv + h, !GDN);
-    if constexpr (SIGM) beta = sigmoid<true>(beta);
+    for (int j = 0; j < (GDN ? 1 : 16); ++j) dec[j] = fast_exp<true>(x.g.get(j));
+    const float beta = SIGM ? sigmoid<true>(x.beta) : x.beta;
 
     float r[4] = {}, p[4] = {}, kq = 0.f, kk = 0.f, qq = 0.f;
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      const float kj = rk.get(j), qj = rq.get(j);
+      const float kj = x.k.get(j), qj = x.q.get(j);
       kq = fmaf(kj, qj, kq);
       if constexpr (NORM) kk = fmaf(kj, kj, kk), qq = fmaf(qj, qj, qq);
 #pragma unroll
@@ -91,18 +105,17 @@ __global__ __launch_bounds__(256) void step_kernel(StepArgs a) {
     float out[4], coef[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float c = beta * (rv.get(e) - nk * r[e]);
-      coef[e] = c * nk;
+      coef[e] = beta * (x.v.get(e) - nk * r[e]) * nk;
       out[e] = a.scale * nq * fmaf(kq, coef[e], p[e]);
     }
 #pragma unroll
     for (int j = 0; j < 16; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) S[j][e] = fmaf(rk.get(j), coef[e], S[j][e]);
+      for (int e = 0; e < 4; ++e) S[j][e] = fmaf(x.k.get(j), coef[e], S[j][e]);
     if (rg == 0) {
       Raw<u16, 4> ro;
       ro.set(out);
-      ro.store(a.o + ((int64_t)t * a.Hv + h) * HD + 32 * slice + 4 * qd);
+      ro.store(a.o + ((int64_t)t * a.Hv + h) * HD + col);
     }
   }
 #pragma unroll
@@ -120,15 +133,18 @@ hipError_t launch_step(bool gdn, const gdr_step &p, uint16_t *o, hipStream_t str
   a.qs = p.q_stride; a.ks = p.k_stride; a.vs = p.v_stride;
   a.scale = p.scale;
   const unsigned blocks = (unsigned)p.N * (unsigned)p.H_v;
-  const bool norm = p.input_flags & GDR_IN_QK_L2NORM, sigm = p.input_flags & GDR_IN_BETA_SIGMOID;
-  auto go = [&](auto g, auto n, auto s) {
-    step_kernel<decltype(g)::value, decltype(n)::value, decltype(s)::value><<<blocks, 256, 0, stream>>>(a);
-    return hipGetLastError();
-  };
   using Y = std::true_type;
   using X = std::false_type;
-  if (gdn) return norm ? (sigm ? go(Y(), Y(), Y()) : go(Y(), Y(), X())) : (sigm ? go(Y(), X(), Y()) : go(Y(), X(), X()));
-  return norm ? (sigm ? go(X(), Y(), Y()) : go(X(), Y(), X())) : (sigm ? go(X(), X(), Y()) : go(X(), X(), X()));
+  auto go = [&](auto g, auto n, auto s) {
+    if (a.cu) step_kernel<decltype(g)::value, decltype(n)::value, decltype(s)::value, true><<<blocks, 256, 0, stream>>>(a);
+    else step_kernel<decltype(g)::value, decltype(n)::value, decltype(s)::value, false><<<blocks, 256, 0, stream>>>(a);
+    return hipGetLastError();
+  };
+  auto flags = [&](auto g) {
+    const bool norm = p.input_flags & GDR_IN_QK_L2NORM, sigm = p.input_flags & GDR_IN_BETA_SIGMOID;
+    return norm ? (sigm ? go(g, Y(), Y()) : go(g, Y(), X())) : (sigm ? go(g, X(), Y()) : go(g, X(), X()));
+  };
+  return gdn ? flags(Y()) : flags(X());
 }
 
 }  // namespace gdr

@@ -123,7 +123,7 @@ def _call(prob, stream, name, *args):
 
     dev = prob.device.index
     if stream is None:
-        stream = torch.cuda.current_stream(dev).cuda_stream
+        stream = torch._C._cuda_getCurrentRawStream(dev)  # what current_stream(dev).cuda_stream reads, without the object
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
     fn = getattr(lib(), name)
