@@ -334,11 +334,21 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int R, int nw
       }
     }
   }
-  __shared__ float sums[256 * VEC];
+  __shared__ float lds[(W + 1) * VEC * 256];
+  float v[(W + 1) * VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i * VEC + e] = dw[i][e];
+    v[W * VEC + e] = db[e];
+  }
+  add_sets<(W + 1) * VEC>(v, lds, tx, ty, a.lx, a.ly);
+  if (!live || ty != 0) return;
   float *p = partial + (int64_t)wb * (W + 1) * a.C + c;
 #pragma unroll
-  for (int i = 0; i < W; ++i) block_partial<VEC>(dw[i], sums, tx, ty, a.lx, a.ly, live, p + (int64_t)i * a.C);
-  block_partial<VEC>(db, sums, tx, ty, a.lx, a.ly, live, p + (int64_t)W * a.C);
+  for (int i = 0; i <= W; ++i)
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) p[(int64_t)i * a.C + e] = v[i * VEC + e];
 }
 
 // One token per sequence: the W-1 rows of the sequence's slot and the new row give

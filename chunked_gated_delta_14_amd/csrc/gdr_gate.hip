@@ -161,18 +161,20 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateArgs p, int workers, 
     d += U * gstep;
     out += U * ostep;
   }
-  __shared__ float sums[256 * VEC];
-  const int per_row = gate_partial_row(p.C, p.D, VEC);
-  float *q = partial + (int64_t)(blockIdx.x / p.nchb) * per_row;
-  block_partial<VEC>(sb, sums, tx, ty, p.lx, p.ly, live, q + c);
-  if (p.D == 1) {
-    block_partial<VEC>(sa, sums, tx, ty, p.lx, p.ly, live, q + p.C + c);
-  } else {
-    float s[1] = {0.f};
+  __shared__ float lds[2 * VEC * 256];
+  float v[2 * VEC], s = 0.f;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) s[0] += sa[e];
-    block_partial<1>(s, sums, tx, ty, p.lx, p.ly, live, q + p.C + c / VEC);
+  for (int e = 0; e < VEC; ++e) v[e] = sb[e], v[VEC + e] = sa[e], s += sa[e];
+  if (p.D != 1) v[VEC] = s;  // one term per thread
+  add_sets<2 * VEC>(v, lds, tx, ty, p.lx, p.ly);
+  if (!live || ty != 0) return;
+  float *q = partial + (int64_t)(blockIdx.x / p.nchb) * gate_partial_row(p.C, p.D, VEC);
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    q[c + e] = v[e];
+    if (p.D == 1) q[p.C + c + e] = v[VEC + e];
   }
+  if (p.D != 1) q[p.C + c / VEC] = v[VEC];
 }
 
 GateArgs args_of(const gdr_gate &p, const Lanes &l) {

@@ -255,23 +255,14 @@ __global__ __launch_bounds__(row_threads(LPR)) void norm_bwd_kernel(NormArgs a) 
     }
   }
   if (!a.partial) return;
-  __shared__ float sums[RPB > 1 ? 256 * VEC : 1];
+  __shared__ float sums[RPB > 1 ? THREADS * VEC * N : 1];
+  if constexpr (RPB > 1) {
+    static_assert(N == 1, "rows shared by a block have one group per thread");
+    add_sets<VEC>(dw[0], sums, cols.lane, sub, LPR, RPB);
+  }
+  if (sub == 0) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    float s[VEC];
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) s[e] = dw[i][e];
-    if constexpr (RPB > 1) {
-      __syncthreads();
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) sums[threadIdx.x * VEC + e] = s[e];
-      __syncthreads();
-      if (sub == 0)
-        for (int j = 1; j < RPB; ++j)
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) s[e] += sums[(j * LPR + cols.lane) * VEC + e];
-    }
-    if (sub == 0) cols.store(a.partial + (int64_t)blockIdx.x * a.D, i, s);
+    for (int i = 0; i < N; ++i) cols.store(a.partial + (int64_t)blockIdx.x * a.D, i, dw[i]);
   }
 }
 

@@ -111,28 +111,25 @@ __device__ __forceinline__ int set_of(int lx) {
   return UNI ? __builtin_amdgcn_readfirstlane(ty) : ty;
 }
 
-// Adds a block's LY sets of per-thread sums (LX threads, VEC values each) in set
-// order and stores the LX x VEC results at each first-set thread's `out`.  Every
-// thread of the block calls it; `sums` holds 256 x VEC floats.
-template <int VEC>
-__device__ __forceinline__ void block_partial(const float (&v)[VEC], float *sums, int tx, int ty, int lx, int ly, bool live,
-                                              float *__restrict__ out) {
-  float s[VEC];
+// Adds a block's `ly` sets of K sums per thread (a set is lx threads wide) in a
+// fixed tree, halving the sets; the sums of set 0's threads are the block's.  Every
+// thread of the block calls it; `lds` holds K x (threads of the block) floats.
+template <int K>
+__device__ __forceinline__ void add_sets(float (&v)[K], float *lds, int tx, int ty, int lx, int ly) {
+  const int threads = blockDim.x;
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) s[e] = v[e];
-  if (ly > 1) {
-    __syncthreads();  // the sums of an earlier call have been read
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) sums[threadIdx.x * VEC + e] = s[e];
+  for (int k = 0; k < K; ++k) lds[k * threads + threadIdx.x] = v[k];
+  for (int n = ly; n > 1;) {
+    const int h = (n + 1) / 2;
     __syncthreads();
-    if (ty == 0)
-      for (int j = 1; j < ly; ++j)
+    if (ty + h < n) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) s[e] += sums[(j * lx + tx) * VEC + e];
-  }
-  if (live && ty == 0) {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) out[e] = s[e];
+      for (int k = 0; k < K; ++k) {
+        v[k] += lds[k * threads + (ty + h) * lx + tx];
+        lds[k * threads + threadIdx.x] = v[k];
+      }
+    }
+    n = h;
   }
 }
 
