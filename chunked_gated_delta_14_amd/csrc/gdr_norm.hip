@@ -112,19 +112,34 @@ __global__ __launch_bounds__(row_threads(LPR)) void norm_fwd_kernel(NormArgs a) 
   float w[N][VEC];
   load_weight<N>(a, cols, w);
   const float inv = 1.f / (float)a.D;
-  for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < a.rows; row0 += (int64_t)gridDim.x * RPB) {
+  struct Row {
+    Raw<T, VEC> x[N], z[GATE ? N : 1];
+    Raw<R, VEC> res[PLACE == GDR_RES_NONE ? 1 : N];
+  };
+  auto fetch = [&](int64_t row0, Row &r) {
     const int64_t row = min(row0 + sub, a.rows - 1);
-    const bool mine = row0 + sub < a.rows;
     const T *x = static_cast<const T *>(a.x) + row_at(row, a.xs, a.H, a.D);
     const T *z = GATE ? static_cast<const T *>(a.z) + row_at(row, a.zs, a.H, a.D) : nullptr;
-    Raw<T, VEC> rx[N], rz[GATE ? N : 1];
-    Raw<R, VEC> rr[PLACE == GDR_RES_NONE ? 1 : N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int c = cols.at(i);
-      rx[i].load(x + c);
-      if constexpr (PLACE != GDR_RES_NONE) rr[i].load(static_cast<const R *>(a.res) + row * a.D + c);
-      if constexpr (GATE) rz[i].load(z + c);
+      r.x[i].load(x + c);
+      if constexpr (PLACE != GDR_RES_NONE) r.res[i].load(static_cast<const R *>(a.res) + row * a.D + c);
+      if constexpr (GATE) r.z[i].load(z + c);
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  constexpr bool AHEAD = LPR > 64;  // the next row is in flight while this one's sums cross the wavefronts
+  Row r, ahead;
+  if constexpr (AHEAD) fetch((int64_t)blockIdx.x * RPB, ahead);
+  for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < a.rows; row0 += step) {
+    const int64_t row = row0 + sub;
+    const bool mine = row < a.rows;
+    if constexpr (AHEAD) {
+      r = ahead;
+      if (row0 + step < a.rows) fetch(row0 + step, ahead);
+    } else {
+      fetch(row0, r);
     }
     float q[1] = {0.f};
     float s[PLACE == GDR_RES_BEFORE ? N : 1][VEC];  // the unrounded stream
@@ -134,8 +149,8 @@ __global__ __launch_bounds__(row_threads(LPR)) void norm_fwd_kernel(NormArgs a) 
       float u[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        u[e] = rx[i].get(e);
-        if constexpr (PLACE == GDR_RES_BEFORE) s[i][e] = u[e] = fmaf(a.alpha, u[e], rr[i].get(e));
+        u[e] = r.x[i].get(e);
+        if constexpr (PLACE == GDR_RES_BEFORE) s[i][e] = u[e] = fmaf(a.alpha, u[e], r.res[i].get(e));
         q[0] = fmaf(e >= skip ? u[e] : 0.f, u[e], q[0]);
       }
       if constexpr (PLACE == GDR_RES_BEFORE) {
@@ -151,13 +166,13 @@ __global__ __launch_bounds__(row_threads(LPR)) void norm_fwd_kernel(NormArgs a) 
       for (int e = 0; e < VEC; ++e) {
         float u = 0.f;
         if constexpr (PLACE == GDR_RES_BEFORE) u = s[i][e];
-        else u = rx[i].get(e);
+        else u = r.x[i].get(e);
         y[e] = u * rs * w[i][e];
         if constexpr (GATE) {
-          const float zz = rz[i].get(e), g = sigmoid<EXACT>(zz);
+          const float zz = r.z[i].get(e), g = sigmoid<EXACT>(zz);
           y[e] *= a.act == GDR_ACT_SILU ? zz * g : g;
         }
-        if constexpr (PLACE == GDR_RES_AFTER) y[e] = fmaf(a.alpha, y[e], rr[i].get(e));
+        if constexpr (PLACE == GDR_RES_AFTER) y[e] = fmaf(a.alpha, y[e], r.res[i].get(e));
       }
       if (mine) cols.store(static_cast<Y *>(a.y) + row * a.D, i, y);
     }
@@ -181,26 +196,41 @@ __global__ __launch_bounds__(row_threads(LPR)) void norm_bwd_kernel(NormArgs a) 
     for (int e = 0; e < VEC; ++e) dw[i][e] = 0.f;
   const float inv = 1.f / (float)a.D, ty = PLACE == GDR_RES_AFTER ? a.alpha : 1.f;
   const bool silu = a.act == GDR_ACT_SILU;
-  for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < a.rows; row0 += (int64_t)gridDim.x * RPB) {
+  struct Row {
+    Raw<U, VEC> u[N];
+    Raw<Y, VEC> t[N];
+    Raw<T, VEC> z[GATE ? N : 1];
+    Raw<R, VEC> d[PLACE == GDR_RES_BEFORE ? N : 1];
+  };
+  auto fetch = [&](int64_t row0, Row &r) {
     const int64_t row = min(row0 + sub, a.rows - 1);
-    const bool mine = row0 + sub < a.rows;
     const U *x = PLACE == GDR_RES_BEFORE ? static_cast<const U *>(a.s) + row * a.D
                                          : static_cast<const U *>(a.x) + row_at(row, a.xs, a.H, a.D);
     const T *z = GATE ? static_cast<const T *>(a.z) + row_at(row, a.zs, a.H, a.D) : nullptr;
-    Raw<U, VEC> ru[N];
-    Raw<Y, VEC> rt[N];
-    Raw<T, VEC> rz[GATE ? N : 1];
-    Raw<R, VEC> rd[PLACE == GDR_RES_BEFORE ? N : 1];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int c = cols.at(i);
-      ru[i].load(x + c);
-      rt[i].load(static_cast<const Y *>(a.dy) + row * a.D + c);
-      if constexpr (GATE) rz[i].load(z + c);
+      r.u[i].load(x + c);
+      r.t[i].load(static_cast<const Y *>(a.dy) + row * a.D + c);
+      if constexpr (GATE) r.z[i].load(z + c);
       if constexpr (PLACE == GDR_RES_BEFORE) {
-        if (a.ds) rd[i].load(static_cast<const R *>(a.ds) + row * a.D + c);
-        else rd[i].zero();
+        if (a.ds) r.d[i].load(static_cast<const R *>(a.ds) + row * a.D + c);
+        else r.d[i].zero();
       }
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  constexpr bool AHEAD = LPR > 64;  // as in the forward
+  Row r, ahead;
+  if constexpr (AHEAD) fetch((int64_t)blockIdx.x * RPB, ahead);
+  for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < a.rows; row0 += step) {
+    const int64_t row = row0 + sub;
+    const bool mine = row < a.rows;
+    if constexpr (AHEAD) {
+      r = ahead;
+      if (row0 + step < a.rows) fetch(row0 + step, ahead);
+    } else {
+      fetch(row0, r);
     }
     // t act(z) and t act'(z), kept where registers allow and formed again otherwise
     constexpr bool KEEP = GATE && N == 1;
@@ -211,10 +241,10 @@ __global__ __launch_bounds__(row_threads(LPR)) void norm_bwd_kernel(NormArgs a) 
       const int skip = cols.skip(i);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const float u = ru[i].get(e), um = e >= skip ? u : 0.f;
-        float t = rt[i].get(e) * ty;
+        const float u = r.u[i].get(e), um = e >= skip ? u : 0.f;
+        float t = r.t[i].get(e) * ty;
         if constexpr (GATE) {
-          const float zz = rz[i].get(e), g = sigmoid<EXACT>(zz);
+          const float zz = r.z[i].get(e), g = sigmoid<EXACT>(zz);
           if constexpr (KEEP) tz[e] = t * (silu ? g * fmaf(zz, 1.f - g, 1.f) : g * (1.f - g));
           t *= silu ? zz * g : g;
           if constexpr (KEEP) ta[e] = t;
@@ -231,19 +261,19 @@ __global__ __launch_bounds__(row_threads(LPR)) void norm_bwd_kernel(NormArgs a) 
       float d[VEC], dz[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const float u = ru[i].get(e), n = u * rs;
-        float t = rt[i].get(e) * ty;
+        const float u = r.u[i].get(e), n = u * rs;
+        float t = r.t[i].get(e) * ty;
         if constexpr (KEEP) {
           dz[e] = tz[e] * w[i][e] * n;
           t = ta[e];
         } else if constexpr (GATE) {
-          const float zz = rz[i].get(e), g = sigmoid<EXACT>(zz);
+          const float zz = r.z[i].get(e), g = sigmoid<EXACT>(zz);
           dz[e] = t * w[i][e] * n * (silu ? g * fmaf(zz, 1.f - g, 1.f) : g * (1.f - g));
           t *= silu ? zz * g : g;
         }
         dw[i][e] = fmaf(t, n, dw[i][e]);
         d[e] = rs * fmaf(t, w[i][e], -u * m);
-        if constexpr (PLACE == GDR_RES_BEFORE) d[e] += rd[i].get(e);
+        if constexpr (PLACE == GDR_RES_BEFORE) d[e] += r.d[i].get(e);
       }
       if constexpr (PLACE == GDR_RES_BEFORE) {
         cols.store(static_cast<R *>(a.dres) + row * a.D, i, d);
@@ -334,9 +364,10 @@ hipError_t launch_norm_fwd(const gdr_norm &p, void *y, hipStream_t stream) {
   return with_types(p, [&](auto s) {
     using S = decltype(s);
     constexpr int rpb = S::threads / S::lpr;
-    // as many blocks as the compute units hold at once, so that a block reads the weight
-    // for many rows ([4182272, 128] 605 us, [4000, 10240] 78 us; 8192 blocks: 639 and 112)
-    const int64_t blocks = std::min<int64_t>((a.rows + rpb - 1) / rpb, 524288 / S::threads);
+    // half of the threads that the compute units hold, each block taking many rows: the
+    // weight is read seldom and the rows in flight lie close together.  [4182272, 128]
+    // 564 us, with twice the blocks 573-684, with half of them 843; [4000, 10240] 68, 74, 63.
+    const int64_t blocks = std::min<int64_t>((a.rows + rpb - 1) / rpb, 262144 / S::threads);
     norm_fwd_kernel<typename S::Type, typename S::Res, S::place, S::gate, S::vec, S::lpr, S::n>
         <<<(unsigned)blocks, S::threads, 0, stream>>>(a);
     return hipGetLastError();
