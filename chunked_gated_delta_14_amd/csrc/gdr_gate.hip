@@ -219,7 +219,7 @@ hipError_t launch_gate_fwd(const gdr_gate &p, float *g, hipStream_t stream) {
   const int C = p.H * p.D;
   const int vec = fwd_vec(C, p.dtype);
   const Lanes l = lanes_for(groups_of(C, vec));
-  const int workers = workers_for((p.T + U - 1) / U, l, 1 << 21);
+  const int workers = workers_for(((int64_t)p.T + U - 1) / U, l, 1 << 21);
   const GateArgs a = args_of(p, l);
   const unsigned blocks = (unsigned)(workers / l.ly * l.nchb);
   return with_types<4>(p, vec, l.uniform, [&](auto t, auto v, auto k, auto u) {

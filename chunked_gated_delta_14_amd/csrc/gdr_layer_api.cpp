@@ -65,6 +65,7 @@ int32_t check_conv(const gdr_conv *p, bool step) {
   const int64_t least = ((int64_t)p->T + 63) / 64;
   if (p->n_chunks < 0 || p->n_chunks > p->T || p->n_chunks < least || p->n_chunks > least + p->N)
     return invalid("n_chunks is inconsistent with T and N");
+  if (p->n_chunks >= (1 << 28)) return unsupported("2^28 chunks or more");  // runs of 8 tokens are counted with 32 bits
   if (p->T > 0 && p->N == 0) return invalid("tokens without documents");
   if (p->N > 0 && !p->chunk_table) return invalid("chunk_table must be non-NULL");
   return GDR_OK;
@@ -226,6 +227,7 @@ int32_t check_norm_sizes(int32_t T, int32_t H, int32_t D) {
   if (T < 0) return invalid("T must be >= 0");
   if (H < 1 || D < 1) return invalid("H and D must be positive");
   if (D > 16384) return unsupported("D above 16384");
+  if ((int64_t)T * H > (int64_t(1) << 40)) return unsupported("more than 2^40 rows");
   return GDR_OK;
 }
 int32_t check_norm(const gdr_norm *p, bool fwd) {

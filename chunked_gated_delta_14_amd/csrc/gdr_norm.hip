@@ -151,7 +151,7 @@ __global__ __launch_bounds__(row_threads(LPR)) void norm_fwd_kernel(NormArgs a) 
       for (int e = 0; e < VEC; ++e) {
         u[e] = r.x[i].get(e);
         if constexpr (PLACE == GDR_RES_BEFORE) s[i][e] = u[e] = fmaf(a.alpha, u[e], r.res[i].get(e));
-        q[0] = fmaf(e >= skip ? u[e] : 0.f, u[e], q[0]);
+        q[0] = e >= skip ? fmaf(u[e], u[e], q[0]) : q[0];
       }
       if constexpr (PLACE == GDR_RES_BEFORE) {
         if (mine) cols.store(static_cast<R *>(a.s) + row * a.D, i, u);
@@ -241,7 +241,7 @@ __global__ __launch_bounds__(row_threads(LPR)) void norm_bwd_kernel(NormArgs a) 
       const int skip = cols.skip(i);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const float u = r.u[i].get(e), um = e >= skip ? u : 0.f;
+        const float u = r.u[i].get(e);
         float t = r.t[i].get(e) * ty;
         if constexpr (GATE) {
           const float zz = r.z[i].get(e), g = sigmoid<EXACT>(zz);
@@ -249,8 +249,7 @@ __global__ __launch_bounds__(row_threads(LPR)) void norm_bwd_kernel(NormArgs a) 
           t *= silu ? zz * g : g;
           if constexpr (KEEP) ta[e] = t;
         }
-        q[0] = fmaf(um, u, q[0]);
-        q[1] = fmaf(um, t * w[i][e], q[1]);
+        if (e >= skip) q[0] = fmaf(u, u, q[0]), q[1] = fmaf(u, t * w[i][e], q[1]);
       }
     }
     row_sum<LPR, 2>(q, lds);

@@ -87,10 +87,10 @@ def _dtype_code(dtype, name):
 
 def _need(t, name, shape=None, dtype=None, device=None, contiguous=True):
     """Check one tensor argument of a call."""
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         _bad("%s must be %s, not %s" % (name, dtype, t.dtype))
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        _bad("%s must be of shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
+    if shape is not None and t.shape != shape:
+        _bad("%s must be of shape %s, not %s" % (name, shape, tuple(t.shape)))
     if device is not None and t.device != device:
         _bad("%s must be on %s, not %s" % (name, device, t.device))
     if contiguous and not t.is_contiguous():
@@ -101,6 +101,8 @@ def _need(t, name, shape=None, dtype=None, device=None, contiguous=True):
 def _rows(t, name, shape, dtype, device):
     """A tensor of token rows: everything inside a row contiguous, any row stride.  Returns the stride in elements."""
     _need(t, name, shape, dtype, device, contiguous=False)
+    if t.shape[0] > 1 and t.is_contiguous():
+        return t.stride(0) or 1
     inner = 1
     for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
         if size != 1 and stride != inner and t.numel():

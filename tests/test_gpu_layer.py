@@ -73,6 +73,8 @@ CONV = [
     ((2, 2, 2, 191), 3, 8, "f32", "f32", False, False, False, 1),
     ((64, 64), 1028, 6, "f32", "f32", True, True, False, 0),
     ((90, 38), 72, 7, "bf16", "f32", True, True, True, 0),
+    ((9000, 3, 3400), 2048, 4, "bf16", "bf16", True, False, False, 0),  # workers of several 64-token runs
+    ((1500, 700), 512, 4, "bf16", "bf16", True, False, True, 16),
 ]
 
 
@@ -192,6 +194,8 @@ GATE = [
     (9, 13, 1, "sigmoid", "bf16", True, 1),
     (700, 1, 1, "sigmoid", "bf16", True, 0),
     (40, 17, 128, "softplus", "f32", True, 0),
+    (5000, 2, 128, "softplus", "bf16", True, 0),
+    (20000, 3, 1, "softplus", "f32", True, 0),
 ]
 
 
@@ -355,6 +359,15 @@ NORM = [
     (300, 1, 384, "before", "f32", "f32", "none", None, 4),
     (1030, 5, 40, "none", "bf16", "bf16", "silu", "f32", 0),
     (3, 2, 700, "none", "bf16", "bf16", "sigmoid", "f32", 5),
+    (1500, 1, 1200, "before", "bf16", "bf16", "silu", "f32", 0),
+    (20000, 1, 40, "after", "bf16", "f32", "sigmoid", "f32", 0),
+    (5, 1, 3000, "none", "bf16", "bf16", "silu", "f32", 0),
+    (3, 1, 8000, "after", "bf16", "f32", "silu", "f32", 8),
+    (700, 1, 5120, "before", "f32", "f32", "none", "f32", 0),
+    (2, 1, 12000, "before", "bf16", "f32", "sigmoid", "f32", 0),
+    (3, 1, 16001, "before", "bf16", "bf16", "silu", "f32", 1),
+    (2, 1, 8192, "after", "f32", "f32", "silu", "f32", 0),
+    (2, 1, 16383, "before", "f32", "f32", "silu", "bf16", 0),
 ]
 
 
@@ -602,3 +615,167 @@ def test_training_graph_replays():
         torch.cuda.synchronize()
         for k in outs:
             assert torch.equal(got[k], outs[k]), (i, k)
+
+
+# ---- far offsets, values that must not spread, other ways to call ----
+
+
+def test_offsets_past_32_bits():
+    """Rows, states and outputs whose element offsets pass 2^32: the same bits as from compact buffers."""
+    g = gdr()
+    T, stride = 440000, 10000  # 4.4e9 elements
+    wide = torch.zeros(T, stride, dtype=BF, device="cuda")
+    compact = dev(rng(1).standard_normal((T, 136)), BF)
+    x = wide[:, 5:141]
+    x.copy_(compact)
+    docs = (T - 300, 300)
+    w, plan = dev(0.5 * rng(2).standard_normal((136, 4)), BF), g.Plan(cu_of(docs))
+    y, want = nan((T, 136), BF), nan((T, 136), BF)
+    g.conv_fwd(g.ConvProblem(x, w, plan), y)
+    g.conv_fwd(g.ConvProblem(compact, w, plan), want)
+    assert torch.equal(y, want)
+    dx, dwant = wide[:, 200:336], nan((T, 136), BF)
+    dw, dw2 = nan((136, 4), F32), nan((136, 4), F32)
+    p, q = g.ConvProblem(x, w, plan), g.ConvProblem(compact, w, plan)
+    g.conv_bwd(p, y, None, dx, dw, None, None, p.alloc_workspace())
+    g.conv_bwd(q, want, None, dwant, dw2, None, None, q.alloc_workspace())
+    assert torch.equal(dx, dwant) and torch.equal(dw, dw2)
+    a = torch.zeros(1, device="cuda")
+    gates, gwant = nan((T, 128), F32), nan((T, 128), F32)
+    g.gate_fwd(g.GateProblem(x[:, :128], a), gates)
+    g.gate_fwd(g.GateProblem(compact[:, :128].contiguous(), a), gwant)
+    assert torch.equal(gates, gwant)
+    nw = torch.ones(136, device="cuda")
+    g.norm_fwd(g.NormProblem(x, nw), y)
+    g.norm_fwd(g.NormProblem(compact, nw), want)
+    assert torch.equal(y, want)
+    del wide, x, dx, compact, gates, gwant, y, want, dwant, p, q
+    torch.cuda.empty_cache()
+    slots, hv = 5600, 48  # 4.4e9 state elements
+    pool = torch.zeros(slots, hv, 128, 128, device="cuda")
+    qq, k, v, gate, beta, state, _ = step_inputs("gdn", (1, 1), 16, hv, 0, 0, 3)
+    pool[slots - 1], pool[7] = state[0], state[1]
+    at = torch.tensor([slots - 1, 7], dtype=torch.int32, device="cuda")
+    o, want = nan(v.shape, BF), nan(v.shape, BF)
+    g.gdn_step(g.StepProblem(g.GDR_GDN, qq, k, v, gate, beta, pool, None, at), o)
+    g.gdn_step(g.StepProblem(g.GDR_GDN, qq, k, v, gate, beta, state), want)
+    assert torch.equal(o, want) and torch.equal(pool[slots - 1], state[0]) and torch.equal(pool[7], state[1])
+
+
+@pytest.mark.parametrize("C,W", [(130, 4), (40, 8), (5, 2)])
+def test_conv_documents_are_separate(C, W):
+    """NaN and infinities in one document leave its neighbours' outputs and gradients as they were."""
+    g = gdr()
+    docs = (3, 70, 1, 65, 2)
+    x, w, b, h, dy, dst = conv_inputs(docs, C, W, "bf16", "bf16", True, True, 0, 8)
+    plan = g.Plan(cu_of(docs))
+
+    def both():
+        p = g.ConvProblem(x, w, plan, b, h)
+        y, st, dx, ds0 = nan(x.shape, BF), nan(h.shape, BF), nan(x.shape, BF), nan(h.shape, BF)
+        g.conv_fwd(p, y, st)
+        g.conv_bwd(p, dy, dst, dx, nan((C, W), F32), nan((C,), F32), ds0, p.alloc_workspace())
+        return [t.clone() for t in (y, dx, st, ds0)]
+
+    clean = both()
+    x[3:73], dy[3:73], h[1], dst[1] = float("nan"), float("inf"), float("nan"), float("nan")
+    dirty = both()
+    rows = torch.cat([torch.arange(3), torch.arange(73, 141)]).cuda()
+    for a, b2 in zip(clean[:2], dirty[:2]):
+        assert torch.equal(a[rows], b2[rows])
+    for a, b2 in zip(clean[2:], dirty[2:]):
+        assert torch.equal(a[[0, 2, 3, 4]], b2[[0, 2, 3, 4]])
+
+
+def test_norm_infinity_stays_in_its_row():
+    """An infinite value: its row follows the formula (zeros beside a NaN), the other rows and every width are untouched by
+    lanes that read a neighbour's value."""
+    g = gdr()
+    for D in (129, 40, 2050):
+        x = dev(rng(D).standard_normal((9, D)))
+        clean, y = nan((9, D), F32), nan((9, D), F32)
+        g.norm_fwd(g.NormProblem(x, None), clean)
+        x[4, D - 2] = float("inf")
+        g.norm_fwd(g.NormProblem(x, None), y)
+        torch.cuda.synchronize()
+        others = [r for r in range(9) if r != 4]
+        assert torch.equal(y[others], clean[others])
+        row = y[4].tolist()
+        assert row[D - 2] != row[D - 2] and all(v == 0 for i, v in enumerate(row) if i != D - 2)
+
+
+def test_step_extreme_gates_and_nan_padding():
+    """g = -inf clears the state before the write, g = 0 keeps it; NaN operands of a skipped sequence reach nothing."""
+    g = gdr()
+    q, k, v, gate, beta, state, _ = step_inputs("kda", (1, 1, 1), 1, 1, 0, 0, 4)
+    gate[0], gate[1] = -float("inf"), 0.0
+    for t in (q, k, v, gate):
+        t[2] = float("nan")
+    slots = torch.tensor([0, 1, -1], dtype=torch.int32, device="cuda")
+    before = state.clone()
+    o = nan(v.shape, BF)
+    g.kda_step(g.StepProblem(g.GDR_KDA, q, k, v, gate, beta, state, None, slots), o)
+    torch.cuda.synchronize()
+    ro, Eo, rs, Es = ref.step(f64(q[:2]), f64(k[:2]), f64(v[:2]), f64(gate[:2]), f64(beta[:2]), f64(before), (1, 1), [0, 1],
+                              128 ** -0.5, False, False)
+    ref.close(o[:2], ro, Eo, BF, "o")
+    ref.close(state, rs, Es, F32, "state")
+    assert bool(torch.isnan(o[2].float()).all())
+
+
+def test_recurrence_state_feeds_the_step():
+    """ht of the chunked forward, taken as a state pool as it is, continues a sequence; a Problem serves as a convolution's
+    plan; both variants."""
+    g = gdr()
+    for variant, hqk, hv in (("kda", 2, 2), ("gdn", 1, 3)):
+        from chunked_gated_delta_14_amd import workloads
+        from gpu_runner import to_dev
+
+        docs = (65, 3)
+        d = to_dev(workloads.make_inputs(workloads.custom(variant, (66, 4), hqk, hv, True, seed=6)))
+        rows = torch.cat([torch.arange(65), torch.arange(66, 69)]).cuda()
+        last = torch.tensor([65, 69]).cuda()
+        code = g.GDR_KDA if variant == "kda" else g.GDR_GDN
+        names = ("q", "k", "v", "g", "beta")
+        prob = g.Problem(code, *(d[n][rows].contiguous() for n in names), cu_of(docs), d["h0"])
+        o, ht = nan((68, hv, 128), BF), nan((2, hv, 128, 128), F32)
+        (g.kda_fwd if variant == "kda" else g.gdn_fwd)(prob, o, ht, prob.alloc_workspace(0))
+        o1 = nan((2, hv, 128), BF)
+        (g.kda_step if variant == "kda" else g.gdn_step)(
+            g.StepProblem(code, *(d[n][last].contiguous() for n in names), ht), o1)
+        full = g.Problem(code, *(d[n] for n in names), d["cu_seqlens"], d["h0"])
+        ofull, htfull = nan((70, hv, 128), BF), nan((2, hv, 128, 128), F32)
+        (g.kda_fwd if variant == "kda" else g.gdn_fwd)(full, ofull, htfull, full.alloc_workspace(0))
+        torch.cuda.synchronize()
+        for a, b in ((o1, ofull[last]), (ht, htfull)):  # each side within the recurrence's 1e-2
+            rel = np.linalg.norm(f64(a) - f64(b)) / np.linalg.norm(f64(b))
+            assert rel <= 1.5e-2, (variant, rel)
+        x = d["v"].view(70, -1)
+        y, want = nan(x.shape, BF), nan(x.shape, BF)
+        w = dev(rng(1).standard_normal((x.shape[1], 4)), BF)
+        g.conv_fwd(g.ConvProblem(x, w, full), y)
+        g.conv_fwd(g.ConvProblem(x, w, g.Plan(cu_of((66, 4)))), want)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+
+
+def test_gpu_refusals_write_nothing():
+    """Calls that the binding or the library refuses leave their outputs as they were."""
+    g = gdr()
+    x = torch.ones(8, 32, dtype=BF, device="cuda")
+    w = torch.ones(32, 4, dtype=BF, device="cuda")
+    p = g.ConvProblem(x, w, g.Plan([0, 8]))
+    y = nan((8, 32), BF)
+    small = torch.empty(256, dtype=torch.uint8, device="cuda")
+    for call in (lambda: g.conv_fwd(p, y.float()), lambda: g.conv_fwd(p, y[:4]), lambda: g.conv_fwd(p, y.cpu()),
+                 lambda: g.conv_fwd(p, nan((32, 8), BF).t()), lambda: g.conv_bwd(p, x, None, y, nan((32, 4), F32), None, None, small[1:]),
+                 lambda: g.ConvProblem(x, w, g.Plan([0, 7])), lambda: g.ConvProblem(x, w.t(), g.Plan([0, 8])),
+                 lambda: g.ConvProblem(x, w[:, :1], g.Plan([0, 8])) and g.conv_fwd(g.ConvProblem(x, w[:, :1].contiguous(), g.Plan([0, 8])), y),
+                 lambda: g.ConvStep(x, w, torch.ones(4, 3, 32, dtype=BF, device="cuda"), torch.zeros(8, dtype=torch.int64, device="cuda")),
+                 lambda: g.GateProblem(x.half(), torch.ones(32, device="cuda")),
+                 lambda: g.NormProblem(x, None, residual=x), lambda: g.NormProblem(x, None, residual=x, s=x, placement=g.GDR_RES_BEFORE),
+                 lambda: g.gate_fwd(g.GateProblem(x, torch.ones(32, device="cuda"), floor=-9.0), nan((8, 32), F32))):
+        with pytest.raises(g.GdrError):
+            call()
+    torch.cuda.synchronize()
+    assert bool(torch.isnan(y.float()).all())
