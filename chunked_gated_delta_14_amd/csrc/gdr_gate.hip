@@ -205,7 +205,7 @@ hipError_t with_types(const gdr_gate &p, int vec, bool uniform, F f) {
 }
 
 // Channels per thread of the forward.  From bf16, 4: a wavefront's stores then cover
-// whole lines one after the other ([261392, 2048] 646 us, with 8 channels 701 us).
+// whole lines one after the other ([261392, 2048] 625 us, with 8 channels 701 us).
 // From fp32, 8: twice the bytes in flight ([100000, 2048] 324 us, with 4 359 us).
 int fwd_vec(int C, int dtype) {
   const int v = dtype == GDR_BF16 ? 4 : GATE_VEC;
@@ -219,7 +219,8 @@ hipError_t launch_gate_fwd(const gdr_gate &p, float *g, hipStream_t stream) {
   const int C = p.H * p.D;
   const int vec = fwd_vec(C, p.dtype);
   const Lanes l = lanes_for(groups_of(C, vec));
-  const int workers = workers_for(((int64_t)p.T + U - 1) / U, l, 1 << 21);
+  // up to 4M threads: few rows each, no sums to share ([261392, 2048] 625 us; 2M 648, 0.5M 692)
+  const int workers = workers_for(((int64_t)p.T + U - 1) / U, l, 1 << 22);
   const GateArgs a = args_of(p, l);
   const unsigned blocks = (unsigned)(workers / l.ly * l.nchb);
   return with_types<4>(p, vec, l.uniform, [&](auto t, auto v, auto k, auto u) {
