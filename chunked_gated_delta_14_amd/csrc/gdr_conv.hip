@@ -85,13 +85,22 @@ __device__ __forceinline__ void push(float (&win)[D][VEC], const float (&x)[VEC]
   for (int e = 0; e < VEC; ++e) win[D - 1][e] = x[e];
 }
 
+// Blocks are dealt to the 8 XCDs in turn.  Within groups of 64 blocks the order is
+// changed so that 8 neighbours, whose runs read each other's last rows, share an
+// XCD's cache.  Of `total` blocks, those past the last whole group keep their place.
+__device__ __forceinline__ int neighbours_on_one_xcd(int b, int total) {
+  const int in = b & 63;
+  return (b | 63) < total ? (b & ~63) + (in & 7) * 8 + (in >> 3) : b;
+}
+
 // Forward: a thread takes R consecutive tokens of one chunk.  Blocks past the
 // `nrb` row blocks write the final rows st instead, LY documents each.
 template <class T, int VEC, int W, bool SILU, bool UNI, int R>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int nrb, T *__restrict__ y, int64_t ys,
                                                        T *__restrict__ st) {
   const int tx = threadIdx.x % a.lx, ty = set_of<UNI>(a.lx);
-  const int chb = blockIdx.x % a.nchb, rb = blockIdx.x / a.nchb;
+  const int blk = neighbours_on_one_xcd(blockIdx.x, nrb * a.nchb);
+  const int chb = blk % a.nchb, rb = blk / a.nchb;
   const int group = chb * a.lx + tx;
   if (ty >= a.ly || group >= (a.C + VEC - 1) / VEC) return;
   const int c = first_channel<VEC>(group, a.C);
@@ -132,7 +141,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int nrb, T *_
   const T *__restrict__ px = x + (int64_t)start * a.xs;
   T *__restrict__ py = y + (int64_t)start * ys;
   // Whole runs go without a test per row, which keeps their loads and stores in one
-  // stretch ([261392, 2048] 375-380 us, with the tests 399).
+  // stretch ([261392, 2048] 380 us, with the tests 399).
   auto all_rows = [&](auto whole) {
     constexpr bool WHOLE = decltype(whole)::value;
 #pragma unroll
@@ -441,7 +450,10 @@ hipError_t with_types(const gdr_conv &p, int vec, const Lanes &l, F f) {
   return vec == 1 ? with_flags<float, 1>(p, l, f) : with_flags<float, 4>(p, l, f);
 }
 
-constexpr int FWD_RUN = 16;  // tokens per thread of the forward
+// Tokens per thread of the forward: short runs keep the registers few, but each reads
+// W-1 rows again ([261392, 2048] W = 4 361 us with 8, 380 with 16, 394 with 32; [30000,
+// 6144] W = 8 213 us with 16, 267 with 8).
+constexpr int fwd_run(int W) { return W <= 4 ? 8 : 16; }
 
 }  // namespace
 
@@ -449,13 +461,14 @@ hipError_t launch_conv_fwd(const gdr_conv &p, void *y, int64_t y_stride, void *s
   const int vec = vec_of(p.C, p.dtype);
   const Lanes l = lanes_for(groups_of(p.C, vec));
   const ConvArgs a = args_of(p, l);
-  const int64_t runs = (int64_t)p.n_chunks * (64 / FWD_RUN), nrb = (runs + l.ly - 1) / l.ly;
+  const int64_t runs = (int64_t)p.n_chunks * (64 / fwd_run(p.W)), nrb = (runs + l.ly - 1) / l.ly;
   const int64_t blocks = (nrb + (st ? (p.N + l.ly - 1) / l.ly : 0)) * l.nchb;
   if (blocks == 0) return hipSuccess;
   if (blocks >= (int64_t(1) << 31)) return hipErrorInvalidValue;
   return with_types<8>(p, vec, l, [&](auto t, auto v, auto w, auto s, auto u) {
     using T = decltype(t);
-    conv_fwd_kernel<T, decltype(v)::value, decltype(w)::value, decltype(s)::value, decltype(u)::value, FWD_RUN>
+    conv_fwd_kernel<T, decltype(v)::value, decltype(w)::value, decltype(s)::value, decltype(u)::value,
+                    fwd_run(decltype(w)::value)>
         <<<(unsigned)blocks, l.threads, 0, stream>>>(a, (int)nrb, static_cast<T *>(y), y_stride, static_cast<T *>(st));
     return hipGetLastError();
   });
