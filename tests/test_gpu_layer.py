@@ -779,3 +779,80 @@ def test_gpu_refusals_write_nothing():
             call()
     torch.cuda.synchronize()
     assert bool(torch.isnan(y.float()).all())
+
+
+@pytest.mark.parametrize("variant", ["kda", "gdn"])
+def test_training_step_of_a_layer(variant):
+    """A layer's core forwards and backwards through the library (convolution, gate, recurrence with its activations, head
+    norm with gate) against the fp64 references and oracle, chained.
+
+    The reference rounds q, k, v, o and their gradients to bf16 where the library stores them.  What is left is the
+    recurrence's own stated accuracy (1e-2 relative RMS for dq, dk and dv, 2e-2 for dg and dbeta), which reaches the
+    projections' and parameters' gradients through linear maps: twice it is allowed, since an error may align with a
+    map's larger directions better than the gradient does, and half a bf16 step (2^-8) for the last rounding.  dz
+    depends on o alone (1e-2)."""
+    import oracle
+
+    g = gdr()
+    docs, hqk, hv, W = (70, 1, 129), 1, 2, 4
+    if variant == "kda":
+        hqk = hv
+    T, cu = sum(docs), cu_of(docs)
+    cq, cv, D = hqk * 128, hv * 128, 128 if variant == "kda" else 1
+    C = 2 * cq + cv
+    r = rng(12)
+    qkv, w = dev(r.standard_normal((T, C)), BF), dev(0.5 * r.standard_normal((C, W)), BF)
+    graw, a, gb = dev(0.5 * r.standard_normal((T, hv * D)), BF), dev(0.3 * r.standard_normal(hv)), dev(r.standard_normal(hv * D))
+    beta = dev(r.standard_normal((T, hv)), BF if variant == "kda" else F32)
+    z, nw = dev(r.standard_normal((T, hv, 128)), BF), dev(1 + 0.1 * r.standard_normal(128))
+    dy = dev(r.standard_normal((T, hv, 128)), BF)
+    plan = g.Plan(cu)
+    act = nan((T, C), BF)
+    cp = g.ConvProblem(qkv, w, plan)
+    g.conv_fwd(cp, act)
+    cuts = (0, cq, 2 * cq, C)
+    q, k, v = (act[:, i:j].contiguous().view(T, -1, 128) for i, j in zip(cuts, cuts[1:]))
+    gate = nan((T, hv, 128) if D > 1 else (T, hv), F32)
+    gp = g.GateProblem(graw, a, gb, g.GDR_GATE_SIGMOID)
+    g.gate_fwd(gp, gate)
+    prob = g.Problem(g.GDR_KDA if variant == "kda" else g.GDR_GDN, q, k, v, gate, beta, cu,
+                     input_flags=g.GDR_IN_QK_L2NORM | g.GDR_IN_BETA_SIGMOID)
+    ws, o = prob.alloc_workspace(), nan((T, hv, 128), BF)
+    (g.kda_fwd if variant == "kda" else g.gdn_fwd)(prob, o, None, ws, g.GDR_FWD_SAVE)
+    y, npb = nan(o.shape, BF), g.NormProblem(o, nw, z, g.GDR_ACT_SILU)
+    g.norm_fwd(npb, y)
+    do, dz, dnw = nan(o.shape, BF), nan(o.shape, BF), nan((128,), F32)
+    g.norm_bwd(npb, dy, do, dnw, npb.alloc_workspace(), dgate=dz)
+    dq, dk, dv = nan(q.shape, BF), nan(k.shape, BF), nan(v.shape, BF)
+    dg, dbeta = nan(gate.shape, F32), torch.empty_like(beta)
+    (g.kda_bwd if variant == "kda" else g.gdn_bwd)(prob, do, None, dq, dk, dv, dg, dbeta, None, ws)
+    dgraw, da, dgb = nan((T, hv * D), BF), nan((hv,), F32), nan((hv * D,), F32)
+    g.gate_bwd(gp, dg, dgraw, da, dgb, gp.alloc_workspace())
+    dact = torch.cat([dq.view(T, -1), dk.view(T, -1), dv.view(T, -1)], 1)
+    dqkv, dw = nan((T, C), BF), nan((C, W), F32)
+    g.conv_bwd(cp, dact, None, dqkv, dw, None, None, cp.alloc_workspace())
+    torch.cuda.synchronize()
+
+    def bf(x):
+        return torch.from_numpy(np.ascontiguousarray(x)).to(BF).double().numpy()
+
+    f = ref.conv(f64(qkv), f64(w), 0.0 * f64(w)[:, 0], None, docs, True)
+    rq, rk, rv = (bf(f["y"][:, i:j].reshape(T, -1, 128)) for i, j in zip(cuts, cuts[1:]))
+    rg = ref.gate(f64(graw).reshape(T, hv, D), f64(a), f64(gb).reshape(hv, D), "sigmoid", -5.0)[0]
+    rg = rg if D > 1 else rg[..., 0]
+    flags = dict(qk_l2norm=True, beta_sigmoid=True)
+    ro = bf(oracle.forward_act(rq, rk, rv, rg, f64(beta), cu, None, **flags)[0])
+    n = ref.norm_grad(ro, f64(nw), f64(z), f64(dy), None, "none", "silu", 1.0, 1e-6)
+    b = oracle.backward_act(rq, rk, rv, rg, f64(beta), cu, bf(n["dx"]), None, None, **flags)
+    gg = ref.gate_grad(f64(graw).reshape(T, hv, D), f64(a), f64(gb).reshape(hv, D), "sigmoid", -5.0, b["dg"].reshape(T, hv, D))
+    rdact = np.concatenate([bf(b[x]).reshape(T, -1) for x in ("dq", "dk", "dv")], 1)
+    c = ref.conv_grad(f, f64(qkv), f64(w), docs, rdact, None, True)
+    half = 2.0 ** -8
+    for name, got, want, lim in (("y", y, ref.norm(ro, f64(nw), f64(z), None, "none", "silu", 1.0, 1e-6)["y"], 2e-2 + half),
+                                 ("dz", dz, n["dz"], 2e-2 + half), ("dnw", dnw, n["dw"], 2e-2), ("dqkv", dqkv, c["dx"], 2e-2 + half),
+                                 ("dw", dw, c["dw"], 2e-2), ("dgraw", dgraw, gg["dx"].reshape(T, -1), 4e-2 + half), ("da", da, gg["da"], 4e-2),
+                                 ("dgb", dgb, gg["db"].reshape(-1), 4e-2), ("dbeta", dbeta, b["dbeta"], 4e-2 + half)):
+        got = f64(got)
+        rel = np.linalg.norm(got - want) / np.linalg.norm(want)
+        print("[layer] %s %s %.2e" % (variant, name, rel), flush=True)
+        assert rel <= lim, "%s: %.3g" % (name, rel)
