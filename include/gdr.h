@@ -265,8 +265,9 @@ int32_t gdr_kda_ckpt_noalloc(const gdr_problem *p, uint16_t *o, float *ht, const
  * Here rows may also be strided: an `*_stride` is the distance between the rows of
  * two tokens in elements, at least the row's width (so a call can read and write
  * parts of a wider projection buffer); tensors without one are contiguous.  Rows
- * need no alignment beyond their element's.  Values are held, summed and rounded
- * in fp32; an output is rounded once.
+ * need no alignment beyond their element's.  Values are held and summed in fp32;
+ * an output is rounded once.  A backward's workspace and a pool belong to one call
+ * at a time: calls that may overlap, captured graphs among them, need their own.
  * ------------------------------------------------------------------------- */
 enum gdr_dtype { GDR_BF16 = 0, GDR_F32 = 1 };
 enum gdr_activation { GDR_ACT_NONE = 0, GDR_ACT_SILU = 1, GDR_ACT_SIGMOID = 2 };
