@@ -188,12 +188,20 @@ __global__ __launch_bounds__(row_threads(LPR)) void norm_bwd_kernel(NormArgs a) 
   __shared__ float lds[2 * THREADS / 64];
   const Cols<VEC, LPR> cols{(int)threadIdx.x % LPR, a.D};
   const int sub = threadIdx.x / LPR;
-  float w[N][VEC], dw[N][VEC];
+  // The weight gradient's terms: in registers, or, for the widest rows, which need
+  // those for the row itself, in LDS ([3000, 16000] with gate 187 us, from registers 303).
+  constexpr bool LDS_DW = LPR >= 1024;
+  __shared__ float dwl[LDS_DW ? THREADS * VEC * N : 1];
+  float w[N][VEC], dw[LDS_DW ? 1 : N][VEC];
   load_weight<N>(a, cols, w);
+  auto dw_at = [&](int i, int e) -> float & {
+    if constexpr (LDS_DW) return dwl[(i * VEC + e) * THREADS + threadIdx.x];
+    else return dw[i][e];
+  };
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) dw[i][e] = 0.f;
+    for (int e = 0; e < VEC; ++e) dw_at(i, e) = 0.f;
   const float inv = 1.f / (float)a.D, ty = PLACE == GDR_RES_AFTER ? a.alpha : 1.f;
   const bool silu = a.act == GDR_ACT_SILU;
   struct Row {
@@ -220,7 +228,7 @@ __global__ __launch_bounds__(row_threads(LPR)) void norm_bwd_kernel(NormArgs a) 
     }
   };
   const int64_t step = (int64_t)gridDim.x * RPB;
-  constexpr bool AHEAD = LPR > 64;  // as in the forward
+  constexpr bool AHEAD = LPR > 64 && LPR < (GATE ? 640 : 1024);  // as in the forward, where registers allow
   Row r, ahead;
   if constexpr (AHEAD) fetch((int64_t)blockIdx.x * RPB, ahead);
   for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < a.rows; row0 += step) {
@@ -270,7 +278,7 @@ __global__ __launch_bounds__(row_threads(LPR)) void norm_bwd_kernel(NormArgs a) 
           dz[e] = t * w[i][e] * n * (silu ? g * fmaf(zz, 1.f - g, 1.f) : g * (1.f - g));
           t *= silu ? zz * g : g;
         }
-        dw[i][e] = fmaf(t, n, dw[i][e]);
+        dw_at(i, e) = fmaf(t, n, dw_at(i, e));
         d[e] = rs * fmaf(t, w[i][e], -u * m);
         if constexpr (PLACE == GDR_RES_BEFORE) d[e] += r.d[i].get(e);
       }
@@ -291,7 +299,12 @@ __global__ __launch_bounds__(row_threads(LPR)) void norm_bwd_kernel(NormArgs a) 
   }
   if (sub == 0) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) cols.store(a.partial + (int64_t)blockIdx.x * a.D, i, dw[i]);
+    for (int i = 0; i < N; ++i) {
+      float s[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) s[e] = dw_at(i, e);
+      cols.store(a.partial + (int64_t)blockIdx.x * a.D, i, s);
+    }
   }
 }
 
