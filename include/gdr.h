@@ -268,6 +268,7 @@ int32_t gdr_kda_ckpt_noalloc(const gdr_problem *p, uint16_t *o, float *ht, const
  * need no alignment beyond their element's.  Values are held and summed in fp32;
  * an output is rounded once.  A backward's workspace and a pool belong to one call
  * at a time: calls that may overlap, captured graphs among them, need their own.
+ * An output given the address of an input is refused.
  * ------------------------------------------------------------------------- */
 enum gdr_dtype { GDR_BF16 = 0, GDR_F32 = 1 };
 enum gdr_activation { GDR_ACT_NONE = 0, GDR_ACT_SILU = 1, GDR_ACT_SIGMOID = 2 };

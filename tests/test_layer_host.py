@@ -10,6 +10,7 @@ import chunked_gated_delta_14_amd as gdr
 import layer_ref as ref
 from chunked_gated_delta_14_amd import layer
 
+IN, OUT, OUT2 = 1 << 20, 1 << 21, 1 << 22
 PTR = 4096  # never dereferenced: every call below is refused, or stops at the device check
 
 
@@ -57,8 +58,8 @@ BIG = 1 << 40
 ])
 def test_conv_refusals(kw, code, word):
     L, p = gdr.lib(), conv(**kw)
-    refused(L.gdr_conv_fwd(ctypes.byref(p), PTR, 1 << 26, None, None), code, word)
-    refused(L.gdr_conv_bwd(ctypes.byref(p), PTR, 1 << 26, None, PTR, 1 << 26, PTR, None, None, PTR, BIG, None), code, word)
+    refused(L.gdr_conv_fwd(ctypes.byref(p), OUT, 1 << 26, None, None), code, word)
+    refused(L.gdr_conv_bwd(ctypes.byref(p), PTR, 1 << 26, None, OUT, 1 << 26, PTR, None, None, PTR, BIG, None), code, word)
 
 
 def test_conv_call_refusals():
@@ -73,9 +74,9 @@ def test_conv_call_refusals():
     refused(L.gdr_conv_bwd(r, PTR, 16, None, PTR, 16, None, None, None, PTR, need, None), 1, "dweight")
     refused(L.gdr_conv_bwd(r, None, 16, None, PTR, 16, PTR, None, None, PTR, need, None), 1, "dy and dx")
     refused(L.gdr_conv_bwd(r, PTR, 16, None, PTR, 15, PTR, None, None, PTR, need, None), 1, "stride")
-    refused(L.gdr_conv_bwd(r, PTR, 16, None, PTR, 16, PTR, None, None, PTR, need - 1, None), 3, "too small")
-    refused(L.gdr_conv_bwd(r, PTR, 16, None, PTR, 16, PTR, None, None, PTR + 16, need, None), 3, "aligned")
-    refused(L.gdr_conv_bwd(r, PTR, 16, None, PTR, 16, PTR, None, None, None, need, None), 3, "NULL")
+    refused(L.gdr_conv_bwd(r, PTR, 16, None, OUT, 16, PTR, None, None, PTR, need - 1, None), 3, "too small")
+    refused(L.gdr_conv_bwd(r, PTR, 16, None, OUT, 16, PTR, None, None, PTR + 16, need, None), 3, "aligned")
+    refused(L.gdr_conv_bwd(r, PTR, 16, None, OUT, 16, PTR, None, None, None, need, None), 3, "NULL")
     q = conv(T=3, N=3)
     s = ctypes.byref(q)
     refused(L.gdr_conv_step(r, PTR, 16, PTR, PTR, 4, None), 1, "N must equal T")
@@ -107,7 +108,7 @@ def test_gate_call_refusals():
     refused(L.gdr_gate_bwd(r, PTR, PTR, 256, None, None, PTR, need, None), 1, "da_log")
     refused(L.gdr_gate_bwd(r, PTR, None, 256, PTR, None, PTR, need, None), 1, "dg and dx")
     refused(L.gdr_gate_bwd(r, PTR, PTR, 200, PTR, None, PTR, need, None), 1, "dx_stride")
-    refused(L.gdr_gate_bwd(r, PTR, PTR, 256, PTR, None, PTR, need - 256, None), 3, "too small")
+    refused(L.gdr_gate_bwd(r, PTR, OUT, 256, PTR, None, PTR, need - 256, None), 3, "too small")
 
 
 @pytest.mark.parametrize("kw,code,word", [
@@ -154,11 +155,42 @@ def test_norm_call_refusals():
     refused(L.gdr_norm_bwd(r, PTR, None, PTR, 256, None, 256, None, PTR, PTR, need, None), 1, "dgate is NULL")
     refused(L.gdr_norm_bwd(r, PTR, None, None, 256, PTR, 256, None, PTR, PTR, need, None), 1, "dx is NULL")
     refused(L.gdr_norm_bwd(r, PTR, None, PTR, 256, PTR, 255, None, PTR, PTR, need, None), 1, "dgate_stride")
-    refused(L.gdr_norm_bwd(r, PTR, None, PTR, 256, PTR, 256, None, PTR, PTR, need - 256, None), 3, "too small")
+    refused(L.gdr_norm_bwd(r, PTR, None, OUT, 256, OUT2, 256, None, PTR, PTR, need - 256, None), 3, "too small")
     q = norm(gate=None, activation=0)
     refused(L.gdr_norm_bwd(ctypes.byref(q), PTR, None, PTR, 256, PTR, 256, None, PTR, PTR, need, None), 1, "dgate without")
     b = norm(placement=1, x=None, s=PTR)
     refused(L.gdr_norm_bwd(ctypes.byref(b), PTR, None, PTR, 256, PTR, 256, None, PTR, PTR, need, None), 1, "dres is NULL")
+
+
+def test_outputs_that_are_inputs_are_refused():
+    """Each output given the address of one of the call's inputs."""
+    L = gdr.lib()
+    A, B, C, D, E = (IN + 4096 * i for i in range(5))
+    c = ctypes.byref(conv(x=A, s0=B))
+    for y, st in ((A, OUT), (B, OUT), (OUT, A), (OUT, B)):
+        refused(L.gdr_conv_fwd(c, y, 16, st, None), 1, "is an input")
+    ws = 1 << 24
+    for dx, ds0 in ((A, OUT), (B, OUT), (C, OUT), (D, OUT), (OUT, A), (OUT, B), (OUT, C), (OUT, D)):
+        refused(L.gdr_conv_bwd(c, C, 16, D, dx, 16, OUT2, None, ds0, ws, BIG, None), 1, "is an input")
+    s = ctypes.byref(conv(T=3, N=3, x=A))
+    for y, state in ((A, B), (B, B), (OUT, A)):
+        refused(L.gdr_conv_step(s, y, 16, state, None, 3, None), 1, "is an input")
+    g = ctypes.byref(gate(x=A, dtype=1))
+    refused(L.gdr_gate_fwd(g, A, None), 1, "is an input")
+    for dx in (A, B):
+        refused(L.gdr_gate_bwd(g, B, dx, 256, OUT2, None, ws, BIG, None), 1, "is an input")
+    t = ctypes.byref(step(q=A, k=B, v=C, state=D))
+    for o in (A, B, C, D):
+        refused(L.gdr_gdn_step(t, o, None), 1, "is an input")
+    for y, q in ((A, norm(x=A, gate=B)), (B, norm(x=A, gate=B)), (C, norm(x=A, gate=B, placement=2, residual=C)),
+                 (D, norm(x=A, gate=B, placement=1, residual=C, s=D)), (OUT, norm(x=A, gate=B, placement=1, residual=C, s=C))):
+        refused(L.gdr_norm_fwd(ctypes.byref(q), y, None), 1, "is an input")
+    b = ctypes.byref(norm(x=None, gate=B, placement=1, s=D))
+    outs = [OUT, OUT2, OUT2 + 4096]
+    for i in range(3):
+        for bad in (B, C, D, E):
+            dx, dz, dres = (bad if j == i else o for j, o in enumerate(outs))
+            refused(L.gdr_norm_bwd(b, C, E, dx, 256, dz, 256, dres, None, None, 0, None), 1, "is an input")
 
 
 def test_binding_refuses_cpu_tensors_and_bad_shapes():
