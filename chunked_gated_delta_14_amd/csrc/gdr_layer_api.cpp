@@ -310,12 +310,14 @@ int32_t norm_bwd(const gdr_norm *p, const void *dy, const void *ds, void *dx, in
   const int workers = gdr::norm_workers((int64_t)p->T * p->H, p->D);
   if (dw && (rc = check_workspace(ws, ws_bytes, round_up((int64_t)workers * p->D * 4)))) return rc;
   if ((rc = gdr::host_check_device())) return rc;
-  float *partial = dw ? static_cast<float *>(ws) : nullptr;
+  // one worker's partial row is the gradient itself
+  const bool one = workers == 1;
+  float *partial = !dw ? nullptr : one ? dw : static_cast<float *>(ws);
   if ((rc = launch(gdr::TK_NORM_BWD, stream, "norm gradient launch", [&](hipStream_t s) {
          return gdr::launch_norm_bwd(*p, dy, ds, dx, dx_stride, dgate, dgate_stride, dres, partial, workers, s);
        })))
     return rc;
-  if (dw && (rc = launch(gdr::TK_PARAM_SUM, stream, "parameter sum launch",
+  if (dw && !one && (rc = launch(gdr::TK_PARAM_SUM, stream, "parameter sum launch",
                          [&](hipStream_t s) { return gdr::launch_norm_sum(partial, workers, p->D, dw, s); })))
     return rc;
   return host_status(GDR_OK, "");

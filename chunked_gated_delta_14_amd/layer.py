@@ -87,6 +87,8 @@ def _dtype_code(dtype, name):
 
 def _need(t, name, shape=None, dtype=None, device=None, contiguous=True):
     """Check one tensor argument of a call."""
+    if t.shape == shape and t.dtype is dtype and t.device == device and (not contiguous or t.is_contiguous()):
+        return t
     if dtype is not None and t.dtype is not dtype:
         _bad("%s must be %s, not %s" % (name, dtype, t.dtype))
     if shape is not None and t.shape != shape:
