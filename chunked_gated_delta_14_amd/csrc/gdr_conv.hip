@@ -7,6 +7,12 @@
 //   dX[s] = sum_{i<W} w[c,i] dz[s+(W-1)-i] (+ dst on the last W-1 rows of X)
 //   dw[c,i] = sum_t dz[t] X[t-(W-1)+i],   db = sum_t dz[t]
 // dX before the document's first row is ds0.
+//
+// Bound by HBM: about 17 (forward) and 34 (backward) lane operations a value against
+// 4 and 6 bytes leave the vector units 0.65 and 0.7 busy.  W = 4, SiLU, bf16, on a card
+// that copies 5.5 TB/s: forward [261392, 2048] 357 us, 6.0 TB/s; backward [241817,
+// 6144] 1771 us, 5.1 TB/s.  Nothing is kept for the backward, since z costs less to
+// form again than to read.
 #include "gdr_layer.h"
 #include "gdr_vec.h"
 
@@ -366,7 +372,8 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int R, int nw
     for (int e = 0; e < VEC; ++e) p[(int64_t)i * a.C + e] = v[i * VEC + e];
 }
 
-// One token per sequence: the W-1 rows of the sequence's slot and the new row give
+// One token per sequence ([64, 10240] 4.5 us, the latency of slot, state and store):
+// the W-1 rows of the sequence's slot and the new row give
 // y; the slot keeps the last W-1 rows.  Rows whose slot lies outside the pool are
 // left alone.
 template <class T, int VEC, int W, bool SILU>

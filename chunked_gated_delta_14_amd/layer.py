@@ -8,7 +8,8 @@ checked) once and used for any number of calls on those tensors, so the calls of
 a training step or a serving loop cost one C call each.  A tensor that does not
 fit raises GdrError with GDR_ERR_INVALID_ARG before anything is enqueued.  Calls
 run on the device of the problem's tensors, on `stream` or that device's current
-stream.
+stream; keeping a tensor that was allocated on another stream is the caller's part
+(`Tensor.record_stream`), as in the rest of the binding.
 """
 from __future__ import annotations
 
@@ -102,9 +103,9 @@ def _need(t, name, shape=None, dtype=None, device=None, contiguous=True):
 
 def _rows(t, name, shape, dtype, device):
     """A tensor of token rows: everything inside a row contiguous, any row stride.  Returns the stride in elements."""
-    _need(t, name, shape, dtype, device, contiguous=False)
-    if t.shape[0] > 1 and t.is_contiguous():
+    if t.shape == shape and t.dtype is dtype and t.device == device and shape[0] > 1 and t.is_contiguous():
         return t.stride(0) or 1
+    _need(t, name, shape, dtype, device, contiguous=False)
     inner = 1
     for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
         if size != 1 and stride != inner and t.numel():
