@@ -92,15 +92,15 @@ inline int gate_rows(int64_t T, int C) {
 }
 __host__ __device__ inline int gate_partial_row(int C, int D, int vec) { return C + (D == 1 ? C : C / vec); }
 
-// The norm's backward: a worker is a block (gdr_norm.hip); at least 2048 values or 64
-// rows for each and fewer for wide rows, whose blocks are larger, so that the
-// partial rows stay a small part of the traffic.  Long streams take half as many:
-// the rows in flight then lie closer together in memory ([4182272, 128] 915 us with
-// 512 blocks, 961 with 1024; [10000, 1500], which they leave idle, 46 and 35 us).
+// The norm's backward: a worker is a block (gdr_norm.hip).  At most this many, by
+// which the workspace is sized: at least 2048 values or 64 rows for each and fewer
+// for wide rows, whose blocks are larger, so that the partial rows stay a small part
+// of the traffic.  The launch takes norm_bwd_workers of them.
 inline int norm_workers(int64_t rows, int D) {
   const int64_t n = std::max<int64_t>(rows * D / 2048, (rows + 63) / 64);
-  return (int)std::min<int64_t>(n, std::min(rows * D >= (1 << 26) ? 512 : 1024, (1 << 22) / D));
+  return (int)std::min<int64_t>(n, std::min(1024, (1 << 22) / D));
 }
+int norm_bwd_workers(const gdr_norm &p);
 
 hipError_t launch_conv_fwd(const gdr_conv &p, void *y, int64_t y_stride, void *st, hipStream_t stream);
 hipError_t launch_conv_bwd(const gdr_conv &p, const void *dy, int64_t dy_stride, const void *dst, void *dx,

@@ -307,9 +307,10 @@ int32_t norm_bwd(const gdr_norm *p, const void *dy, const void *ds, void *dx, in
   const void *u = before ? p->s : p->x;  // the normed row
   if (aliases(dx, u, p->gate, dy, ds) || aliases(dgate, u, p->gate, dy, ds) || aliases(dres, u, p->gate, dy, ds))
     return invalid("dx, dgate or dres is an input");
-  const int workers = gdr::norm_workers((int64_t)p->T * p->H, p->D);
-  if (dw && (rc = check_workspace(ws, ws_bytes, round_up((int64_t)workers * p->D * 4)))) return rc;
+  const int most = gdr::norm_workers((int64_t)p->T * p->H, p->D);
+  if (dw && (rc = check_workspace(ws, ws_bytes, round_up((int64_t)most * p->D * 4)))) return rc;
   if ((rc = gdr::host_check_device())) return rc;
+  const int workers = gdr::norm_bwd_workers(*p);
   // one worker's partial row is the gradient itself
   const bool one = workers == 1;
   float *partial = !dw ? nullptr : one ? dw : static_cast<float *>(ws);

@@ -371,21 +371,58 @@ hipError_t with_types(const gdr_norm &p, F f) {
 
 }  // namespace
 
+namespace {
+// Blocks for `rows` rows of D values, `each` bytes of input to a value: whole rounds
+// of the 256 compute units, as few as keep `want` bytes in flight, so that the rows in
+// flight lie close together and the weight is read seldom.  Measured on both sides:
+//   rows that span wavefronts, whose next row is in flight too, 4 MB: [32674, 2048]
+//   backward with an fp32 stream 184 us with one round, 200 with two, 209 with one and
+//   a half; [40000, 2048] bf16 147 with two, 165 with four;
+//   rows within a wavefront, 10 MB forward and 6 MB backward: heads [4182272, 128]
+//   forward 595 us with four or five rounds, 670 with three, 843 with two; backward
+//   985 with two, 1083 with four;
+//   rows that leave lanes idle or start off a 128-byte line take longer to arrive,
+//   9 MB: [40000, 1500] backward 133 us with four or more rounds, 158 with two;
+//   [40000, 2049] 360 with two, 473 with one; [400000, 200] 160 with four, 182 with three.
+constexpr int64_t AHEAD_BYTES = 4000000, FWD_BYTES = 10000000, BWD_BYTES = 6000000, ODD_BYTES = 9000000;
+template <class S>
+int64_t blocks_for(int64_t rows, int D, int each, int64_t want) {
+  constexpr int rpb = S::threads / S::lpr;
+  if (D != S::lpr * S::n * S::vec) want = ODD_BYTES;
+  else if (S::lpr > 64) want = AHEAD_BYTES;
+  const int64_t round = (int64_t)256 * rpb * D * each;
+  return std::min<int64_t>((rows + rpb - 1) / rpb, 256 * std::min<int64_t>((want + round - 1) / round, 8));
+}
+}  // namespace
+
 hipError_t launch_norm_fwd(const gdr_norm &p, void *y, hipStream_t stream) {
   if (p.T == 0) return hipSuccess;
   NormArgs a = args_of(p);
   a.y = y;
   return with_types(p, [&](auto s) {
     using S = decltype(s);
-    constexpr int rpb = S::threads / S::lpr;
-    // half of the threads that the compute units hold, each block taking many rows: the
-    // weight is read seldom and the rows in flight lie close together.  [4182272, 128]
-    // 564 us, with twice the blocks 573-684, with half of them 843; [4000, 10240] 68, 74, 63.
-    const int64_t blocks = std::min<int64_t>((a.rows + rpb - 1) / rpb, 262144 / S::threads);
+    constexpr int each = (S::gate ? 2 : 1) * sizeof(typename S::Type) + (S::place == GDR_RES_NONE ? 0 : sizeof(typename S::Res));
+    const int64_t blocks = blocks_for<S>(a.rows, a.D, each, FWD_BYTES);
     norm_fwd_kernel<typename S::Type, typename S::Res, S::place, S::gate, S::vec, S::lpr, S::n>
         <<<(unsigned)blocks, S::threads, 0, stream>>>(a);
     return hipGetLastError();
   });
+}
+
+int norm_bwd_workers(const gdr_norm &p) {
+  if (p.T == 0) return 0;
+  const int64_t rows = (int64_t)p.T * p.H;
+  int64_t blocks = 0;
+  (void)with_types(p, [&](auto s) {
+    using S = decltype(s);
+    constexpr int row = S::place == GDR_RES_BEFORE ? 2 * sizeof(typename S::Res) + sizeof(typename S::Type)
+                        : S::place == GDR_RES_AFTER ? sizeof(typename S::Type) + sizeof(typename S::Res)
+                                                    : 2 * sizeof(typename S::Type);
+    constexpr int each = row + (S::gate ? sizeof(typename S::Type) : 0);
+    blocks = blocks_for<S>(rows, p.D, each, BWD_BYTES);
+    return hipSuccess;
+  });
+  return (int)std::min<int64_t>(norm_workers(rows, p.D), blocks);
 }
 
 hipError_t launch_norm_bwd(const gdr_norm &p, const void *dy, const void *ds, void *dx, int64_t dx_stride, void *dgate,

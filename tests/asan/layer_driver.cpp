@@ -28,6 +28,7 @@ hipError_t launch_gate_bwd(const gdr_gate &, const float *, void *, int64_t, flo
 hipError_t launch_step(bool, const gdr_step &, uint16_t *, hipStream_t) { return count(); }
 hipError_t launch_norm_fwd(const gdr_norm &, void *, hipStream_t) { return count(); }
 hipError_t launch_norm_bwd(const gdr_norm &, const void *, const void *, void *, int64_t, void *, int64_t, void *, float *, int, hipStream_t) { return count(); }
+int norm_bwd_workers(const gdr_norm &) { return 1; }
 hipError_t launch_conv_sum(const float *, int, int, int, float *, float *, hipStream_t) { return count(); }
 hipError_t launch_gate_sum(const float *, int, int, int, float *, float *, hipStream_t) { return count(); }
 hipError_t launch_norm_sum(const float *, int, int, float *, hipStream_t) { return count(); }
