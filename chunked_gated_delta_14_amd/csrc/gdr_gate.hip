@@ -85,22 +85,31 @@ __device__ __forceinline__ void load_params(const GateArgs &p, int c, float (&A)
 
 constexpr int U = 4;  // rows in flight per thread
 
+// First row of a thread set: a block takes U x LY neighbouring rows at a time, its
+// sets' rows side by side, and the blocks follow one another, so that what is in
+// flight lies close together.  ([261392, 2048], softplus: forward 580 us and backward
+// 794; with a set's U rows a whole round of workers apart 621 and 887.)
+__device__ __forceinline__ int64_t first_row(const GateArgs &p, int ty) {
+  return (int64_t)(blockIdx.x / p.nchb) * U * p.ly + ty;
+}
+
 template <class T, int VEC, int KIND, bool UNI>
 __global__ __launch_bounds__(256) void gate_fwd_kernel(GateArgs p, int workers, float *__restrict__ g) {
   const int tx = threadIdx.x % p.lx, ty = set_of<UNI>(p.lx);
-  const int chb = blockIdx.x % p.nchb, worker = (blockIdx.x / p.nchb) * p.ly + ty;
+  const int chb = blockIdx.x % p.nchb;
   const int group = chb * p.lx + tx;
   if (ty >= p.ly || group >= (p.C + VEC - 1) / VEC) return;
   const int c = first_channel<VEC>(group, p.C);
   float A[VEC], b[VEC];
   load_params<VEC>(p, c, A, b);
-  const T *__restrict__ x = static_cast<const T *>(p.x) + worker * p.xs;
-  float *__restrict__ out = g + (int64_t)worker * p.C;
-  const int64_t xstep = workers * p.xs, gstep = (int64_t)workers * p.C;
-  for (int64_t t = worker; t < p.T; t += (int64_t)U * workers) {
+  const int64_t first = first_row(p, ty), step = (int64_t)U * workers;
+  const T *__restrict__ x = static_cast<const T *>(p.x) + first * p.xs;
+  float *__restrict__ out = g + first * p.C;
+  const int64_t xstep = p.ly * p.xs, gstep = (int64_t)p.ly * p.C;
+  for (int64_t t = first; t < p.T; t += step) {
     Raw<T, VEC> r[U];
 #pragma unroll
-    for (int i = 0; i < U; ++i) r[i].load((t + (int64_t)i * workers < p.T ? x + i * xstep : x) + c);
+    for (int i = 0; i < U; ++i) r[i].load((t + i * p.ly < p.T ? x + i * xstep : x) + c);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       float v[VEC];
@@ -108,10 +117,10 @@ __global__ __launch_bounds__(256) void gate_fwd_kernel(GateArgs p, int workers, 
       for (int e = 0; e < VEC; ++e) v[e] = gate_value<KIND>(r[i].get(e) + b[e], A[e], p.floor);
       Raw<float, VEC> o;
       o.set(v);
-      if (t + (int64_t)i * workers < p.T) o.store(out + i * gstep + c);
+      if (t + i * p.ly < p.T) o.store(out + i * gstep + c);
     }
-    x += U * xstep;
-    out += U * gstep;
+    x += step * p.xs;
+    out += step * p.C;
   }
 }
 
@@ -121,7 +130,7 @@ template <class T, int VEC, int KIND, bool UNI>
 __global__ __launch_bounds__(256) void gate_bwd_kernel(GateArgs p, int workers, const float *__restrict__ dg,
                                                        T *__restrict__ dx, int64_t dxs, float *__restrict__ partial) {
   const int tx = threadIdx.x % p.lx, ty = set_of<UNI>(p.lx);
-  const int chb = blockIdx.x % p.nchb, worker = (blockIdx.x / p.nchb) * p.ly + ty;
+  const int chb = blockIdx.x % p.nchb;
   const int group = chb * p.lx + tx, groups = (p.C + VEC - 1) / VEC;
   const bool live = ty < p.ly && group < groups;
   const int c = first_channel<VEC>(min(group, groups - 1), p.C);
@@ -129,22 +138,23 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateArgs p, int workers, 
   load_params<VEC>(p, c, A, b);
 #pragma unroll
   for (int e = 0; e < VEC; ++e) sa[e] = sb[e] = 0.f;
-  const T *__restrict__ x = static_cast<const T *>(p.x) + worker * p.xs;
-  const float *__restrict__ d = dg + (int64_t)worker * p.C;
-  T *__restrict__ out = dx + worker * dxs;
-  const int64_t xstep = workers * p.xs, gstep = (int64_t)workers * p.C, ostep = workers * dxs;
-  for (int64_t t = live ? worker : p.T; t < p.T; t += (int64_t)U * workers) {
+  const int64_t first = first_row(p, ty), step = (int64_t)U * workers;
+  const T *__restrict__ x = static_cast<const T *>(p.x) + first * p.xs;
+  const float *__restrict__ d = dg + first * p.C;
+  T *__restrict__ out = dx + first * dxs;
+  const int64_t xstep = p.ly * p.xs, gstep = (int64_t)p.ly * p.C, ostep = p.ly * dxs;
+  for (int64_t t = live ? first : p.T; t < p.T; t += step) {
     Raw<T, VEC> r[U];
     Raw<float, VEC> q[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const bool there = t + (int64_t)i * workers < p.T;
+      const bool there = t + i * p.ly < p.T;
       r[i].load((there ? x + i * xstep : x) + c);
       q[i].load((there ? d + i * gstep : d) + c);
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      if (t + (int64_t)i * workers < p.T) {
+      if (t + i * p.ly < p.T) {
         float v[VEC];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
@@ -159,9 +169,9 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateArgs p, int workers, 
         o.store(out + i * ostep + c);
       }
     }
-    x += U * xstep;
-    d += U * gstep;
-    out += U * ostep;
+    x += step * p.xs;
+    d += step * p.C;
+    out += step * dxs;
   }
   __shared__ float lds[2 * VEC * 256];
   float v[2 * VEC], s = 0.f;
