@@ -9,10 +9,10 @@
 // dX before the document's first row is ds0.
 //
 // Bound by HBM: about 17 (forward) and 34 (backward) lane operations a value against
-// 4 and 6 bytes leave the vector units 0.65 and 0.7 busy.  W = 4, SiLU, bf16, on a card
-// that copies 5.5 TB/s: forward [261392, 2048] 357 us, 6.0 TB/s; backward [241817,
-// 6144] 1771 us, 5.1 TB/s.  Nothing is kept for the backward, since z costs less to
-// form again than to read.
+// 4 and 6 bytes keep the vector units 0.6 and 0.8 busy.  W = 4, SiLU, bf16, on a card
+// that copies 5.1 TB/s: forward [261392, 2048] 364 us, 6.0 TB/s; backward [241817,
+// 6144] 1771 us, 5.2 TB/s, each with the 7 % that run starts read again.  Nothing is
+// kept for the backward, since z costs less to form again than to read.
 #include "gdr_layer.h"
 #include "gdr_vec.h"
 

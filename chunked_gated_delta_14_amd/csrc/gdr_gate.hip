@@ -8,9 +8,9 @@
 // with e = exp(-|u|) in (0,1], and log(1+e) = 2 artanh(v) with v = e/(2+e) <= 1/3:
 // an odd function of v keeps its relative accuracy for tiny e, where 1 + e would
 // lose it.  Bound by HBM; the arithmetic, about 30 lane operations per value, is up
-// to 0.8 of what the vector units do in that time, so it is kept short.  On a card that
-// copies 5.5 TB/s: forward [261392, 2048] from bf16 596 us, 5.4 TB/s; backward [32674,
-// 2048] 102 us with its sums, 5.3 TB/s.
+// to 0.9 of what the vector units do in that time, so it is kept short.  On a card that
+// copies 5.1 TB/s: forward [261392, 2048] from bf16 580 us, 5.5 TB/s; backward [32674,
+// 2048] 103 us with its sums, 5.2 TB/s.
 #include "gdr_layer.h"
 #include "gdr_vec.h"
 
@@ -218,7 +218,8 @@ hipError_t with_types(const gdr_gate &p, int vec, bool uniform, F f) {
 
 // Channels per thread of the forward.  From bf16, 4: a wavefront's stores then cover
 // whole lines one after the other ([261392, 2048] 625 us, with 8 channels 701 us).
-// From fp32, 8: twice the bytes in flight ([100000, 2048] 324 us, with 4 359 us).
+// From fp32, 8: twice the bytes in flight ([100000, 2048] 324 us, with 4 359 us).  All
+// four measured before a block's rows lay side by side.
 int fwd_vec(int C, int dtype) {
   const int v = dtype == GDR_BF16 ? 4 : GATE_VEC;
   return C >= v ? v : 1;
@@ -231,7 +232,8 @@ hipError_t launch_gate_fwd(const gdr_gate &p, float *g, hipStream_t stream) {
   const int C = p.H * p.D;
   const int vec = fwd_vec(C, p.dtype);
   const Lanes l = lanes_for(groups_of(C, vec));
-  // up to 4M threads: few rows each, no sums to share ([261392, 2048] 625 us; 2M 648, 0.5M 692)
+  // up to 4M threads: few rows each, no sums to share ([261392, 2048] 580 us; 0.5M 616,
+  // 0.25M 603, 0.125M 830)
   const int workers = workers_for(((int64_t)p.T + U - 1) / U, l, 1 << 22);
   const GateArgs a = args_of(p, l);
   const unsigned blocks = (unsigned)(workers / l.ly * l.nchb);

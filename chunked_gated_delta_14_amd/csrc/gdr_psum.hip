@@ -2,7 +2,7 @@
 // A block takes 32 neighbouring columns (128-byte lines) with 32 sets of threads;
 // set k adds rows k, k + 32, ... and the sets' sums are added in a fixed order.  Bound
 // by the read of the partials, a percent or two of what the first step moves, and
-// by its latency where they are few ([85, 5 x 6144] 6 us, [1024, 2048] 5 us).
+// by its latency where they are few ([85, 5 x 6144] 6 us, [256, 2048] 5 us).
 #include "gdr_layer.h"
 #include "gdr_vec.h"
 
