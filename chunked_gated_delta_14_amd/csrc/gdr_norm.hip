@@ -264,7 +264,12 @@ __global__ __launch_bounds__(row_threads(LPR)) void norm_bwd_kernel(NormArgs a) 
       }
     }
     row_sum<LPR, 2>(q, lds);
-    const float rs = __builtin_amdgcn_rsqf(fmaf(q[0], inv, a.eps)), m = q[1] * inv * rs * rs;
+    const float rs = __builtin_amdgcn_rsqf(fmaf(q[0], inv, a.eps));
+    float m = q[1] * inv * rs * rs, k = rs;
+    // A row of one value: v - u rs^2 (v u) = v eps rs^2, of which the subtraction would
+    // leave only its rounding.
+    if constexpr (VEC == 1)
+      if (a.D == 1) m = 0.f, k = rs * (a.eps * (rs * rs));
     if (!mine) continue;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -282,7 +287,7 @@ __global__ __launch_bounds__(row_threads(LPR)) void norm_bwd_kernel(NormArgs a) 
           t *= silu ? zz * g : g;
         }
         dw_at(i, e) = fmaf(t, n, dw_at(i, e));
-        d[e] = rs * fmaf(t, w[i][e], -u * m);
+        d[e] = k * fmaf(t, w[i][e], -u * m);
         if constexpr (PLACE == GDR_RES_BEFORE) d[e] += r.d[i].get(e);
       }
       if constexpr (PLACE == GDR_RES_BEFORE) {

@@ -420,6 +420,36 @@ def test_norm(case):
         ref.close(dres2, d2["dres"], d2["Edres"], rtype, "dres without ds")
 
 
+@pytest.mark.parametrize("place,act,eps", [("none", "none", 1e-6), ("after", "silu", 1e-6), ("before", "none", 1e-3),
+                                            ("none", "sigmoid", 0.0)])
+def test_norm_rows_of_one_value(place, act, eps):
+    """D = 1: du = eps rs^3 v, to a few roundings of itself although v and u rs^2 mean(v u) nearly cancel."""
+    g, r = gdr(), rng(int(1e4 * eps) + len(act))
+    acts = {"none": g.GDR_ACT_NONE, "silu": g.GDR_ACT_SILU, "sigmoid": g.GDR_ACT_SIGMOID}
+    codes = {"none": g.GDR_RES_NONE, "before": g.GDR_RES_BEFORE, "after": g.GDR_RES_AFTER}
+    shape, alpha = (333, 2, 1), 0.5 if place != "none" else 1.0
+    print("[case] norm of one value", place, act, eps, flush=True)
+    x, dy, res = (dev(r.standard_normal(shape), F32) for _ in range(3))
+    w = dev(1 + 0.2 * r.standard_normal(1), F32)
+    z = dev(2 * r.standard_normal(shape), F32) if act != "none" else None
+    s = x if place == "before" else None  # the stored stream
+    p = g.NormProblem(None if s is not None else x, w, z, acts[act], None if place != "after" else res, s, codes[place], alpha,
+                      eps, **(dict(dtype=F32) if s is not None else {}))
+    dx, dw = nan(shape, F32), nan((1,), F32)
+    dz = nan(shape, F32) if z is not None else None
+    dres = nan(shape, F32) if place == "before" else None
+    g.norm_bwd(p, dy, None if place == "before" else dx, dw, p.alloc_workspace(), dz, None, dres)
+    torch.cuda.synchronize()
+    e = float(np.float32(eps))
+    a, Ea, _, _ = ref._act(f64(z), act)
+    t = f64(dy) * f64(w) * (alpha if place == "after" else 1.0)
+    scale = e / np.sqrt(f64(x) ** 2 + e) ** 3
+    # rs: the square, the sum and rsq (two) at half the relative error of its argument, 3; cubed 9; its products 3;
+    # v's 3 and the last 1, over the activation's own error
+    want = scale * t * a
+    ref.close(dx if place != "before" else dres, want, 16 * np.abs(want) + scale * np.abs(t) * Ea, F32, "du")
+
+
 def test_norm_zero_rows_and_empty():
     """A row of zeros stays finite; no rows give zero parameter gradients."""
     g = gdr()
