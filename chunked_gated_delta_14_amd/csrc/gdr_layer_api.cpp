@@ -101,6 +101,8 @@ int32_t conv_bwd(const gdr_conv *p, const void *dy, int64_t dy_stride, const voi
   if (rc) return rc;
   if (!dw) return invalid("dweight is NULL");
   if (p->T > 0 && (!dy || !dx)) return invalid("dy and dx must be non-NULL");
+  // the kernel reads the weight wherever it is launched, for ds0 of empty documents too
+  if (p->N > 0 && ds0 && !p->weight) return invalid("weight must be non-NULL with ds0");
   if (!stride_ok(dy_stride, p->C, p->T) || !stride_ok(dx_stride, p->C, p->T)) return invalid("dy_stride or dx_stride below C");
   if (!element_aligned(dy, p->dtype) || !element_aligned(dst, p->dtype) || !element_aligned(dx, p->dtype) ||
       !element_aligned(ds0, p->dtype) || !element_aligned(dw, GDR_F32) || !element_aligned(dbias, GDR_F32))

@@ -162,6 +162,15 @@ def test_norm_call_refusals():
     refused(L.gdr_norm_bwd(ctypes.byref(b), PTR, None, PTR, 256, PTR, 256, None, PTR, PTR, need, None), 1, "dres is NULL")
 
 
+def test_conv_backward_of_empty_documents_needs_a_weight():
+    """ds0 of documents without tokens launches a kernel, so a NULL weight is refused there too.  Without ds0, or without
+    documents, nothing reads it and the call passes on to the check that follows, of a misaligned workspace."""
+    L = gdr.lib()
+    for N, ds0, code, word in ((3, OUT2, 1, "weight"), (3, None, 3, "aligned"), (0, OUT2, 3, "aligned")):
+        p = conv(N=N, T=0, n_chunks=0, x=None, weight=None)
+        refused(L.gdr_conv_bwd(ctypes.byref(p), None, 16, None, None, 16, OUT, None, ds0, PTR + 16, BIG, None), code, word)
+
+
 def test_outputs_that_are_inputs_are_refused():
     """Each output given the address of one of the call's inputs."""
     L = gdr.lib()
