@@ -464,26 +464,19 @@ hipError_t with_types(const gdr_conv &p, int vec, const Lanes &l, F f) {
   return vec == 1 ? with_flags<float, 1>(p, l, f) : with_flags<float, 4>(p, l, f);
 }
 
-// Tokens per thread of the forward: short runs keep the registers few, but each reads
-// W-1 rows again ([261392, 2048] W = 4 361 us with 8, 380 with 16, 394 with 32; [30000,
-// 6144] W = 8 213 us with 16, 267 with 8).
-constexpr int fwd_run(int W) { return W <= 4 ? 8 : 16; }
-
 }  // namespace
 
 hipError_t launch_conv_fwd(const gdr_conv &p, void *y, int64_t y_stride, void *st, hipStream_t stream) {
-  const int vec = vec_of(p.C, p.dtype);
-  const Lanes l = lanes_for(groups_of(p.C, vec));
+  const ConvFwdPlan plan = conv_fwd_plan(p, st != nullptr);
+  const Lanes &l = plan.lanes;
   const ConvArgs a = args_of(p, l);
-  const int64_t runs = (int64_t)p.n_chunks * (64 / fwd_run(p.W)), nrb = (runs + l.ly - 1) / l.ly;
-  const int64_t blocks = (nrb + (st ? (p.N + l.ly - 1) / l.ly : 0)) * l.nchb;
+  const unsigned blocks = (unsigned)(plan.rows() * l.nchb);
   if (blocks == 0) return hipSuccess;
-  if (blocks >= (int64_t(1) << 31)) return hipErrorInvalidValue;
-  return with_types<8>(p, vec, l, [&](auto t, auto v, auto w, auto s, auto u) {
+  return with_types<8>(p, plan.vec, l, [&](auto t, auto v, auto w, auto s, auto u) {
     using T = decltype(t);
     conv_fwd_kernel<T, decltype(v)::value, decltype(w)::value, decltype(s)::value, decltype(u)::value,
-                    fwd_run(decltype(w)::value)>
-        <<<(unsigned)blocks, l.threads, 0, stream>>>(a, (int)nrb, static_cast<T *>(y), y_stride, static_cast<T *>(st));
+                    conv_fwd_run(decltype(w)::value)>
+        <<<blocks, l.threads, 0, stream>>>(a, (int)plan.runs, static_cast<T *>(y), y_stride, static_cast<T *>(st));
     return hipGetLastError();
   });
 }
@@ -494,14 +487,13 @@ hipError_t launch_conv_bwd(const gdr_conv &p, const void *dy, int64_t dy_stride,
   const ConvBwdPlan plan = conv_bwd_plan(p.n_chunks, p.C);
   const Lanes &l = plan.lanes;
   const ConvArgs a = args_of(p, l);
-  const int nwb = plan.workers / l.ly;  // a multiple
-  const int64_t blocks = ((int64_t)nwb + (ds0 ? (p.N + l.ly - 1) / l.ly : 0)) * l.nchb;
+  const int nwb = plan.rows();
+  const unsigned blocks = (unsigned)((nwb + plan.docs(p.N, ds0 != nullptr)) * l.nchb);
   if (blocks == 0) return hipSuccess;
-  if (blocks >= (int64_t(1) << 31)) return hipErrorInvalidValue;
   return with_types<4>(p, vec, l, [&](auto t, auto v, auto w, auto s, auto u) {
     using T = decltype(t);
     conv_bwd_kernel<T, decltype(v)::value, decltype(w)::value, decltype(s)::value, decltype(u)::value>
-        <<<(unsigned)blocks, l.threads, 0, stream>>>(a, plan.run, nwb, plan.workers, static_cast<const T *>(dy), dy_stride,
+        <<<blocks, l.threads, 0, stream>>>(a, plan.run, nwb, plan.workers, static_cast<const T *>(dy), dy_stride,
                                                      static_cast<const T *>(dst), static_cast<T *>(dx), dx_stride,
                                                      static_cast<T *>(ds0), partial);
     return hipGetLastError();
@@ -510,16 +502,14 @@ hipError_t launch_conv_bwd(const gdr_conv &p, const void *dy, int64_t dy_stride,
 
 hipError_t launch_conv_step(const gdr_conv &p, void *y, int64_t y_stride, void *state, const int32_t *slots,
                             int32_t n_slots, hipStream_t stream) {
-  const int full = vec_of(p.C, p.dtype), vec = p.C % full == 0 ? full : 1;
-  Lanes l = lanes_for(p.C / vec);
-  l.uniform = false;
+  const ConvStepPlan plan = conv_step_plan(p);
+  const Lanes &l = plan.lanes;
   const ConvArgs a = args_of(p, l);
-  const int64_t blocks = (int64_t)l.nchb * ((p.N + l.ly - 1) / l.ly);
+  const unsigned blocks = (unsigned)(plan.rows * l.nchb);
   if (blocks == 0) return hipSuccess;
-  if (blocks >= (int64_t(1) << 31)) return hipErrorInvalidValue;
-  return with_types<8>(p, vec, l, [&](auto t, auto v, auto w, auto s, auto) {
+  return with_types<8>(p, plan.vec, l, [&](auto t, auto v, auto w, auto s, auto) {
     using T = decltype(t);
-    conv_step_kernel<T, decltype(v)::value, decltype(w)::value, decltype(s)::value><<<(unsigned)blocks, l.threads, 0, stream>>>(
+    conv_step_kernel<T, decltype(v)::value, decltype(w)::value, decltype(s)::value><<<blocks, l.threads, 0, stream>>>(
         a, static_cast<T *>(y), y_stride, static_cast<T *>(state), slots, n_slots);
     return hipGetLastError();
   });

@@ -47,6 +47,13 @@ inline int vec_of(int channels, int dtype) {
 }
 inline int groups_of(int channels, int vec) { return (channels + vec - 1) / vec; }
 
+// What one launch takes: HIP's grids hold fewer than 2^32 threads, and the kernels
+// count their sets (`ly` to a block, each one row, run or document) with 32 bits.
+inline bool one_launch(int64_t blocks, int threads) { return blocks * threads < (int64_t(1) << 32); }
+inline bool one_launch(int64_t row_blocks, const Lanes &l) {
+  return row_blocks * l.ly <= INT32_MAX && one_launch(row_blocks * l.nchb, l.threads);
+}
+
 // Row workers of the parameter-gradient sums: each set of LX threads adds its rows'
 // terms in registers, a block adds its LY sets and leaves one partial row, and a
 // second kernel adds the blocks' partials in a fixed order, so the sums do not
@@ -55,6 +62,44 @@ inline int workers_for(int64_t rows, const Lanes &l, int64_t target) {
   const int64_t n = std::max<int64_t>(1, target / ((int64_t)l.nchb * l.lx));
   const int64_t w = std::min<int64_t>(std::max<int64_t>(rows, 0), n);
   return (int)((w + l.ly - 1) / l.ly * l.ly);
+}
+
+// Tokens per thread of the convolution's forward: short runs keep the registers few,
+// but each reads W-1 rows again ([261392, 2048] W = 4 361 us with 8, 380 with 16, 394
+// with 32; [30000, 6144] W = 8 213 us with 16, 267 with 8).
+constexpr int conv_fwd_run(int W) { return W <= 4 ? 8 : 16; }
+
+// The forward's blocks: `runs` of them take the chunks' runs, `docs` the final rows.
+struct ConvFwdPlan {
+  Lanes lanes;
+  int vec;
+  int64_t runs, docs;
+  int64_t rows() const { return runs + docs; }
+};
+inline ConvFwdPlan conv_fwd_plan(const gdr_conv &p, bool st) {
+  ConvFwdPlan r;
+  r.vec = vec_of(p.C, p.dtype);
+  r.lanes = lanes_for(groups_of(p.C, r.vec));
+  const int64_t ly = r.lanes.ly;
+  r.runs = ((int64_t)p.n_chunks * (64 / conv_fwd_run(p.W)) + ly - 1) / ly;
+  r.docs = st ? (p.N + ly - 1) / ly : 0;
+  return r;
+}
+
+// The single-token call: whole groups of channels, since the pool's rows are rewritten in place.
+struct ConvStepPlan {
+  Lanes lanes;
+  int vec;
+  int64_t rows;
+};
+inline ConvStepPlan conv_step_plan(const gdr_conv &p) {
+  ConvStepPlan r;
+  const int full = vec_of(p.C, p.dtype);
+  r.vec = p.C % full == 0 ? full : 1;
+  r.lanes = lanes_for(p.C / r.vec);
+  r.lanes.uniform = false;
+  r.rows = ((int64_t)p.N + r.lanes.ly - 1) / r.lanes.ly;
+  return r;
 }
 
 // The convolution's backward: 4 channels per thread, runs of 64 tokens, or shorter
@@ -66,6 +111,8 @@ struct ConvBwdPlan {
   Lanes lanes;
   int run, workers;
   int rows() const { return workers / lanes.ly; }  // partial rows, one per block
+  // blocks of ds0, which follow those of the workers
+  int64_t docs(int N, bool ds0) const { return ds0 ? ((int64_t)N + lanes.ly - 1) / lanes.ly : 0; }
 };
 inline int conv_bwd_vec(int C) { return C >= 4 ? 4 : 1; }
 inline ConvBwdPlan conv_bwd_plan(int n_chunks, int C) {
@@ -118,6 +165,8 @@ hipError_t launch_norm_bwd(const gdr_norm &p, const void *dy, const void *ds, vo
 // Sums of `rows` partial rows, in a fixed order.  conv: partial [rows][W + 1][C] ->
 // dw [C][W], dbias [C].  gate: partial [rows][gate_partial_row] -> dbias [H D] and da
 // [H] (D is 1 or 128).  norm: partial [rows][D] -> dw.  A NULL dbias is skipped.
+constexpr int SUM_PARTS = 32, SUM_COLS = 32;  // threads of a block: sets and columns
+inline int64_t sum_blocks(int64_t columns) { return (columns + SUM_COLS - 1) / SUM_COLS; }
 hipError_t launch_conv_sum(const float *partial, int rows, int C, int W, float *dw, float *dbias, hipStream_t stream);
 hipError_t launch_gate_sum(const float *partial, int rows, int H, int D, float *da, float *dbias, hipStream_t stream);
 hipError_t launch_norm_sum(const float *partial, int rows, int D, float *dw, hipStream_t stream);

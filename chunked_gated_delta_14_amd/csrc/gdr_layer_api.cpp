@@ -77,6 +77,11 @@ int32_t check_conv(const gdr_conv *p, bool step) {
   if (p->N > 0 && !p->chunk_table) return invalid("chunk_table must be non-NULL");
   return GDR_OK;
 }
+const char *const kTooMany = "too many rows and channels for one launch";
+// The parameter sums take a launch of their own over (W + 1) C columns.
+bool conv_sum_fits(int32_t C, int32_t W) {
+  return gdr::one_launch(gdr::sum_blocks((int64_t)(W + 1) * C), gdr::SUM_PARTS * gdr::SUM_COLS);
+}
 int64_t conv_bytes(int32_t n_chunks, int32_t C, int32_t W) {
   return round_up((int64_t)gdr::conv_bwd_plan(n_chunks, C).rows() * (W + 1) * C * 4);
 }
@@ -86,6 +91,8 @@ int32_t conv_fwd(const gdr_conv *p, void *y, int64_t y_stride, void *st, void *s
   if (rc) return rc;
   if (p->T > 0 && !y) return invalid("y is NULL");
   if (!stride_ok(y_stride, p->C, p->T)) return invalid("y_stride below C");
+  const gdr::ConvFwdPlan plan = gdr::conv_fwd_plan(*p, st != nullptr);
+  if (!gdr::one_launch(plan.rows(), plan.lanes)) return unsupported(kTooMany);
   if (!element_aligned(y, p->dtype) || !element_aligned(st, p->dtype)) return invalid("y and st must be aligned to their elements");
   if (aliases(y, p->x, p->s0) || aliases(st, p->x, p->s0)) return invalid("y or st is an input");
   if ((rc = gdr::host_check_device())) return rc;
@@ -104,6 +111,9 @@ int32_t conv_bwd(const gdr_conv *p, const void *dy, int64_t dy_stride, const voi
   // the kernel reads the weight wherever it is launched, for ds0 of empty documents too
   if (p->N > 0 && ds0 && !p->weight) return invalid("weight must be non-NULL with ds0");
   if (!stride_ok(dy_stride, p->C, p->T) || !stride_ok(dx_stride, p->C, p->T)) return invalid("dy_stride or dx_stride below C");
+  const gdr::ConvBwdPlan plan = gdr::conv_bwd_plan(p->n_chunks, p->C);
+  if (!conv_sum_fits(p->C, p->W) || !gdr::one_launch(plan.rows() + plan.docs(p->N, ds0 != nullptr), plan.lanes))
+    return unsupported(kTooMany);
   if (!element_aligned(dy, p->dtype) || !element_aligned(dst, p->dtype) || !element_aligned(dx, p->dtype) ||
       !element_aligned(ds0, p->dtype) || !element_aligned(dw, GDR_F32) || !element_aligned(dbias, GDR_F32))
     return invalid("gradients must be aligned to their elements");
@@ -111,7 +121,7 @@ int32_t conv_bwd(const gdr_conv *p, const void *dy, int64_t dy_stride, const voi
   const int64_t need = conv_bytes(p->n_chunks, p->C, p->W);
   if ((rc = check_workspace(ws, ws_bytes, need))) return rc;
   if ((rc = gdr::host_check_device())) return rc;
-  const int rows = gdr::conv_bwd_plan(p->n_chunks, p->C).rows();
+  const int rows = plan.rows();
   float *partial = static_cast<float *>(ws);
   if ((rc = launch(gdr::TK_CONV_BWD, stream, "convolution gradient launch", [&](hipStream_t s) {
          return gdr::launch_conv_bwd(*p, dy, dy_stride, dst, dx, dx_stride, ds0, partial, s);
@@ -130,6 +140,8 @@ int32_t conv_step(const gdr_conv *p, void *y, int64_t y_stride, void *state, con
   if (!slots && p->N > n_slots) return invalid("fewer slots than sequences");
   if (p->T > 0 && (!y || (n_slots > 0 && !state))) return invalid("y and state must be non-NULL");
   if (!stride_ok(y_stride, p->C, p->T)) return invalid("y_stride below C");
+  const gdr::ConvStepPlan plan = gdr::conv_step_plan(*p);
+  if (!gdr::one_launch(plan.rows, plan.lanes)) return unsupported(kTooMany);
   if (!element_aligned(y, p->dtype) || !element_aligned(state, p->dtype) || !element_aligned(slots, GDR_F32))
     return invalid("y, state and slots must be aligned to their elements");
   if (aliases(y, p->x, state) || aliases(state, p->x)) return invalid("y or state is an input");
@@ -212,7 +224,7 @@ int32_t step(bool gdn, const gdr_step *p, uint16_t *o, void *stream) {
   if (p->K != 128 || p->V != 128) return unsupported("only K = V = 128 is implemented");
   if (!gdn && p->H_qk != p->H_v) return unsupported("KDA needs H_qk == H_v");
   if (gdn && p->H_v % p->H_qk != 0) return unsupported("GDN needs H_v to be a multiple of H_qk");
-  if (p->H_v > 65536 || (int64_t)p->N * p->H_v >= (int64_t(1) << 31)) return unsupported("problem too large");
+  if (p->H_v > 65536 || !gdr::one_launch((int64_t)p->N * p->H_v, 256)) return unsupported("problem too large");
   if (!(p->scale == p->scale)) return invalid("scale is NaN");
   if (p->input_flags & ~(GDR_IN_QK_L2NORM | GDR_IN_BETA_SIGMOID)) return invalid("unknown input flag");
   if (!p->cu_seqlens && p->N != p->T) return invalid("N must equal T without cu_seqlens");
@@ -337,6 +349,7 @@ int64_t gdr_conv_workspace_bytes(int32_t n_chunks, int32_t C, int32_t W, int32_t
   if (n_chunks < 0 || C < 1 || !is_dtype(dtype)) return -(int64_t)invalid("n_chunks must be >= 0, C positive and dtype known");
   if (W < 2 || W > 8) return -(int64_t)unsupported("W outside 2..8");
   if (C > (1 << 24)) return -(int64_t)unsupported("C above 2^24");
+  if (!conv_sum_fits(C, W)) return -(int64_t)unsupported(kTooMany);
   return conv_bytes(n_chunks, C, W);
 }
 int32_t gdr_conv_bwd(const gdr_conv *p, const void *dy, int64_t dy_stride, const void *dst, void *dx, int64_t dx_stride,

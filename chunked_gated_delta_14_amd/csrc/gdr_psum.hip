@@ -9,7 +9,7 @@
 namespace gdr {
 namespace {
 
-constexpr int PARTS = 32, COLS = 32;
+constexpr int PARTS = SUM_PARTS, COLS = SUM_COLS;
 
 // The sum of column `col` of [rows][M], returned to the threads of set 0.
 __device__ __forceinline__ float column_sum(const float *__restrict__ partial, int rows, int M, int col, float *lds) {
@@ -74,7 +74,7 @@ __global__ __launch_bounds__(PARTS *COLS) void norm_sum_kernel(const float *__re
   if (threadIdx.x < COLS && col < D) dw[col] = s;
 }
 
-int blocks_for(int64_t columns) { return (int)((columns + COLS - 1) / COLS); }
+int blocks_for(int64_t columns) { return (int)sum_blocks(columns); }
 
 }  // namespace
 

@@ -268,7 +268,8 @@ int32_t gdr_kda_ckpt_noalloc(const gdr_problem *p, uint16_t *o, float *ht, const
  * need no alignment beyond their element's.  Values are held and summed in fp32;
  * an output is rounded once.  A backward's workspace and a pool belong to one call
  * at a time: calls that may overlap, captured graphs among them, need their own.
- * An output given the address of an input is refused.
+ * An output given the address of an input is refused.  A call whose rows need a
+ * launch of 2^32 threads or more is refused with GDR_ERR_UNSUPPORTED.
  * ------------------------------------------------------------------------- */
 enum gdr_dtype { GDR_BF16 = 0, GDR_F32 = 1 };
 enum gdr_activation { GDR_ACT_NONE = 0, GDR_ACT_SILU = 1, GDR_ACT_SIGMOID = 2 };
@@ -276,7 +277,12 @@ enum gdr_activation { GDR_ACT_NONE = 0, GDR_ACT_SILU = 1, GDR_ACT_SIGMOID = 2 };
 /* Short causal depthwise convolution over packed documents:
  *     z[t,c] = bias[c] + sum_{i<W} weight[c,i] X[t-(W-1)+i, c],   y = z or z * sigmoid(z)
  * where X is the document's rows preceded by the W-1 rows s0 (zeros when NULL),
- * the oldest first.  2 <= W <= 8. */
+ * the oldest first.  2 <= W <= 8.  A thread takes 8 channels (bf16) or 4 (fp32) of a
+ * row; the forward starts 8 threads of a row's width for every chunk (4 with W > 4),
+ * however short its document, and one for each document of st; the backward one of
+ * C / 4 for each document of ds0; the single-token call one for each sequence.  Their
+ * number stays below 2^32, and so do 32 (W + 1) C: from 2^21 one-token documents at
+ * 2048 bf16 channels on, for instance, a pack takes more than one call. */
 typedef struct gdr_conv {
   int32_t T;          /* tokens (rows of x), >= 0 */
   int32_t N;          /* documents; the single-token call: sequences, N == T */
@@ -350,7 +356,8 @@ int32_t gdr_gate_bwd(const gdr_gate *p, const float *dg, void *dx, int64_t dx_st
  * the forward is such a state.  Sequences without tokens and sequences whose slot
  * lies outside [0, n_slots) are skipped: their state and o are left as they were,
  * and so are rows of o that no sequence covers.  The slots of the other sequences
- * are distinct; two sequences of one slot race.  cu_seqlens is clipped to [0, T]. */
+ * are distinct; two sequences of one slot race.  cu_seqlens is clipped to [0, T].
+ * N * H_v < 2^24. */
 typedef struct gdr_step {
   int32_t T, N, H_qk, H_v, K, V; /* as gdr_problem; KDA: H_qk == H_v */
   int32_t n_slots;

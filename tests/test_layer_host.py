@@ -171,6 +171,50 @@ def test_conv_backward_of_empty_documents_needs_a_weight():
         refused(L.gdr_conv_bwd(ctypes.byref(p), None, 16, None, None, 16, OUT, None, ds0, PTR + 16, BIG, None), code, word)
 
 
+def test_launch_limits():
+    """A launch holds fewer than 2^32 threads and counts its rows, runs and documents with 32 bits: calls past that are
+    refused by the checks.  The largest accepted sizes pass on to the check that follows, of an output off its alignment."""
+    L = gdr.lib()
+
+    def fwd(st, **kw):
+        p = conv(x_stride=kw["C"], **kw)
+        return L.gdr_conv_fwd(ctypes.byref(p), OUT + 1, kw["C"], OUT2 if st else None, None)
+
+    # 2048 bf16 channels fill a block of 256 threads: 8 runs of each chunk (4 with W > 4), and a block for each final row
+    for n, W, st, ok in ((2 ** 21 - 1, 4, False, True), (2 ** 21, 4, False, False), (2 ** 21 - 1, 4, True, False),
+                         (2 ** 22 - 1, 5, False, True), (2 ** 22, 5, False, False)):
+        rc = fwd(st, T=n, N=n, n_chunks=n, C=2048, W=W)
+        refused(rc, *((1, "aligned") if ok else (2, "one launch")))
+    # narrow rows: 256 sets to a block (C = 1), 85 (C = 3)
+    most = 2 ** 28 - 32
+    for n, C, ok in ((most, 1, True), (most + 31, 1, False), (2 ** 28 - 1, 3, False), (2 ** 24 * 85 // 8 - 86, 3, True)):
+        rc = fwd(False, T=n, N=n, n_chunks=n, C=C)
+        refused(rc, *((1, "aligned") if ok else (2, "one launch")))
+    # the backward: a block of 256 threads for each half of ds0's rows beside the 16 workers' of 2 chunks in
+    # runs of 8 tokens
+    for N, ds0, ok in ((2 ** 23 - 17, True, True), (2 ** 23 - 16, True, False), (2 ** 23, False, True)):
+        p = conv(N=N, C=2048, x_stride=2048)
+        rc = L.gdr_conv_bwd(ctypes.byref(p), IN, 2048, None, OUT + 1, 2048, OUT2, None, OUT if ds0 else None, 1 << 24, BIG, None)
+        refused(rc, *((1, "aligned") if ok else (2, "one launch")))
+    # the parameter sums: (W + 1) C columns, 32 to a block of 1024 threads
+    for W, ok in ((6, True), (7, False), (8, False)):
+        p = conv(C=1 << 24, x_stride=1 << 24, W=W)
+        rc = L.gdr_conv_bwd(ctypes.byref(p), IN, 1 << 24, None, OUT + 1, 1 << 24, OUT2, None, None, 1 << 24, BIG, None)
+        refused(rc, *((1, "aligned") if ok else (2, "one launch")))
+        if ok:
+            assert gdr.conv_workspace_bytes(2, 1 << 24, W, 0) > 0
+        else:
+            with pytest.raises(gdr.GdrError):
+                gdr.conv_workspace_bytes(2, 1 << 24, W, 0)
+    for N, ok in ((2 ** 24 - 1, True), (2 ** 24, False)):
+        p = conv(T=N, N=N, C=2048, x_stride=2048)
+        rc = L.gdr_conv_step(ctypes.byref(p), OUT + 1, 2048, OUT2, PTR, 4, None)
+        refused(rc, *((1, "aligned") if ok else (2, "one launch")))
+    for N, ok in ((2 ** 20 - 1, True), (2 ** 20, False)):
+        p = step(T=N, N=N, H_qk=16, H_v=16, q_stride=2048, k_stride=2048, v_stride=2048, slots=PTR + 2)
+        refused(L.gdr_kda_step(ctypes.byref(p), OUT, None), *((1, "aligned") if ok else (2, "too large")))
+
+
 def test_outputs_that_are_inputs_are_refused():
     """Each output given the address of one of the call's inputs."""
     L = gdr.lib()
