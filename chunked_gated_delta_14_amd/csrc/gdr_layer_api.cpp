@@ -3,6 +3,7 @@
 #include "gdr_layer.h"
 
 #include <cstdio>
+#include <initializer_list>
 
 #include "gdr_host.h"
 #include "gdr_kernels.h"
@@ -24,11 +25,14 @@ bool element_aligned(const void *p, int32_t dtype) {
 // Stride of [T] rows `width` wide; rows of fewer than two tokens have none to check.
 bool stride_ok(int64_t stride, int64_t width, int64_t T) { return T < 2 || stride >= width; }
 
-// Whether an output is one of a call's inputs.  (Parts of one wider buffer, which
-// rows may be, start at different addresses; other overlaps are the caller's.)
-template <class... P>
-bool aliases(const void *out, P... in) {
-  return out && ((out == static_cast<const void *>(in)) || ...);
+// Whether one of a call's outputs is one of its inputs.  (Parts of one wider buffer,
+// which rows may be, start at different addresses; other overlaps are the caller's.)
+using Pointers = std::initializer_list<const void *>;
+bool aliases(Pointers outs, Pointers ins) {
+  for (const void *out : outs)
+    for (const void *in : ins)
+      if (out && out == in) return true;
+  return false;
 }
 
 int32_t check_workspace(void *ws, int64_t have, int64_t need) {
@@ -94,7 +98,7 @@ int32_t conv_fwd(const gdr_conv *p, void *y, int64_t y_stride, void *st, void *s
   const gdr::ConvFwdPlan plan = gdr::conv_fwd_plan(*p, st != nullptr);
   if (!gdr::one_launch(plan.rows(), plan.lanes)) return unsupported(kTooMany);
   if (!element_aligned(y, p->dtype) || !element_aligned(st, p->dtype)) return invalid("y and st must be aligned to their elements");
-  if (aliases(y, p->x, p->s0) || aliases(st, p->x, p->s0)) return invalid("y or st is an input");
+  if (aliases({y, st}, {p->x, p->weight, p->bias, p->s0, p->chunk_table})) return invalid("y or st is an input");
   if ((rc = gdr::host_check_device())) return rc;
   if ((rc = launch(gdr::TK_CONV_FWD, stream, "convolution launch",
                    [&](hipStream_t s) { return gdr::launch_conv_fwd(*p, y, y_stride, st, s); })))
@@ -117,9 +121,10 @@ int32_t conv_bwd(const gdr_conv *p, const void *dy, int64_t dy_stride, const voi
   if (!element_aligned(dy, p->dtype) || !element_aligned(dst, p->dtype) || !element_aligned(dx, p->dtype) ||
       !element_aligned(ds0, p->dtype) || !element_aligned(dw, GDR_F32) || !element_aligned(dbias, GDR_F32))
     return invalid("gradients must be aligned to their elements");
-  if (aliases(dx, p->x, p->s0, dy, dst) || aliases(ds0, p->x, p->s0, dy, dst)) return invalid("dx or ds0 is an input");
   const int64_t need = conv_bytes(p->n_chunks, p->C, p->W);
   if ((rc = check_workspace(ws, ws_bytes, need))) return rc;
+  if (aliases({dx, dw, dbias, ds0}, {p->x, p->weight, p->bias, p->s0, p->chunk_table, dy, dst}))
+    return invalid("dx, dweight, dbias or ds0 is an input");
   if ((rc = gdr::host_check_device())) return rc;
   const int rows = plan.rows();
   float *partial = static_cast<float *>(ws);
@@ -144,7 +149,8 @@ int32_t conv_step(const gdr_conv *p, void *y, int64_t y_stride, void *state, con
   if (!gdr::one_launch(plan.rows, plan.lanes)) return unsupported(kTooMany);
   if (!element_aligned(y, p->dtype) || !element_aligned(state, p->dtype) || !element_aligned(slots, GDR_F32))
     return invalid("y, state and slots must be aligned to their elements");
-  if (aliases(y, p->x, state) || aliases(state, p->x)) return invalid("y or state is an input");
+  if (aliases({y}, {p->x, p->weight, p->bias, slots, state}) || aliases({state}, {p->x, p->weight, p->bias, slots}))
+    return invalid("y or state is an input");
   if ((rc = gdr::host_check_device())) return rc;
   if ((rc = launch(gdr::TK_CONV_STEP, stream, "convolution step launch",
                    [&](hipStream_t s) { return gdr::launch_conv_step(*p, y, y_stride, state, slots, n_slots, s); })))
@@ -183,7 +189,7 @@ int32_t gate_fwd(const gdr_gate *p, float *g, void *stream) {
   if (rc) return rc;
   if (p->T > 0 && !g) return invalid("g is NULL");
   if (!element_aligned(g, GDR_F32)) return invalid("g must be aligned to its elements");
-  if (aliases(g, p->x)) return invalid("g is an input");
+  if (aliases({g}, {p->x, p->a_log, p->bias})) return invalid("g is an input");
   if ((rc = gdr::host_check_device())) return rc;
   if ((rc = launch(gdr::TK_GATE_FWD, stream, "gate launch", [&](hipStream_t s) { return gdr::launch_gate_fwd(*p, g, s); })))
     return rc;
@@ -201,8 +207,8 @@ int32_t gate_bwd(const gdr_gate *p, const float *dg, void *dx, int64_t dx_stride
   if (!element_aligned(dg, GDR_F32) || !element_aligned(dx, p->dtype) || !element_aligned(da, GDR_F32) ||
       !element_aligned(dbias, GDR_F32))
     return invalid("gradients must be aligned to their elements");
-  if (aliases(dx, p->x, dg)) return invalid("dx is an input");
   if ((rc = check_workspace(ws, ws_bytes, gate_bytes(p->T, C, p->D)))) return rc;
+  if (aliases({dx, da, dbias}, {p->x, p->a_log, p->bias, dg})) return invalid("dx, da_log or dbias is an input");
   if ((rc = gdr::host_check_device())) return rc;
   float *partial = static_cast<float *>(ws);
   const int rows = gdr::gate_rows(p->T, C);
@@ -241,7 +247,9 @@ int32_t step(bool gdn, const gdr_step *p, uint16_t *o, void *stream) {
       !element_aligned(p->g, GDR_F32) || !element_aligned(p->beta, gdn ? GDR_F32 : GDR_BF16) ||
       !element_aligned(p->cu_seqlens, GDR_F32) || !element_aligned(p->slots, GDR_F32) || !element_aligned(o, GDR_BF16))
     return invalid("operands must be aligned to their elements");
-  if (aliases(o, p->q, p->k, p->v, p->state)) return invalid("o is an input");
+  if (aliases({o}, {p->q, p->k, p->v, p->g, p->beta, p->cu_seqlens, p->slots, p->state}) ||
+      aliases({p->state}, {p->q, p->k, p->v, p->g, p->beta, p->cu_seqlens, p->slots}))
+    return invalid("o or state is an input");
   int32_t rc = gdr::host_check_device();
   if (rc) return rc;
   if ((rc = launch(gdr::TK_STEP, stream, "step launch", [&](hipStream_t s) { return gdr::launch_step(gdn, *p, o, s); }))) return rc;
@@ -291,7 +299,8 @@ int32_t norm_fwd(const gdr_norm *p, void *y, void *stream) {
   if (p->T > 0 && !y) return invalid("y is NULL");
   if (!element_aligned(y, p->placement == GDR_RES_AFTER ? p->res_dtype : p->dtype)) return invalid("y must be aligned to its elements");
   const void *s = p->placement == GDR_RES_BEFORE ? p->s : nullptr;
-  if (aliases(y, p->x, p->gate, p->residual, s) || aliases(s, p->x, p->gate, p->residual)) return invalid("y or s is an input");
+  if (aliases({y}, {p->x, p->weight, p->gate, p->residual, s}) || aliases({s}, {p->x, p->weight, p->gate, p->residual}))
+    return invalid("y or s is an input");
   if ((rc = gdr::host_check_device())) return rc;
   if ((rc = launch(gdr::TK_NORM_FWD, stream, "norm launch", [&](hipStream_t s) { return gdr::launch_norm_fwd(*p, y, s); })))
     return rc;
@@ -319,10 +328,9 @@ int32_t norm_bwd(const gdr_norm *p, const void *dy, const void *ds, void *dx, in
       !element_aligned(dgate, p->dtype) || !element_aligned(dres, p->res_dtype) || !element_aligned(dw, GDR_F32))
     return invalid("gradients must be aligned to their elements");
   const void *u = before ? p->s : p->x;  // the normed row
-  if (aliases(dx, u, p->gate, dy, ds) || aliases(dgate, u, p->gate, dy, ds) || aliases(dres, u, p->gate, dy, ds))
-    return invalid("dx, dgate or dres is an input");
   const int most = gdr::norm_workers((int64_t)p->T * p->H, p->D);
   if (dw && (rc = check_workspace(ws, ws_bytes, round_up((int64_t)most * p->D * 4)))) return rc;
+  if (aliases({dx, dgate, dres, dw}, {u, p->weight, p->gate, dy, ds})) return invalid("dx, dgate, dres or dweight is an input");
   if ((rc = gdr::host_check_device())) return rc;
   const int workers = gdr::norm_bwd_workers(*p);
   // one worker's partial row is the gradient itself

@@ -246,6 +246,43 @@ def test_outputs_that_are_inputs_are_refused():
             refused(L.gdr_norm_bwd(b, C, E, dx, 256, dz, 256, dres, None, None, 0, None), 1, "is an input")
 
 
+def test_parameters_and_indices_are_not_outputs():
+    """The same for every other pair: parameters, their gradients, tables, slots and the step's gates."""
+    L, ws = gdr.lib(), 1 << 24
+    A, B, C, D, E, F, G = (IN + 4096 * i for i in range(7))
+    outs = [OUT + 4096 * i for i in range(4)]
+
+    def each(n, ins):
+        """The n outputs with one of them, in turn, one of the inputs."""
+        for i in range(n):
+            for bad in ins:
+                yield [bad if j == i else o for j, o in enumerate(outs[:n])]
+
+    c = ctypes.byref(conv(x=A, s0=B, weight=C, bias=D, chunk_table=E))
+    for y, st in each(2, (A, B, C, D, E)):
+        refused(L.gdr_conv_fwd(c, y, 16, st, None), 1, "is an input")
+    for dx, dw, db, ds0 in each(4, (A, B, C, D, E, F, G)):
+        refused(L.gdr_conv_bwd(c, F, 16, G, dx, 16, dw, db, ds0, ws, BIG, None), 1, "is an input")
+    s = ctypes.byref(conv(T=3, N=3, x=A, weight=C, bias=D))
+    for y, state in each(2, (A, C, D, E)):
+        refused(L.gdr_conv_step(s, y, 16, state, E, 3, None), 1, "is an input")
+    g = ctypes.byref(gate(x=A, a_log=B, bias=C, dtype=1))
+    for out in (A, B, C):
+        refused(L.gdr_gate_fwd(g, out, None), 1, "is an input")
+    for dx, da, db in each(3, (A, B, C, D)):
+        refused(L.gdr_gate_bwd(g, D, dx, 256, da, db, ws, BIG, None), 1, "is an input")
+    for o, state in each(2, (A, B, C, D, E, F, G)):
+        t = step(N=2, q=A, k=B, v=C, g=D, beta=E, cu_seqlens=F, slots=G, state=state)
+        refused(L.gdr_kda_step(ctypes.byref(t), o, None), 1, "is an input")
+        refused(L.gdr_gdn_step(ctypes.byref(t), o, None), 1, "is an input")
+    for y, stream in each(2, (A, B, C, D)):
+        n = norm(x=A, weight=B, gate=C, residual=D, s=stream, placement=1)
+        refused(L.gdr_norm_fwd(ctypes.byref(n), y, None), 1, "is an input")
+    n = ctypes.byref(norm(x=None, weight=B, gate=C, s=D, placement=1))
+    for dx, dz, dres, dw in each(4, (B, C, D, E, F)):
+        refused(L.gdr_norm_bwd(n, E, F, dx, 256, dz, 256, dres, dw, ws, BIG, None), 1, "is an input")
+
+
 def test_binding_refuses_cpu_tensors_and_bad_shapes():
     import torch
 
