@@ -76,6 +76,13 @@ def _bad(detail: str):
     raise GdrError(1, detail)
 
 
+def _sizes(*sizes):
+    """The C structs and calls hold sizes with 32 bits, and ctypes would cut larger ones without a word."""
+    for n in sizes:
+        if not -(1 << 31) <= n < 1 << 31:
+            _bad("a size of %d is past 32 bits" % n)
+
+
 def _dtype_code(dtype, name):
     import torch
 
@@ -190,6 +197,7 @@ class ConvProblem(_Base):
         if x.dim() != 2 or weight.dim() != 2:
             _bad("x must be [T, C] and weight [C, W]")
         self.T, self.C, self.W, self.N = int(x.shape[0]), int(x.shape[1]), int(weight.shape[1]), plan.N
+        _sizes(self.T, self.C, self.W)
         self.dtype, self.n_chunks = _dtype_code(x.dtype, "x"), plan.n_chunks
         if plan.T != self.T:
             _bad("the plan holds %d tokens, x %d" % (plan.T, self.T))
@@ -211,6 +219,7 @@ class ConvProblem(_Base):
 
 
 def conv_workspace_bytes(n_chunks, C, W, dtype) -> int:
+    _sizes(n_chunks, C, W)
     return _bytes(lib().gdr_conv_workspace_bytes(n_chunks, C, W, dtype))
 
 
@@ -255,6 +264,7 @@ class ConvStep(_Base):
         if x.dim() != 2 or weight.dim() != 2 or state.dim() != 3:
             _bad("x must be [N, C], weight [C, W] and state [n_slots, W-1, C]")
         self.N, self.C, self.W, self.n_slots = int(x.shape[0]), int(x.shape[1]), int(weight.shape[1]), int(state.shape[0])
+        _sizes(self.N, self.C, self.W, self.n_slots)
         stride = _rows(x, "x", None, None, dev)
         _need(weight, "weight", (self.C, self.W), None, dev)
         if bias is not None:
@@ -290,6 +300,7 @@ class GateProblem(_Base):
         if self.H < 1 or width % self.H or (x.dim() == 3 and x.shape[1] != self.H):
             _bad("x must be [T, H * D] or [T, H, D] with a_log's H")
         self.D = width // self.H
+        _sizes(self.T, self.H, self.D)
         self.dtype = _dtype_code(x.dtype, "x")
         stride = _rows(x, "x", None, None, dev)
         _need(a_log, "a_log", None, torch.float32, dev)
@@ -306,6 +317,7 @@ class GateProblem(_Base):
 
 
 def gate_workspace_bytes(T, H, D, dtype) -> int:
+    _sizes(T, H, D)
     return _bytes(lib().gdr_gate_workspace_bytes(T, H, D, dtype))
 
 
@@ -358,6 +370,7 @@ class StepProblem(_Base):
         self.variant = variant
         self.T, self.H_qk, self.H_v, self.n_slots = int(q.shape[0]), int(q.shape[1]), int(v.shape[1]), int(state.shape[0])
         K, V = int(q.shape[2]), int(v.shape[2])
+        _sizes(self.T, self.H_qk, self.H_v, self.n_slots, K, V)
         bf, f32 = torch.bfloat16, torch.float32
         qs = _rows(q, "q", None, bf, dev)
         ks = _rows(k, "k", tuple(q.shape), bf, dev)
@@ -367,6 +380,7 @@ class StepProblem(_Base):
         _need(state, "state", (self.n_slots, self.H_v, K, V), f32, dev)
         self.N = self.T if cu_seqlens is None else int(cu_seqlens.shape[0]) - 1
         if cu_seqlens is not None:
+            _sizes(self.N)
             _need(cu_seqlens, "cu_seqlens", (self.N + 1,), torch.int32, dev)
         if slots is not None:
             _need(slots, "slots", (self.N,), torch.int32, dev)
@@ -418,6 +432,7 @@ class NormProblem(_Base):
         self.shape = tuple(like.shape)
         self.T, self.D = int(like.shape[0]), int(like.shape[-1])
         self.H = int(like.shape[1]) if like.dim() == 3 else 1
+        _sizes(self.T, self.H, self.D)
         self.dtype = dtype if x is None else x.dtype
         if x is not None and dtype is not None and dtype != x.dtype:
             _bad("dtype differs from x's")
@@ -453,6 +468,7 @@ class NormProblem(_Base):
 
 
 def norm_workspace_bytes(T, H, D) -> int:
+    _sizes(T, H, D)
     return _bytes(lib().gdr_norm_workspace_bytes(T, H, D))
 
 

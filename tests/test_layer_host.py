@@ -296,6 +296,40 @@ def test_binding_refuses_cpu_tensors_and_bad_shapes():
         assert e.value.status == 1
 
 
+def test_binding_refuses_sizes_past_32_bits():
+    """A size that the C structs cannot hold is refused, not cut to its low 32 bits (2^32 + 8 rows are no 8 rows)."""
+    import torch
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    far = (1 << 32) + 8
+    for call in (lambda: gdr.conv_workspace_bytes(far, 16, 4, 0), lambda: gdr.gate_workspace_bytes(far, 2, 128, 0),
+                 lambda: gdr.norm_workspace_bytes(far, 1, 128), lambda: gdr.norm_workspace_bytes(8, far, 128)):
+        with pytest.raises(gdr.GdrError, match="32 bits") as e:
+            call()
+        assert e.value.status == 1
+    bf, i32 = torch.bfloat16, torch.int32
+    with FakeTensorMode():  # shapes without memory
+
+        def t(*shape, dtype=torch.float32):
+            return torch.empty(shape, dtype=dtype, device="cuda")
+
+        class Plan:
+            N, T, n_chunks, table = 1, far, far // 64, None
+
+        one = [t(1, 1, 128, dtype=bf)] * 3
+        for build in (lambda: gdr.ConvProblem(t(far, 1), t(1, 4), Plan),
+                      lambda: gdr.ConvStep(t(far, 1), t(1, 4), t(4, 3, 1), t(far, dtype=i32)),
+                      lambda: gdr.ConvStep(t(2, 1), t(1, 4), t(far, 3, 1), t(2, dtype=i32)),
+                      lambda: gdr.GateProblem(t(far, 1), t(1)), lambda: gdr.NormProblem(t(far, 1), None),
+                      lambda: gdr.NormProblem(t(2, far, 1), None),
+                      lambda: gdr.StepProblem(gdr.GDR_GDN, *[t(far, 1, 128, dtype=bf)] * 3, t(far, 1), t(far, 1), t(4, 1, 128, 128)),
+                      lambda: gdr.StepProblem(gdr.GDR_GDN, *one, t(1, 1), t(1, 1), t(far, 1, 128, 128), None, t(1, dtype=i32)),
+                      lambda: gdr.StepProblem(gdr.GDR_GDN, *one, t(1, 1), t(1, 1), t(4, 1, 128, 128), t(far + 1, dtype=i32))):
+            with pytest.raises(gdr.GdrError, match="32 bits") as e:
+                build()
+            assert e.value.status == 1
+
+
 def test_binding_row_checks():
     """The row checks work on any device's tensors: strides, overlaps and types."""
     import torch
