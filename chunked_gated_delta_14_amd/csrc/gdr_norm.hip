@@ -182,10 +182,25 @@ __global__ __launch_bounds__(row_threads(LPR)) void norm_fwd_kernel(NormArgs a) 
   }
 }
 
-template <class T, class R, int PLACE, bool GATE, int VEC, int LPR, int N>
+// act(z) and act'(z).  sigma' = s (1 - s) takes 1 - s to its own precision, since a gate
+// far from zero leaves little of it; SiLU' = s (1 + z (1 - s)) is of order one there.
+template <int ACT, bool EXACT>
+__device__ __forceinline__ void act_and_slope(float z, float &a, float &d) {
+  if constexpr (ACT == GDR_ACT_SILU) {
+    const float s = sigmoid<EXACT>(z);
+    a = z * s;
+    d = s * fmaf(z, 1.f - s, 1.f);
+  } else {
+    float c;
+    sigmoid_both<EXACT>(z, a, c);
+    d = a * c;
+  }
+}
+
+template <class T, class R, int PLACE, int ACT, int VEC, int LPR, int N>
 __global__ __launch_bounds__(row_threads(LPR)) void norm_bwd_kernel(NormArgs a) {
   constexpr int THREADS = row_threads(LPR), RPB = THREADS / LPR;
-  constexpr bool EXACT = sizeof(T) == 4;
+  constexpr bool EXACT = sizeof(T) == 4, GATE = ACT != GDR_ACT_NONE;
   using U = std::conditional_t<PLACE == GDR_RES_BEFORE, R, T>;  // the normed row as stored
   using Y = std::conditional_t<PLACE == GDR_RES_AFTER, R, T>;
   __shared__ float lds[2 * THREADS / 64];
@@ -206,7 +221,6 @@ __global__ __launch_bounds__(row_threads(LPR)) void norm_bwd_kernel(NormArgs a) 
 #pragma unroll
     for (int e = 0; e < VEC; ++e) dw_at(i, e) = 0.f;
   const float inv = 1.f / (float)a.D, ty = PLACE == GDR_RES_AFTER ? a.alpha : 1.f;
-  const bool silu = a.act == GDR_ACT_SILU;
   struct Row {
     Raw<U, VEC> u[N];
     Raw<Y, VEC> t[N];
@@ -255,9 +269,10 @@ __global__ __launch_bounds__(row_threads(LPR)) void norm_bwd_kernel(NormArgs a) 
         const float u = r.u[i].get(e);
         float t = r.t[i].get(e) * ty;
         if constexpr (GATE) {
-          const float zz = r.z[i].get(e), g = sigmoid<EXACT>(zz);
-          if constexpr (KEEP) tz[e] = t * (silu ? g * fmaf(zz, 1.f - g, 1.f) : g * (1.f - g));
-          t *= silu ? zz * g : g;
+          float g, dg;
+          act_and_slope<ACT, EXACT>(r.z[i].get(e), g, dg);
+          if constexpr (KEEP) tz[e] = t * dg;
+          t *= g;
           if constexpr (KEEP) ta[e] = t;
         }
         if (e >= skip) q[0] = fmaf(u, u, q[0]), q[1] = fmaf(u, t * w[i][e], q[1]);
@@ -282,9 +297,10 @@ __global__ __launch_bounds__(row_threads(LPR)) void norm_bwd_kernel(NormArgs a) 
           dz[e] = tz[e] * w[i][e] * n;
           t = ta[e];
         } else if constexpr (GATE) {
-          const float zz = r.z[i].get(e), g = sigmoid<EXACT>(zz);
-          dz[e] = t * w[i][e] * n * (silu ? g * fmaf(zz, 1.f - g, 1.f) : g * (1.f - g));
-          t *= silu ? zz * g : g;
+          float g, dg;
+          act_and_slope<ACT, EXACT>(r.z[i].get(e), g, dg);
+          dz[e] = t * w[i][e] * n * dg;
+          t *= g;
         }
         dw_at(i, e) = fmaf(t, n, dw_at(i, e));
         d[e] = k * fmaf(t, w[i][e], -u * m);
@@ -431,6 +447,10 @@ int norm_bwd_workers(const gdr_norm &p) {
   return (int)std::min<int64_t>(norm_workers(rows, p.D), blocks);
 }
 
+// The backward's activation is a compile-time value (the forward's is not: HBM hides it).
+template <int ACT>
+using Act = std::integral_constant<int, ACT>;
+
 hipError_t launch_norm_bwd(const gdr_norm &p, const void *dy, const void *ds, void *dx, int64_t dx_stride, void *dgate,
                            int64_t dgate_stride, void *dres, float *partial, int workers, hipStream_t stream) {
   if (p.T == 0) return hipSuccess;
@@ -440,9 +460,13 @@ hipError_t launch_norm_bwd(const gdr_norm &p, const void *dy, const void *ds, vo
   a.partial = partial;
   return with_types(p, [&](auto s) {
     using S = decltype(s);
-    norm_bwd_kernel<typename S::Type, typename S::Res, S::place, S::gate, S::vec, S::lpr, S::n>
-        <<<workers, S::threads, 0, stream>>>(a);
-    return hipGetLastError();
+    auto go = [&](auto act) {
+      norm_bwd_kernel<typename S::Type, typename S::Res, S::place, decltype(act)::value, S::vec, S::lpr, S::n>
+          <<<workers, S::threads, 0, stream>>>(a);
+      return hipGetLastError();
+    };
+    if constexpr (!S::gate) return go(Act<GDR_ACT_NONE>());
+    else return p.activation == GDR_ACT_SILU ? go(Act<GDR_ACT_SILU>()) : go(Act<GDR_ACT_SIGMOID>());
   });
 }
 

@@ -94,6 +94,16 @@ __device__ __forceinline__ float sigmoid(float x) {
   return __builtin_amdgcn_rcpf(1.f + fast_exp<EXACT>(-x));
 }
 
+// sigma(x) and 1 - sigma(x), either to a few roundings of itself: with e = e^-x they are
+// 1 / (1 + e) and e / (1 + e), where 1 - s would leave of a small one only the rounding of
+// s.  Where e overflows, s is 0 and so is the c given, which is of use as a factor beside s.
+template <bool EXACT>
+__device__ __forceinline__ void sigmoid_both(float x, float &s, float &c) {
+  const float e = fast_exp<EXACT>(-x);
+  s = __builtin_amdgcn_rcpf(1.f + e);
+  c = fminf(e, 0x1p126f) * s;
+}
+
 // The lane's first channel; the last group of a row whose width is no multiple of
 // VEC starts early and repeats its neighbour's channels (the same values, written
 // twice), so every access is whole.
