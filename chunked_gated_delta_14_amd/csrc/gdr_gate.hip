@@ -69,16 +69,24 @@ __device__ __forceinline__ void gate_slopes(float u, float A, float floor, float
     da = held ? 0.f : raw;
   } else {
     const float e = exp_neg_abs(A * u), r = __builtin_amdgcn_rcpf(1.f + e);
-    du = floor * A * (e * r * r);       // s (1 - s) = e / (1 + e)^2 on either side
+    // s (1 - s) = e / (1 + e)^2 on either side; floor A, like A, stays finite beside a zero
+    du = fmaxf(floor * A, -0x1.fffffep126f) * (e * r * r);
     da = du == 0.f ? 0.f : du * u;      // the slope vanished: u itself may be infinite
   }
+}
+
+// A = e^a, cut at half of fp32's largest value: an infinite A times a softplus of zero, or
+// times u = 0, would be NaN where g is the floor, or half of it.  A NaN passes.
+__device__ __forceinline__ float rate(float a) {
+  const float A = fast_exp<true>(a);
+  return A > 0x1.fffffep126f ? 0x1.fffffep126f : A;
 }
 
 template <int VEC>
 __device__ __forceinline__ void load_params(const GateArgs &p, int c, float (&A)[VEC], float (&b)[VEC]) {
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
-    A[e] = fast_exp<true>(p.a[p.D == 1 ? c + e : (c + e) >> 7]);
+    A[e] = rate(p.a[p.D == 1 ? c + e : (c + e) >> 7]);
     b[e] = p.b ? p.b[c + e] : 0.f;
   }
 }

@@ -326,7 +326,8 @@ int32_t gdr_conv_step(const gdr_conv *p, void *y, int64_t y_stride, void *state,
  *     u = x + bias,   A = exp(a_log)
  *     GDR_GATE_SOFTPLUS:  g = max(floor, -A softplus(u))
  *     GDR_GATE_SIGMOID:   g = floor * sigmoid(A u)
- * with a_log one value per head and bias one per channel.  floor in [-8, 0): both
+ * with a_log one value per head and bias one per channel; A is cut at 2^127, half of
+ * fp32's range.  floor in [-8, 0): both
  * kinds then meet the recurrence's precondition on g.  D is 128 for KDA's g and 1
  * for GDN's. */
 enum gdr_gate_kind { GDR_GATE_SOFTPLUS = 0, GDR_GATE_SIGMOID = 1 };

@@ -39,3 +39,26 @@ def test_norm_gate_far_from_zero(D, dt, place):
     want = f64(dy) * (alpha if place == "after" else 1.0) * f64(w) * n * ref.sig(zz) * ref.sig(-zz)
     e = 4 + (1.5 * np.abs(zz) if dt == "bf16" else 0)
     ref.close(dz, want, np.abs(want) * ((e + 3) + (2 * e + 4) + 1 + 16 + 4), dtype, "dz")
+
+
+@pytest.mark.parametrize("D", [1, 128])
+@pytest.mark.parametrize("kind", ["softplus", "sigmoid"])
+def test_gate_rates_past_the_range(kind, D):
+    """e^a near and past fp32's largest value: the floor (softplus), or a step at u = 0 (sigmoid), and no slope beside it."""
+    g = gdr()
+    a = torch.tensor([88.0, 88.5, 89.0, 300.0, float("inf")], device="cuda")
+    u = torch.tensor([-50.0, -1.0, -1e-6, 0.0, 1e-6, 3.0, 40.0], device="cuda")
+    H, T = len(a), len(u)
+    x = u[:, None].expand(T, H * D).contiguous()
+    print("[case] gate rates", kind, D, flush=True)
+    p = g.GateProblem(x, a, None, g.GDR_GATE_SOFTPLUS if kind == "softplus" else g.GDR_GATE_SIGMOID, -5.0)
+    out, dx, da, db = nan((T, H * D), F32), nan((T, H * D), F32), nan((H,), F32), nan((H * D,), F32)
+    g.gate_fwd(p, out)
+    dg = torch.ones(T, H * D, device="cuda")
+    dg[3] = 0.0 if kind == "sigmoid" else 1.0  # the step itself: a slope of -5 A / 4, past the range
+    g.gate_bwd(p, dg, dx, da, db, p.alloc_workspace())
+    torch.cuda.synchronize()
+    want = torch.full((T,), -5.0) if kind == "softplus" else torch.tensor([0.0, 0.0, 0.0, -2.5, -5.0, -5.0, -5.0])
+    assert torch.equal(out.cpu(), want[:, None].expand(T, H * D)), out
+    for t in (dx, da, db):
+        assert not t.any(), t
