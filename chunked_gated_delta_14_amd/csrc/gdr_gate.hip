@@ -218,34 +218,30 @@ hipError_t with_flags(int kind, bool uniform, F f) {
     return uniform ? f(t, v, Int<GDR_GATE_SOFTPLUS>(), Int<1>()) : f(t, v, Int<GDR_GATE_SOFTPLUS>(), Int<0>());
   return uniform ? f(t, v, Int<GDR_GATE_SIGMOID>(), Int<1>()) : f(t, v, Int<GDR_GATE_SIGMOID>(), Int<0>());
 }
-template <int BF_VEC, class F>
+template <int VEC, class F>
 hipError_t with_types(const gdr_gate &p, int vec, bool uniform, F f) {
-  if (p.dtype == GDR_BF16) return vec == 1 ? with_flags<u16, 1>(p.kind, uniform, f) : with_flags<u16, BF_VEC>(p.kind, uniform, f);
-  return vec == 1 ? with_flags<float, 1>(p.kind, uniform, f) : with_flags<float, GATE_VEC>(p.kind, uniform, f);
+  if (p.dtype == GDR_BF16) return vec == 1 ? with_flags<u16, 1>(p.kind, uniform, f) : with_flags<u16, VEC>(p.kind, uniform, f);
+  return vec == 1 ? with_flags<float, 1>(p.kind, uniform, f) : with_flags<float, VEC>(p.kind, uniform, f);
 }
 
-// Channels per thread of the forward.  From bf16, 4: a wavefront's stores then cover
-// whole lines one after the other ([261392, 2048] 625 us, with 8 channels 701 us).
-// From fp32, 8: twice the bytes in flight ([100000, 2048] 324 us, with 4 359 us).  All
-// four measured before a block's rows lay side by side.
-int fwd_vec(int C, int dtype) {
-  const int v = dtype == GDR_BF16 ? 4 : GATE_VEC;
-  return C >= v ? v : 1;
-}
+// Channels per thread of the forward: a wavefront's stores then cover whole lines one
+// after the other (bf16 [261392, 2048] 581 us, with 8 channels 678; fp32 [100000, 2048]
+// 289 us, with 8 310).
+constexpr int FWD_VEC = 4;
 
 }  // namespace
 
 hipError_t launch_gate_fwd(const gdr_gate &p, float *g, hipStream_t stream) {
   if (p.T == 0) return hipSuccess;
   const int C = p.H * p.D;
-  const int vec = fwd_vec(C, p.dtype);
+  const int vec = C >= FWD_VEC ? FWD_VEC : 1;
   const Lanes l = lanes_for(groups_of(C, vec));
   // up to 4M threads: few rows each, no sums to share ([261392, 2048] 580 us; 0.5M 616,
   // 0.25M 603, 0.125M 830)
   const int workers = workers_for(((int64_t)p.T + U - 1) / U, l, 1 << 22);
   const GateArgs a = args_of(p, l);
   const unsigned blocks = (unsigned)(workers / l.ly * l.nchb);
-  return with_types<4>(p, vec, l.uniform, [&](auto t, auto v, auto k, auto u) {
+  return with_types<FWD_VEC>(p, vec, l.uniform, [&](auto t, auto v, auto k, auto u) {
     using T = decltype(t);
     gate_fwd_kernel<T, decltype(v)::value, decltype(k)::value, decltype(u)::value><<<blocks, l.threads, 0, stream>>>(a, workers, g);
     return hipGetLastError();

@@ -130,10 +130,9 @@ inline ConvBwdPlan conv_bwd_plan(int n_chunks, int C) {
 constexpr int GATE_VEC = 8;
 inline int gate_vec(int C) { return C >= GATE_VEC ? GATE_VEC : 1; }
 inline Lanes gate_lanes(int C) { return lanes_for(groups_of(C, gate_vec(C))); }
-// Workers: 131072 threads ([261392, 2048], before a block's rows lay side by side, 865
-// us; 65536 or 262144 threads 931 and 905), for rows narrower than a wavefront twice
-// that ([241817, 48] 32 us, not 37: their blocks add up more sets, so the partials
-// stay few).
+// Workers: 131072 threads ([261392, 2048] 799 us; 65536 or 262144 threads 935 and 824),
+// for rows narrower than a wavefront twice that ([241817, 48] 36.0 us; half of it 38.3,
+// twice 36.0: their blocks add up more sets, so the partials stay few).
 inline int gate_rows(int64_t T, int C) {
   const Lanes l = gate_lanes(C);
   return workers_for((T + 7) / 8, l, l.lx < 64 ? 262144 : 131072) / l.ly;
