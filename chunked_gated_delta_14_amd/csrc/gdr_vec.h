@@ -77,8 +77,13 @@ __device__ __forceinline__ float ld_param(const void *p, int64_t i, bool bf) {
 }
 
 // e^x by the hardware's 2^t.  With EXACT the rounding error of t = x log2(e), which
-// grows with |x|, is carried into the result (fp32 outputs); without, it costs a
-// relative |x| 2^-24, below a bf16 output's half step for every |x| < 88.
+// grows with |x|, is carried into the result; without, it costs a relative |x| 2^-24.
+// The convolution and the norm take EXACT for fp32 rows.  For bf16 rows they do not, also
+// where an output is fp32 (the parameter sums, and y or dres beside an fp32 residual):
+// the error stays below a bf16 half step for every |x| < 88, it is random from value to
+// value, so a sum averages it, and the correction would cost the backwards what they
+// have left of the vector units (convolution [241817, 6144] 1968 us, without 1792; gated
+// norm [4000, 10240] with an fp32 stream 199 us, without 164).
 template <bool EXACT>
 __device__ __forceinline__ float fast_exp(float x) {
   const float t = x * 1.44269504088896341f;

@@ -310,3 +310,20 @@ def test_norm_of_many_passes_is_exact(T, H, D, dt, rdt, place, gated):
         assert torch.equal(dres, d.to(rtype))
         d = alpha * d
     assert torch.equal(dx, d.to(dtype))
+
+
+def test_partial_rows_are_added_without_loss():
+    """The workers' partial sums may differ by more than fp32 holds: one of 2^24 beside 198 of 1, each exact in its run of
+    64 tokens, add up to what fp32 holds, 2^24 + 198."""
+    g, C, runs = gdr(), 2048, 200
+    assert conv_workers(runs, C, 2) == (runs, 1)  # a run for each worker, a partial row for each run
+    T = 64 * runs
+    dy = torch.zeros(T, C, device="cuda")
+    dy[37::64] = 1.0
+    dy[64 * 77 + 37], dy[64 * 5 + 37] = 2.0 ** 24, 0.0
+    p = g.ConvProblem(torch.ones(T, C, device="cuda"), torch.zeros(C, 2, device="cuda"), g.Plan([0, T]), None, None, g.GDR_ACT_NONE)
+    print("[case] partial rows", flush=True)
+    dx, dw, db = nan((T, C), F32), nan((C, 2), F32), nan((C,), F32)
+    g.conv_bwd(p, dy, None, dx, dw, db, None, p.alloc_workspace())
+    torch.cuda.synchronize()
+    assert bool((db == 2.0 ** 24 + 198).all()) and bool((dw == 2.0 ** 24 + 198).all())
