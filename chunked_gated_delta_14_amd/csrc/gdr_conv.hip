@@ -10,8 +10,8 @@
 //
 // Bound by HBM: about 17 (forward) and 34 (backward) lane operations a value against
 // 4 and 6 bytes keep the vector units 0.6 and 0.8 busy.  W = 4, SiLU, bf16, on a card
-// that copies 5.1 TB/s: forward [261392, 2048] 364 us, 6.0 TB/s; backward [241817,
-// 6144] 1771 us, 5.2 TB/s, each with the 7 % that run starts read again.  Nothing is
+// that copies 5.1 TB/s: forward [261392, 2048] 362 us, 6.0 TB/s; backward [241817,
+// 6144] 1781 us, 5.2 TB/s, each with the 7 % that run starts read again.  Nothing is
 // kept for the backward, since z costs less to form again than to read.
 #include "gdr_layer.h"
 #include "gdr_vec.h"
@@ -379,7 +379,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int R, int nw
     for (int e = 0; e < VEC; ++e) p[(int64_t)i * a.C + e] = v[i * VEC + e];
 }
 
-// One token per sequence ([64, 10240] 4.5 us, the latency of slot, state and store):
+// One token per sequence ([64, 10240] 4.4 us, the latency of slot, state and store):
 // the W-1 rows of the sequence's slot and the new row give
 // y; the slot keeps the last W-1 rows.  Rows whose slot lies outside the pool are
 // left alone.

@@ -9,7 +9,7 @@
 //   du = rs (v - u rs^2 mean(v u)),  before: du += ds, dres = du, dx = alpha du
 // sum u^2 and sum v u come out of one pass, so a row is read once and held in
 // registers; rs is formed again in the backward rather than kept.  Bound by HBM: heads
-// with a gate, [4182272, 128] bf16, forward 599 us, 5.4 TB/s; residual [32674, 2048]
+// with a gate, [4182272, 128] bf16, forward 598 us, 5.4 TB/s; residual [32674, 2048]
 // with an fp32 stream 144 us forward and 194 us backward, 5.6 TB/s, on a card that
 // copies 5.1 TB/s.
 #include "gdr_layer.h"

@@ -8,7 +8,7 @@
 // (rg, qd) = (lane / 8, lane % 8) holds keys 16 rg .. +15 of columns 4 qd .. +3 in
 // 64 registers, every load and store of a key's 32 columns covers a 128-byte line,
 // and the reduction runs over the 8 lane groups.  Bound by the state's read and
-// write, 2 x 64 KB per sequence and head: 256 sequences of 48 heads 318 us, 5.1 TB/s,
+// write, 2 x 64 KB per sequence and head: 256 sequences of 48 heads 317 us, 5.1 TB/s,
 // what a copy reaches on that card; one sequence of 16 heads 4.4 us, its loads' latency.
 #include "gdr_layer.h"
 #include "gdr_vec.h"
