@@ -327,3 +327,110 @@ def test_partial_rows_are_added_without_loss():
     g.conv_bwd(p, dy, None, dx, dw, db, None, p.alloc_workspace())
     torch.cuda.synchronize()
     assert bool((db == 2.0 ** 24 + 198).all()) and bool((dw == 2.0 ** 24 + 198).all())
+
+
+@pytest.mark.parametrize("C,W,dt", [(24, 4, "bf16"), (5, 8, "f32"), (260, 2, "bf16")])
+def test_conv_of_tiny_documents_is_exact(C, W, dt):
+    """Twenty thousand documents of 0 to 5 tokens, most of them shorter than the history: whole numbers again."""
+    g, r, dtype, N, H = gdr(), rng(C), DT[dt], 20011, W - 1
+    lens = r.integers(0, 6, N)
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    T = int(cu[-1])
+    x, dy, w, b = ints(r, (T, C), 3, dtype), ints(r, (T, C), 3, dtype), ints(r, (C, W), 2, dtype), ints(r, (C,), 3, dtype)
+    s0, dst = ints(r, (N, H, C), 3, dtype), ints(r, (N, H, C), 3, dtype)
+    print("[case] tiny documents", C, W, dt, flush=True)
+    p = g.ConvProblem(x, w, g.Plan(cu), b, s0, g.GDR_ACT_NONE)
+    y, st, dx, ds0 = nan((T, C), dtype), nan((N, H, C), dtype), nan((T, C), dtype), nan((N, H, C), dtype)
+    dw, db = nan((C, W), F32), nan((C,), F32)
+    g.conv_fwd(p, y, st)
+    g.conv_bwd(p, dy, dst, dx, dw, db, ds0, p.alloc_workspace().fill_(0xFF))
+    torch.cuda.synchronize()
+    # all documents laid out one after the other, each with its history before it
+    L = torch.from_numpy(lens).cuda()
+    start = torch.from_numpy(cu[:-1]).cuda().long() + torch.arange(N, device="cuda") * H  # of a document's history
+    at = torch.arange(T, device="cuda") + torch.repeat_interleave(torch.arange(N, device="cuda"), L) * H + H  # of a token
+    hist = start[:, None] + torch.arange(H, device="cuda")
+    X = torch.zeros(T + N * H, C, device="cuda")
+    X[at], X[hist] = x.float(), s0.float()
+    dX, wf, d = torch.zeros_like(X), w.float(), dy.float()
+    z = b.float().expand(T, C).clone()
+    for i in range(W):
+        z += wf[:, i] * X[at - H + i]
+        dX[at - H + i] += d * wf[:, i]  # the rows of one tap are distinct
+        assert torch.equal(dw[:, i].double(), (d * X[at - H + i]).sum(0, dtype=torch.float64)), i
+    tail = hist + L[:, None]
+    dX[tail] += dst.float()
+    assert torch.equal(y.float(), z) and torch.equal(st.float(), X[tail])
+    assert torch.equal(dx.float(), dX[at]) and torch.equal(ds0.float(), dX[hist])
+    assert torch.equal(db.double(), d.sum(0, dtype=torch.float64))
+
+
+def test_widest_rows():
+    """Channels, heads and states at the largest counts that the checks take."""
+    g, r = gdr(), rng(4)
+    C, W, docs = 1 << 24, 6, (2, 0, 1)  # 32 (W + 1) C just below 2^32
+    T = sum(docs)
+    x, dy, w = ints(r, (T, C), 3), ints(r, (T, C), 3), ints(r, (C, W), 2)
+    print("[case] widest convolution", flush=True)
+    p = g.ConvProblem(x, w, g.Plan(cu_of(docs)), None, None, g.GDR_ACT_NONE)
+    y, dx, dw, db = nan((T, C), F32), nan((T, C), F32), nan((C, W), F32), nan((C,), F32)
+    g.conv_fwd(p, y)
+    g.conv_bwd(p, dy, None, dx, dw, db, None, p.alloc_workspace())
+    torch.cuda.synchronize()
+    assert torch.equal(y[0], w[:, 5] * x[0]) and torch.equal(y[2], w[:, 5] * x[2])
+    assert torch.equal(y[1], w[:, 5] * x[1] + w[:, 4] * x[0])
+    assert torch.equal(dx[0], w[:, 5] * dy[0] + w[:, 4] * dy[1]) and torch.equal(dx[1:], w[:, 5] * dy[1:])
+    assert torch.equal(dw[:, 5], (x * dy).sum(0)) and torch.equal(dw[:, 4], x[0] * dy[1]) and not dw[:, :4].any()
+    assert torch.equal(db, dy.sum(0))
+    del x, dy, w, p, y, dx, dw, db
+    H, T = 65536, 5
+    print("[case] most gate heads", flush=True)
+    row = torch.randn(H * 128, device="cuda").to(BF)
+    dg = ints(r, (T, H * 128), 3, step=4)
+    q = g.GateProblem(row.expand(T, -1).contiguous(), torch.zeros(H, device="cuda"), -row.float(), g.GDR_GATE_SIGMOID, -5.0)
+    out, dx, da, db = nan((T, H * 128), F32), nan((T, H * 128), BF), nan((H,), F32), nan((H * 128,), F32)
+    g.gate_fwd(q, out)
+    g.gate_bwd(q, dg, dx, da, db, q.alloc_workspace())
+    torch.cuda.synchronize()
+    assert bool((out == -2.5).all()) and torch.equal(dx.float(), -1.25 * dg) and torch.equal(db, -1.25 * dg.sum(0)) and not da.any()
+    del row, dg, q, out, dx, da, db
+    print("[case] most state heads", flush=True)
+    k, v = torch.randn(1, 1, 128, device="cuda").to(BF), torch.randn(1, H, 128, device="cuda").to(BF)
+    beta, decay = torch.rand(1, H, device="cuda"), -torch.rand(1, H, device="cuda")
+    state, some = torch.randn(1, H, 128, 128, device="cuda"), [0, 1, 32767, 65535]
+    few = state[:, some].contiguous()
+    o, want = nan(v.shape, BF), nan((1, 4, 128), BF)
+    g.gdn_step(g.StepProblem(g.GDR_GDN, k, k, v, decay, beta, state), o)
+    g.gdn_step(g.StepProblem(g.GDR_GDN, k, k, v[:, some].contiguous(), decay[:, some].contiguous(), beta[:, some].contiguous(), few), want)
+    torch.cuda.synchronize()
+    assert torch.equal(o[:, some], want) and torch.equal(state[:, some], few) and bool(torch.isfinite(o.float()).all())
+
+
+@pytest.mark.parametrize("place", ["none", "before", "after"])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_norm_at_the_borders_of_its_shapes(dt, place):
+    """Widths on either side of every row shape's last value, with a gate, both ways."""
+    g, dtype = gdr(), DT[dt]
+    vec, alpha = 8 if dt == "bf16" else 4, 0.5 if place != "none" else 1.0
+    ends = [vec] + [t * vec for t in (16, 32, 64, 128, 192, 256, 512, 768, 1024, 1280, 1536, 2048)] + [16384]
+    widths = sorted({D for e in ends for D in (e - 1, e, e + 1) if 2 <= D <= 16384})
+    code = {"none": g.GDR_RES_NONE, "before": g.GDR_RES_BEFORE, "after": g.GDR_RES_AFTER}[place]
+    for D in widths:
+        r, shape, act = rng(D), (5, 1, D), ("silu", "sigmoid")[D & 1]
+        print("[case] norm border", dt, place, D, flush=True)
+        x, z, dy = (dev(r.standard_normal(shape), dtype) for _ in range(3))
+        w = dev(1 + 0.2 * r.standard_normal(D))
+        res = dev(r.standard_normal(shape)) if place != "none" else None
+        s, ydt = nan(shape, F32) if place == "before" else None, F32 if place == "after" else dtype
+        dy = dy.to(ydt)
+        p = g.NormProblem(x, w, z, g.GDR_ACT_SILU if act == "silu" else g.GDR_ACT_SIGMOID, res, s, code, alpha)
+        y, dx, dz, dw = nan(shape, ydt), nan(shape, dtype), nan(shape, dtype), nan((D,), F32)
+        dres = nan(shape, F32) if place == "before" else None
+        g.norm_fwd(p, y)
+        g.norm_bwd(p, dy, dx, dw, p.alloc_workspace().fill_(0xFF), dgate=dz, dres=dres)
+        torch.cuda.synchronize()
+        f = ref.norm(f64(x), f64(w), f64(z), f64(res), place, act, alpha, 1e-6)
+        d = ref.norm_grad(f64(s) if s is not None else f64(x), f64(w), f64(z), f64(dy), None, place, act, alpha, 1e-6)
+        ref.close(y, f["y"], f["Ey"], ydt, "y %d" % D)
+        for name, t, odt in (("dx", dx, dtype), ("dz", dz, dtype), ("dw", dw, F32)) + ((("dres", dres, F32),) if dres is not None else ()):
+            ref.close(t, d[name], d["E" + name], odt, "%s %d" % (name, D))
