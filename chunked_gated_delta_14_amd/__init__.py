@@ -24,6 +24,9 @@ __all__ = [
     "GDR_RES_NONE", "GDR_RES_BEFORE", "GDR_RES_AFTER", "Plan", "ConvProblem", "conv_fwd", "conv_bwd", "conv_workspace_bytes",
     "ConvStep", "conv_step", "GateProblem", "gate_fwd", "gate_bwd", "gate_workspace_bytes", "StepProblem", "kda_step",
     "gdn_step", "NormProblem", "norm_fwd", "norm_bwd", "norm_workspace_bytes",
+    "GDR_ROPE_HALF", "GDR_ROPE_PAIRS", "GDR_ROPE_PLAIN", "GDR_ROPE_LINEAR", "GDR_ROPE_BASE", "GDR_ROPE_BLEND", "rope_freqs",
+    "RopeProblem", "rope_fwd", "rope_bwd", "AttnPlan", "AttnProblem", "attn_fwd", "attn_bwd", "attn_workspace_bytes", "KvCache",
+    "KvProblem", "kv_store", "kv_load", "AttnStep", "attn_step", "attn_step_workspace_bytes",
 ]
 
 GDR_KDA = 0
@@ -42,6 +45,8 @@ EXPORTED_SYMBOLS = (
     "gdr_kda_ckpt_noalloc",
     "gdr_conv_fwd", "gdr_conv_bwd", "gdr_conv_step", "gdr_conv_workspace_bytes", "gdr_gate_fwd", "gdr_gate_bwd",
     "gdr_gate_workspace_bytes", "gdr_kda_step", "gdr_gdn_step", "gdr_norm_fwd", "gdr_norm_bwd", "gdr_norm_workspace_bytes",
+    "gdr_rope_freqs", "gdr_rope_fwd", "gdr_rope_bwd", "gdr_plan_attn", "gdr_attn_fwd", "gdr_attn_bwd", "gdr_attn_workspace_bytes",
+    "gdr_kv_store", "gdr_kv_load", "gdr_attn_step_fwd", "gdr_attn_step_workspace_bytes",
 )
 GDR_NOALLOC_SCRATCH_BYTES = 64 << 20  # the static workspace of gdr_kda_ckpt_noalloc
 
@@ -113,6 +118,7 @@ def lib():
             L.gdr_last_error.argtypes = []
             L.gdr_last_error.restype = ctypes.c_char_p
             layer.declare(L)
+            attn.declare(L)
             _lib = L
     return _lib
 
@@ -307,4 +313,10 @@ from .layer import (  # noqa: E402,F401
     GDR_RES_BEFORE, GDR_RES_NONE, ConvProblem, ConvStep, GateProblem, NormProblem, Plan, StepProblem, conv_bwd, conv_fwd,
     conv_step, conv_workspace_bytes, gate_bwd, gate_fwd, gate_workspace_bytes, gdn_step, kda_step, norm_bwd, norm_fwd,
     norm_workspace_bytes,
+)
+from . import attn  # noqa: E402  (the binding of the attention layers' operators)
+from .attn import (  # noqa: E402,F401
+    GDR_ROPE_BASE, GDR_ROPE_BLEND, GDR_ROPE_HALF, GDR_ROPE_LINEAR, GDR_ROPE_PAIRS, GDR_ROPE_PLAIN, AttnPlan, AttnProblem,
+    AttnStep, KvCache, KvProblem, RopeProblem, attn_bwd, attn_fwd, attn_step, attn_step_workspace_bytes, attn_workspace_bytes,
+    kv_load, kv_store, rope_bwd, rope_freqs, rope_fwd,
 )

@@ -12,8 +12,10 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libgdr.so")
 SOURCES = ["gdr_api.cpp", "gdr_fwd.hip", "gdr_bwd.hip", "gdr_layer_api.cpp", "gdr_conv.hip", "gdr_gate.hip", "gdr_step.hip",
-           "gdr_norm.hip", "gdr_psum.hip"]
-HEADERS = ["gdr_device.h", "gdr_kernels.h", "gdr_walk.h", "gdr_host.h", "gdr_layer.h", "gdr_vec.h"]
+           "gdr_norm.hip", "gdr_psum.hip", "gdr_attn_api.cpp", "gdr_rope.hip", "gdr_attn_fwd.hip", "gdr_attn_bwd.hip", "gdr_kv.hip",
+           "gdr_attn_step.hip"]
+HEADERS = ["gdr_device.h", "gdr_kernels.h", "gdr_walk.h", "gdr_host.h", "gdr_layer.h", "gdr_vec.h",
+           "gdr_check.h", "gdr_attn.h", "gdr_attn_device.h"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -276,7 +276,9 @@ struct Timing {
 };
 const char *const kKernelNames[gdr::TK_COUNT] = {"fwd_prep", "fwd_walk", "bwd_walk",  "bwd_grad", "conv_fwd",
                                                  "conv_bwd", "conv_step", "gate_fwd", "gate_bwd", "step",
-                                                 "norm_fwd", "norm_bwd", "param_sum"};
+                                                 "norm_fwd", "norm_bwd", "param_sum", "rope", "attn_fwd",
+                                                 "attn_dq", "attn_dkv", "kv_store", "kv_load", "attn_step",
+                                                 "attn_join"};
 Timing &timing() {
   static Timing t;
   return t;

@@ -11,6 +11,7 @@ namespace gdr {
 enum TimedKernel {
   TK_FWD_PREP, TK_FWD_WALK, TK_BWD_WALK, TK_BWD_GRAD,
   TK_CONV_FWD, TK_CONV_BWD, TK_CONV_STEP, TK_GATE_FWD, TK_GATE_BWD, TK_STEP, TK_NORM_FWD, TK_NORM_BWD, TK_PARAM_SUM,
+  TK_ROPE, TK_ATTN_FWD, TK_ATTN_DQ, TK_ATTN_DKV, TK_KV_STORE, TK_KV_LOAD, TK_ATTN_STEP, TK_ATTN_JOIN,
   TK_COUNT
 };
 

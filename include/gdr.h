@@ -412,6 +412,143 @@ int32_t gdr_norm_bwd(const gdr_norm *p, const void *dy, const void *ds, void *dx
                      int64_t dgate_stride, void *dres, float *dweight, void *workspace, int64_t workspace_bytes,
                      void *stream);
 
+/* -------------------------------------------------------------------------
+ * The softmax-attention layers that stand between gated delta-rule layers:
+ * rotary positions, attention over the same packed documents, and a cache held
+ * in 4 bits with the attention of new tokens over it.  The conventions of the
+ * operators around the recurrence hold, with two exceptions: rotary positions
+ * may be applied in place, and attention's rows are 16-byte aligned.
+ * ------------------------------------------------------------------------- */
+
+/* Rotary positions.  For pair i of the first `rot` channels of every head, at the
+ * angle p f_i of the token's position p, with f_i = freqs[i] turns a token:
+ *     (a, b) -> magnitude (a cos - b sin, b cos + a sin)
+ * GDR_ROPE_HALF pairs channels (i, i + rot/2), GDR_ROPE_PAIRS (2i, 2i + 1); channels
+ * from rot on pass unchanged.  Angles are reduced in fp64, so far positions keep
+ * their precision.  An output may have its input's address and stride (in place:
+ * only the rotated channels are then touched); other overlaps are the caller's. */
+enum gdr_rope_layout { GDR_ROPE_HALF = 0, GDR_ROPE_PAIRS = 1 };
+typedef struct gdr_rope {
+  int32_t T, N;         /* tokens; documents of chunk_table (0 with positions) */
+  int32_t H_q, H_k, D;  /* heads of q and of k (either may be 0), channels a head, D <= 1024 */
+  int32_t rot;          /* rotated channels: even, 2 <= rot <= D */
+  int32_t dtype;        /* gdr_dtype of q, k and their gradients */
+  int32_t layout;       /* gdr_rope_layout */
+  int32_t n_chunks;     /* of chunk_table */
+  float magnitude;
+  int64_t q_stride, k_stride;
+  const void *q, *k;            /* [T, H_q, D], [T, H_k, D]; not read by the backward */
+  const int32_t *positions;     /* device int32 [T], or NULL: the token's place in its document */
+  const int32_t *chunk_table;   /* device copy of the gdr_plan_chunks table (positions NULL) */
+  const double *freqs;          /* device [rot / 2], turns a token */
+} gdr_rope;
+
+/* Frequencies of a rope of `rot` channels, to host memory, in turns a token (radians / 2 pi):
+ *     GDR_ROPE_PLAIN:  f_i = base^(-2i/rot)
+ *     GDR_ROPE_LINEAR: f_i / factor
+ *     GDR_ROPE_BASE:   base * factor^(rot/(rot-2)) in base's place (rot = 2: as plain)
+ *     GDR_ROPE_BLEND:  f_i ((1 - c) / factor + c),  c = clamp((r - low) / (high - low), 0, 1),
+ *                      r = original f_i / 2 pi, the turns within the original context
+ * The scalings differ in nothing else; a magnitude that goes with one is the caller's. */
+enum gdr_rope_scaling { GDR_ROPE_PLAIN = 0, GDR_ROPE_LINEAR = 1, GDR_ROPE_BASE = 2, GDR_ROPE_BLEND = 3 };
+int32_t gdr_rope_freqs(int32_t rot, double base, int32_t scaling, double factor, double original, double low, double high,
+                       double *freqs);
+
+/* q_out, k_out: as q and k; each may be NULL where its head count is 0. */
+int32_t gdr_rope_fwd(const gdr_rope *p, void *q_out, int64_t q_out_stride, void *k_out, int64_t k_out_stride, void *stream);
+/* dq_out, dk_out: gradients of the outputs; writes dq, dk (the rotation by the negative angle). */
+int32_t gdr_rope_bwd(const gdr_rope *p, const void *dq_out, int64_t dq_out_stride, const void *dk_out, int64_t dk_out_stride,
+                     void *dq, int64_t dq_stride, void *dk, int64_t dk_stride, void *stream);
+
+/* Softmax attention over packed documents at head dim 128, forward and backward.
+ * Document n holds queries cu_q[n] .. cu_q[n+1] - 1 and keys cu_k[n] .. cu_k[n+1] - 1;
+ * with Lq and Lk of them, row i stands at p = i + Lk - Lq among the keys and sees key j if
+ *     j <= p (causal),   j > p - window (window > 0, causal only),
+ * every key of the document without `causal`.  Query head h reads kv head h / (H_q / H_kv).
+ *     o_i = sum_j P_ij v_j,   P_ij = exp(scale q_i k_j - lse_i),   lse_i = log sum_j exp(scale q_i k_j)
+ * A row that sees no key has o = 0 and lse = -inf, and its gradients are zero.
+ * Probabilities and their gradients are rounded to bf16 for the matrix products, which
+ * sum in fp32.  Rows start 16-byte aligned (strides are multiples of 8).  A hidden key
+ * or value does not reach a row's forward output, finite or not; the backward takes finite operands: a
+ * value that is not may reach gradients up to 127 rows or keys away in its document.
+ *
+ * gdr_plan_attn: host planner of the tiles, the longest first.  cu_k NULL: cu_q's.
+ * A first call with table NULL gives *table_len (int32s), *n_q_tiles and *n_k_tiles.
+ * The table depends on causal and window; the problem has the same ones. */
+int32_t gdr_plan_attn(const int32_t *cu_q, const int32_t *cu_k, int32_t N, int32_t causal, int32_t window, int32_t *table,
+                      int64_t capacity, int32_t *n_q_tiles, int32_t *n_k_tiles, int64_t *table_len);
+
+typedef struct gdr_attn {
+  int32_t T_q, T_k, N;
+  int32_t H_q, H_kv, D;      /* D == 128 */
+  int32_t causal, window;    /* window 0: none */
+  int32_t n_q_tiles, n_k_tiles;
+  float scale;
+  int64_t q_stride, k_stride, v_stride;
+  const uint16_t *q;         /* bf16 [T_q, H_q, D] */
+  const uint16_t *k, *v;     /* bf16 [T_k, H_kv, D] */
+  const int32_t *tile_table; /* device copy of the gdr_plan_attn table */
+} gdr_attn;
+
+/* o: bf16 [T_q, H_q, D]; lse: fp32 [H_q, T_q], or NULL to skip. */
+int32_t gdr_attn_fwd(const gdr_attn *p, uint16_t *o, float *lse, void *stream);
+int64_t gdr_attn_workspace_bytes(int32_t T_q, int32_t T_k, int32_t n_k_tiles, int32_t H_q, int32_t H_kv);
+/* o, lse: as the forward wrote them; dout: bf16 [T_q, H_q, D].  Writes dq [T_q, H_q, D] and
+ * dk, dv [T_k, H_kv, D] (bf16; dk and dv sum over the query heads of a kv head in fp32).
+ * No atomics: results repeat bit for bit. */
+int32_t gdr_attn_bwd(const gdr_attn *p, const uint16_t *o, const float *lse, const uint16_t *dout, uint16_t *dq,
+                     int64_t dq_stride, uint16_t *dk, int64_t dk_stride, uint16_t *dv, int64_t dv_stride, void *workspace,
+                     int64_t workspace_bytes, void *stream);
+
+/* Keys and values held in 4 bits, in pages.  32 neighbouring channels of a token and head
+ * share a power of two 2^e, the smallest with max|x| <= 6 2^e (e >= -126); each is stored as the nearest of
+ * 0, 0.5, 1, 1.5, 2, 3, 4, 6 times it, ties to the even code, with its sign.  A code byte
+ * holds an even channel in its low half and the next in its high half: bit 3 the sign, bits 0..2 the
+ * value's place in that list.  (With e = 126, magnitudes past 3 2^126 are stored as that: 2^128 is past
+ * bf16.)  A scale byte holds e + 127; 255 marks 32 channels of which one
+ * was infinite or NaN, and they read as NaN.  A page holds `page` tokens of all kv heads. */
+typedef struct gdr_kv {
+  int32_t n_pages, page; /* pages in the pool; tokens a page: 16, 32, 64, 128 or 256 */
+  int32_t H_kv, D;       /* D == 128 */
+  int32_t N, max_pages;  /* sequences; columns of page_table */
+  uint8_t *k_codes, *v_codes; /* [n_pages, H_kv, page, 64], 16-byte aligned */
+  uint8_t *k_scale, *v_scale; /* [n_pages, H_kv, page, 4], 16-byte aligned */
+  const int32_t *page_table;  /* device int32 [N, max_pages]: the page of tokens page * c .. of sequence n */
+} gdr_kv;
+
+/* Tokens cu_seqlens[n] .. cu_seqlens[n+1] - 1 of k and v (or token n, when cu_seqlens is
+ * NULL and T == N) are tokens start[n], start[n] + 1, .. of sequence n.  gdr_kv_store
+ * writes them to the cache, gdr_kv_load reads them back as bf16.  start NULL: zeros.
+ * cu_seqlens is clipped to [0, T].  Tokens that no sequence covers, whose place is negative or past
+ * max_pages, or whose page lies outside [0, n_pages), are skipped: nothing is stored,
+ * and the row of k and v is left as it was.  Two tokens stored to one place race.
+ * k, v: bf16 [T, H_kv, D]. */
+int32_t gdr_kv_store(const gdr_kv *p, int32_t T, const int32_t *cu_seqlens, const int32_t *start, const uint16_t *k,
+                     int64_t k_stride, const uint16_t *v, int64_t v_stride, void *stream);
+int32_t gdr_kv_load(const gdr_kv *p, int32_t T, const int32_t *cu_seqlens, const int32_t *start, uint16_t *k,
+                    int64_t k_stride, uint16_t *v, int64_t v_stride, void *stream);
+
+/* Attention of each sequence's last tokens over its cache: single tokens, or short runs.
+ * Sequence n takes rows cu_seqlens[n] .. cu_seqlens[n+1] - 1 of q (row n when cu_seqlens is
+ * NULL; T == N) and holds lens[n] tokens, the rows' own among them (stored before the call):
+ * the last row sees all of them, the one before all but the last, and so on, each within
+ * `window` tokens up to its own (0: all).  lens is clipped to [0, max_pages * page] and
+ * cu_seqlens to [0, T].  Keys of a page outside [0, n_pages) are hidden.  A row that sees no key gets 0;
+ * rows that no sequence covers are left as they were.  A non-finite value held by a later
+ * token of the same run may reach a row's output.  Workspace: gdr_attn_step_workspace_bytes. */
+typedef struct gdr_attn_step {
+  int32_t T, H_q, window;
+  float scale;
+  int64_t q_stride;
+  const uint16_t *q;         /* bf16 [T, H_q, D] */
+  const int32_t *lens;       /* device int32 [N] */
+  const int32_t *cu_seqlens; /* device int32 [N+1], or NULL */
+} gdr_attn_step;
+int64_t gdr_attn_step_workspace_bytes(int32_t T, int32_t N, int32_t H_q, int32_t H_kv, int32_t max_pages, int32_t page);
+/* o: bf16 [T, H_q, D]. */
+int32_t gdr_attn_step_fwd(const gdr_kv *cache, const gdr_attn_step *p, uint16_t *o, void *workspace, int64_t workspace_bytes,
+                          void *stream);
+
 /* Kernel timing (diagnostics).  gdr_timing_enable(1) makes every later call
  * bracket each of its kernel launches with a pair of hipEvents recorded on the
  * call's stream (the events are created on first use and reused; this is the
@@ -420,8 +557,10 @@ int32_t gdr_norm_bwd(const gdr_norm *p, const void *dy, const void *ds, void *dx
  * totals, writes up to `capacity` entries (kernel name, total milliseconds,
  * number of launches) and, with reset != 0, clears the totals.  Kernel names:
  * "fwd_prep", "fwd_walk", "bwd_walk", "bwd_grad", then "conv_fwd", "conv_bwd",
- * "conv_step", "gate_fwd", "gate_bwd", "step", "norm_fwd", "norm_bwd" and
- * "param_sum" (the sums of the parameter gradients' partials).  Not thread-safe with
+ * "conv_step", "gate_fwd", "gate_bwd", "step", "norm_fwd", "norm_bwd",
+ * "param_sum" (the sums of the parameter gradients' partials), "rope", "attn_fwd",
+ * "attn_dq", "attn_dkv", "kv_store", "kv_load", "attn_step" and "attn_join" (partial results
+ * of attn_dkv and attn_step).  Not thread-safe with
  * respect to concurrent calls that are being timed. */
 int32_t gdr_timing_enable(int32_t on);
 int32_t gdr_timing_read(const char **names, double *total_ms, int64_t *launches, int32_t capacity,
