@@ -25,7 +25,7 @@ __all__ = [
     "ConvStep", "conv_step", "GateProblem", "gate_fwd", "gate_bwd", "gate_workspace_bytes", "StepProblem", "kda_step",
     "gdn_step", "NormProblem", "norm_fwd", "norm_bwd", "norm_workspace_bytes",
     "GDR_ROPE_HALF", "GDR_ROPE_PAIRS", "GDR_ROPE_PLAIN", "GDR_ROPE_LINEAR", "GDR_ROPE_BASE", "GDR_ROPE_BLEND", "rope_freqs",
-    "RopeProblem", "rope_fwd", "rope_bwd", "AttnPlan", "AttnProblem", "attn_fwd", "attn_bwd", "attn_workspace_bytes", "KvCache",
+    "RopeProblem", "rope_fwd", "rope_bwd", "AttnPlan", "AttnProblem", "attn_fwd", "attn_bwd", "KvCache",
     "KvProblem", "kv_store", "kv_load", "AttnStep", "attn_step", "attn_step_workspace_bytes",
 ]
 
@@ -317,6 +317,6 @@ from .layer import (  # noqa: E402,F401
 from . import attn  # noqa: E402  (the binding of the attention layers' operators)
 from .attn import (  # noqa: E402,F401
     GDR_ROPE_BASE, GDR_ROPE_BLEND, GDR_ROPE_HALF, GDR_ROPE_LINEAR, GDR_ROPE_PAIRS, GDR_ROPE_PLAIN, AttnPlan, AttnProblem,
-    AttnStep, KvCache, KvProblem, RopeProblem, attn_bwd, attn_fwd, attn_step, attn_step_workspace_bytes, attn_workspace_bytes,
+    AttnStep, KvCache, KvProblem, RopeProblem, attn_bwd, attn_fwd, attn_step, attn_step_workspace_bytes,
     kv_load, kv_store, rope_bwd, rope_freqs, rope_fwd,
 )

@@ -29,9 +29,14 @@ class _CRope(ctypes.Structure):
                 ("k", _vp), ("positions", _vp), ("chunk_table", _vp), ("freqs", _vp)]
 
 
+class _CAttnPlan(ctypes.Structure):
+    _fields_ = [("n_q_tiles", _i32), ("n_k_tiles", _i32), ("q_longest", _i32), ("k_longest", _i32), ("q_steps", _i64),
+                ("k_steps", _i64), ("table_len", _i64), ("q_items", _i32 * 12), ("k_items", _i32 * 12)]
+
+
 class _CAttn(ctypes.Structure):
     _fields_ = [("T_q", _i32), ("T_k", _i32), ("N", _i32), ("H_q", _i32), ("H_kv", _i32), ("D", _i32), ("causal", _i32),
-                ("window", _i32), ("n_q_tiles", _i32), ("n_k_tiles", _i32), ("scale", _f32), ("q_stride", _i64),
+                ("window", _i32), ("plan", _CAttnPlan), ("scale", _f32), ("q_stride", _i64),
                 ("k_stride", _i64), ("v_stride", _i64), ("q", _vp), ("k", _vp), ("v", _vp), ("tile_table", _vp)]
 
 
@@ -53,8 +58,8 @@ def declare(L) -> None:
         ("gdr_rope_freqs", [_i32, _f64, _i32, _f64, _f64, _f64, _f64, P(_f64)]),
         ("gdr_rope_fwd", [P(_CRope), _vp, _i64, _vp, _i64, _vp]),
         ("gdr_rope_bwd", [P(_CRope), _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp]),
-        ("gdr_plan_attn", [ip, ip, _i32, _i32, _i32, ip, _i64, ip, ip, P(_i64)]),
-        ("gdr_attn_fwd", [P(_CAttn), _vp, _vp, _vp]),
+        ("gdr_plan_attn", [ip, ip, _i32, _i32, _i32, ip, _i64, P(_CAttnPlan)]),
+        ("gdr_attn_fwd", [P(_CAttn), _vp, _vp, _vp, _i64, _vp]),
         ("gdr_attn_bwd", [P(_CAttn), _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp]),
         ("gdr_kv_store", [P(_CKv), _i32, _vp, _vp, _vp, _i64, _vp, _i64, _vp]),
         ("gdr_kv_load", [P(_CKv), _i32, _vp, _vp, _vp, _i64, _vp, _i64, _vp]),
@@ -62,9 +67,8 @@ def declare(L) -> None:
     ):
         fn = getattr(L, name)
         fn.argtypes, fn.restype = args, _i32
-    for name, n in (("gdr_attn_workspace_bytes", 5), ("gdr_attn_step_workspace_bytes", 6)):
-        fn = getattr(L, name)
-        fn.argtypes, fn.restype = [_i32] * n, _i64
+    L.gdr_attn_workspace_bytes.argtypes, L.gdr_attn_workspace_bytes.restype = [P(_CAttn), _i32], _i64
+    L.gdr_attn_step_workspace_bytes.argtypes, L.gdr_attn_step_workspace_bytes.restype = [_i32] * 6, _i64
 
 
 # ---- rotary positions ----
@@ -163,19 +167,21 @@ class AttnPlan:
         _sizes(window)
         self.N, self.T_q, self.T_k = len(cu_q) - 1, int(cu_q[-1]), int(cu_k[-1])
         self.causal, self.window = bool(causal), int(window)
-        ip, nq, nk, n = ctypes.POINTER(_i32), _i32(), _i32(), _i64()
+        ip, self.cplan = ctypes.POINTER(_i32), _CAttnPlan()
         args = (cu_q.ctypes.data_as(ip), cu_k.ctypes.data_as(ip), self.N, int(self.causal), self.window)
-        _check(lib().gdr_plan_attn(*args, None, 0, ctypes.byref(nq), ctypes.byref(nk), ctypes.byref(n)))
-        table = np.zeros(max(n.value, 1), dtype=np.int32)
-        _check(lib().gdr_plan_attn(*args, table.ctypes.data_as(ip), table.size, None, None, None))
-        self.n_q_tiles, self.n_k_tiles = nq.value, nk.value
+        _check(lib().gdr_plan_attn(*args, None, 0, ctypes.byref(self.cplan)))
+        table = np.zeros(max(self.cplan.table_len, 1), dtype=np.int32)
+        _check(lib().gdr_plan_attn(*args, table.ctypes.data_as(ip), table.size, ctypes.byref(self.cplan)))
         self.table = torch.from_numpy(table).to(device)
 
 
 class AttnProblem(_Base):
     """Softmax attention over a packed batch.
 
-    q: bf16 [T_q, H_q, 128]; k, v: bf16 [T_k, H_kv, 128], rows 16-byte aligned at any stride; plan: the batch's AttnPlan."""
+    q: bf16 [T_q, H_q, 128]; k, v: bf16 [T_k, H_kv, 128], rows 16-byte aligned at any stride; plan: the batch's AttnPlan.
+    The problem holds the forward's workspace (none unless few rows have many keys).  What it holds follows from the problem's
+    inputs alone, so calls that overlap without those changing write the same there; overlapping calls on changing
+    inputs would race on the inputs already."""
 
     def __init__(self, q, k, v, plan, scale=None):
         import torch
@@ -195,17 +201,14 @@ class AttnProblem(_Base):
         _need(plan.table, "the plan's table", None, None, dev)
         self.q, self.k, self.v, self.plan = q, k, v, plan
         self.scale = float(self.D ** -0.5 if scale is None else scale)
-        self._c = _CAttn(self.T_q, self.T_k, plan.N, self.H_q, self.H_kv, self.D, int(plan.causal), plan.window, plan.n_q_tiles,
-                         plan.n_k_tiles, self.scale, qs, ks, vs, _p(q), _p(k), _p(v), _p(plan.table))
+        self._c = _CAttn(self.T_q, self.T_k, plan.N, self.H_q, self.H_kv, self.D, int(plan.causal), plan.window, plan.cplan,
+                         self.scale, qs, ks, vs, _p(q), _p(k), _p(v), _p(plan.table))
         self.cstruct = ctypes.byref(self._c)
+        self._fwd_bytes = _bytes(lib().gdr_attn_workspace_bytes(self.cstruct, 0))
+        self._fwd_ws = torch.empty(self._fwd_bytes, dtype=torch.uint8, device=dev) if self._fwd_bytes else None
 
     def workspace_bytes(self) -> int:
-        return attn_workspace_bytes(self.T_q, self.T_k, self.plan.n_k_tiles, self.H_q, self.H_kv)
-
-
-def attn_workspace_bytes(T_q, T_k, n_k_tiles, H_q, H_kv) -> int:
-    _sizes(T_q, T_k, n_k_tiles, H_q, H_kv)
-    return _bytes(lib().gdr_attn_workspace_bytes(T_q, T_k, n_k_tiles, H_q, H_kv))
+        return _bytes(lib().gdr_attn_workspace_bytes(self.cstruct, 1))
 
 
 def attn_fwd(prob, o, lse=None, stream=None):
@@ -215,7 +218,7 @@ def attn_fwd(prob, o, lse=None, stream=None):
     _need(o, "o", (prob.T_q, prob.H_q, prob.D), torch.bfloat16, prob.device)
     if lse is not None:
         _need(lse, "lse", (prob.H_q, prob.T_q), torch.float32, prob.device)
-    _call(prob, stream, "gdr_attn_fwd", _p(o), _p(lse))
+    _call(prob, stream, "gdr_attn_fwd", _p(o), _p(lse), _p(prob._fwd_ws), prob._fwd_bytes)
 
 
 def attn_bwd(prob, o, lse, dout, dq, dk, dv, workspace, stream=None):

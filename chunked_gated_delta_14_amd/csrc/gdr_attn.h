@@ -36,43 +36,88 @@ hipError_t launch_rope(const gdr_rope &p, bool back, const void *q, int64_t q_st
 
 // ---- attention over packed documents ----
 
-// Rows of a query tile and keys of a key tile: a block's, 32 to each of its wavefronts.
-constexpr int ATT_TILE = 128;
+// Rows of a query tile, and keys of a key tile: 32 to each of a block's four and eight wavefronts.
+constexpr int ATT_QTILE = 128, ATT_KTILE = 256;
 // A tile of the table (both kinds), 8 int32: its first row in the packed batch, its
 // rows, the other side's first row in the batch and its document's rows there, the
-// tile's first row within the document, Lk - Lq, two spare.
+// tile's first row within the document, Lk - Lq, the other side's first row (a multiple
+// of 64) and end that its rows meet.
 constexpr int ATT_ENTRY = 8;
 
-// The dk, dv kernel's blocks: (key tile, kv head, part of the kv head's query heads).
-// Where tiles and kv heads leave the chip half empty, the query heads of a kv head
-// are dealt to `parts` blocks whose fp32 sums a second kernel adds in order.
-inline int attn_parts(int64_t tiles, int H_kv, int group) {
-  int parts = 1;
-  while (parts < group && group % (2 * parts) == 0 && tiles * H_kv * parts < 384) parts *= 2;
-  return parts;
+// The table: the entries of the query tiles and of the key tiles, then the lists of parts of
+// either kind by level, an item of 2 int32: the tile, and the part + its tile's parts << 16.
+constexpr int ATT_PARTS = 64;
+inline int attn_parts(int64_t steps, int level) {
+  return (int)std::min<int64_t>(std::max<int64_t>((steps + (int64_t(1) << level) - 1) >> level, 1), ATT_PARTS);
 }
-// Workspace of the backward: lse and delta of every row and head as the matrix kernels take
-// them, then the parts' sums.
-struct AttnWorkspace {
-  int64_t stats, partial, bytes;
-  int parts;
+inline int64_t attn_items(const int32_t (&items)[GDR_ATTN_LEVELS], int levels) {
+  int64_t n = 0;
+  for (int i = 0; i < levels; ++i) n += items[i];
+  return n;
+}
+// How a launch shares its tiles' steps.  Where tiles and heads would leave compute units
+// idle, or a few long tiles would run on after the others, it takes the list of parts whose
+// steps come nearest the mean load of `slots` blocks, but not fewer than `least`, which a block's start and
+// its part's way through memory outweigh; a second kernel then joins the parts' fp32
+// results in order.
+struct AttnShare {
+  int level;        // -1: whole tiles
+  int parts;        // the longest tile's
+  int64_t blocks;   // tiles or parts, of one head
+  int64_t items;    // the list's place in the table, in int32
 };
-inline AttnWorkspace attn_workspace(int32_t T_q, int32_t T_k, int32_t n_k_tiles, int32_t H_q, int32_t H_kv) {
+inline AttnShare attn_share(const gdr_attn_plan &p, bool keys, int64_t heads, int slots, int least) {
+  const int32_t (&items)[GDR_ATTN_LEVELS] = keys ? p.k_items : p.q_items;
+  const int32_t tiles = keys ? p.n_k_tiles : p.n_q_tiles, longest = keys ? p.k_longest : p.q_longest;
+  const int64_t mean = std::max<int64_t>(least, ((keys ? p.k_steps : p.q_steps) * heads + slots - 1) / slots);
+  AttnShare s{-1, 1, tiles, 0};
+  if (longest <= mean + mean / 2) return s;
+  int level = 0;
+  while (level < GDR_ATTN_LEVELS - 1 && (int64_t(4) << level) <= 3 * mean) ++level;  // the power of two within 3/4 and 3/2 of it
+  if (!items[level]) return s;
+  s.level = level;
+  s.parts = attn_parts(longest, level);
+  s.blocks = items[level];
+  s.items = ((int64_t)p.n_q_tiles + p.n_k_tiles) * ATT_ENTRY + 2 * ((keys ? attn_items(p.q_items, GDR_ATTN_LEVELS) : 0) + attn_items(items, level));
+  return s;
+}
+// Blocks of 128 query rows run two to a compute unit, and two rounds of them even out; blocks of 256 keys, whose
+// steps are rows of all of a kv head's query heads, run one to a unit.
+constexpr int ATT_Q_SLOTS = 1024, ATT_K_SLOTS = 384;
+inline AttnShare attn_q_share(const gdr_attn &p) { return attn_share(p.plan, false, p.H_q, ATT_Q_SLOTS, 4); }
+inline AttnShare attn_k_share(const gdr_attn &p) {
+  const int group = p.H_q / p.H_kv;
+  return attn_share(p.plan, true, p.H_kv, ATT_K_SLOTS, std::max(1, 4 / group));
+}
+// The workspace.  Forward: the parts' rows [part][T_q][H_q][128], then their maxima and sums
+// [part][H_q][T_q][2].  Backward: lse and delta of every row and head as the
+// matrix kernels take them, [H_q][T_q] each; the parts of dq [part][T_q][H_q][128] or, later and in the
+// same place, those of dk and of dv [part][T_k][H_kv][128].
+struct AttnWorkspace {
+  int64_t stats, q_part, k_part, fwd, bwd;  // bytes: a row of stats, a part's, the whole
+  AttnShare q, k;
+};
+inline AttnWorkspace attn_workspace(const gdr_attn &p) {
   AttnWorkspace w;
   auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
-  w.parts = attn_parts(n_k_tiles, H_kv, H_q / H_kv);
-  w.stats = up((int64_t)T_q * H_q * 4);
-  w.partial = w.parts > 1 ? up((int64_t)T_k * H_kv * 128 * 4) : 0;
-  w.bytes = 2 * w.stats + 2 * w.parts * w.partial;
+  w.q = attn_q_share(p);
+  w.k = attn_k_share(p);
+  w.stats = up((int64_t)p.T_q * p.H_q * 4);
+  w.q_part = w.q.parts > 1 ? up((int64_t)p.T_q * p.H_q * 128 * 4) : 0;
+  w.k_part = w.k.parts > 1 ? up((int64_t)p.T_k * p.H_kv * 128 * 4) : 0;
+  w.fwd = w.q.parts > 1 ? w.q.parts * (w.q_part + up((int64_t)p.T_q * p.H_q * 8)) : 0;
+  w.bwd = 2 * w.stats + std::max(w.q.parts * w.q_part, 2 * w.k.parts * w.k_part);
   return w;
 }
-hipError_t launch_attn_fwd(const gdr_attn &p, uint16_t *o, float *lse, hipStream_t stream);
+hipError_t launch_attn_fwd(const gdr_attn &p, uint16_t *o, float *lse, void *ws, hipStream_t stream);
+hipError_t launch_attn_fwd_join(const gdr_attn &p, uint16_t *o, float *lse, void *ws, hipStream_t stream);
 hipError_t launch_attn_dq(const gdr_attn &p, const uint16_t *o, const float *lse, const uint16_t *dout, uint16_t *dq,
                           int64_t dq_stride, void *ws, hipStream_t stream);
+hipError_t launch_attn_dq_join(const gdr_attn &p, uint16_t *dq, int64_t dq_stride, void *ws, hipStream_t stream);
 hipError_t launch_attn_dkv(const gdr_attn &p, const uint16_t *dout, uint16_t *dk, int64_t dk_stride, uint16_t *dv,
                            int64_t dv_stride, void *ws, hipStream_t stream);
-hipError_t launch_attn_join(const gdr_attn &p, uint16_t *dk, int64_t dk_stride, uint16_t *dv, int64_t dv_stride, void *ws,
-                            hipStream_t stream);
+hipError_t launch_attn_dkv_join(const gdr_attn &p, uint16_t *dk, int64_t dk_stride, uint16_t *dv, int64_t dv_stride, void *ws,
+                                hipStream_t stream);
 
 // ---- the cache and the attention over it ----
 

@@ -76,17 +76,14 @@ int32_t rope(const gdr_rope *p, bool back, const void *q, int64_t qs, const void
 
 // ---- attention over packed documents ----
 
-int32_t check_attn_sizes(int32_t T_q, int32_t T_k, int32_t n_k_tiles, int32_t H_q, int32_t H_kv) {
-  if (T_q < 0 || T_k < 0 || n_k_tiles < 0) return invalid("T_q, T_k and tile counts must be >= 0");
-  if (H_q < 1 || H_kv < 1) return invalid("head counts must be positive");
-  if (H_q % H_kv) return unsupported("H_q must be a multiple of H_kv");
-  if (H_q > 65536) return unsupported("H above 65536");
-  if (T_q > kMostTokens || T_k > kMostTokens) return unsupported("more than 2^30 tokens");
-  return GDR_OK;
-}
-bool tiles_ok(int32_t tiles, int32_t T, int32_t N) {
-  const int64_t least = ((int64_t)T + gdr::ATT_TILE - 1) / gdr::ATT_TILE;
+bool tiles_ok(int32_t tiles, int32_t T, int32_t N, int rows) {
+  const int64_t least = ((int64_t)T + rows - 1) / rows;
   return tiles >= least && tiles <= T && tiles <= least + N;
+}
+bool steps_ok(int32_t longest, int64_t steps, int32_t tiles, int32_t T, const int32_t (&items)[GDR_ATTN_LEVELS]) {
+  for (int32_t n : items)
+    if (n != 0 && (n < tiles || n > (int64_t)tiles * gdr::ATT_PARTS)) return false;
+  return longest >= 0 && longest <= (T + 63) / 64 + 1 && steps >= longest && steps <= (int64_t)longest * tiles;
 }
 // 16-byte aligned rows of [T, H, 128], no wider than the kernels' 32-bit offsets within a tile.
 bool rows_ok(const void *p, int64_t stride, int32_t H, int32_t T) {
@@ -96,16 +93,21 @@ const char *const kRows = "rows must be 16-byte aligned, with strides that are m
 
 int32_t check_attn(const gdr_attn *p) {
   if (!p) return invalid("problem is NULL");
-  const int32_t rc = check_attn_sizes(p->T_q, p->T_k, p->n_k_tiles, p->H_q, p->H_kv);
-  if (rc) return rc;
-  if (p->N < 0) return invalid("N must be >= 0");
+  if (p->T_q < 0 || p->T_k < 0 || p->N < 0) return invalid("T_q, T_k and N must be >= 0");
+  if (p->H_q < 1 || p->H_kv < 1) return invalid("head counts must be positive");
+  if (p->H_q % p->H_kv) return unsupported("H_q must be a multiple of H_kv");
+  if (p->H_q > 65536) return unsupported("H above 65536");
+  if (p->T_q > kMostTokens || p->T_k > kMostTokens) return unsupported("more than 2^30 tokens");
   if (p->D != 128) return unsupported("only D = 128 is implemented");
   if (p->window < 0) return invalid("window must be >= 0");
   if (p->window > 0 && !p->causal) return unsupported("a window needs causal");
   if (!(p->scale > 0.f) || !std::isfinite(p->scale)) return invalid("scale must be positive and finite");
-  if (!tiles_ok(p->n_q_tiles, p->T_q, p->N) || !tiles_ok(p->n_k_tiles, p->T_k, p->N))
-    return invalid("n_q_tiles and n_k_tiles are inconsistent with T_q, T_k and N");
-  if (p->n_q_tiles + (int64_t)p->n_k_tiles > 0 && !p->tile_table) return invalid("tile_table must be non-NULL");
+  const gdr_attn_plan &plan = p->plan;
+  if (!tiles_ok(plan.n_q_tiles, p->T_q, p->N, gdr::ATT_QTILE) || !tiles_ok(plan.n_k_tiles, p->T_k, p->N, gdr::ATT_KTILE) ||
+      !steps_ok(plan.q_longest, plan.q_steps, plan.n_q_tiles, p->T_k, plan.q_items) ||
+      !steps_ok(plan.k_longest, plan.k_steps, plan.n_k_tiles, p->T_q, plan.k_items))
+    return invalid("the plan is inconsistent with T_q, T_k and N");
+  if (plan.n_q_tiles + (int64_t)plan.n_k_tiles > 0 && !p->tile_table) return invalid("tile_table must be non-NULL");
   if (p->T_q > 0 && !p->q) return invalid("q must be non-NULL");
   if (p->T_k > 0 && (!p->k || !p->v)) return invalid("k and v must be non-NULL");
   if (!element_aligned(p->tile_table, GDR_F32)) return invalid("tile_table must be aligned to its elements");
@@ -113,21 +115,29 @@ int32_t check_attn(const gdr_attn *p) {
       !rows_ok(p->v, p->v_stride, p->H_kv, p->T_k))
     return invalid(kRows);
   if ((int64_t)p->H_q * 128 >= (1 << 24)) return unsupported("H_q * 128 of 2^24 or more");
-  if (!grid_ok((int64_t)p->n_q_tiles * p->H_q, 256) || !grid_ok((int64_t)p->n_k_tiles * p->H_q, 256) ||
-      !grid_ok((int64_t)p->T_k * p->H_kv * 64 / 256 + 1, 256))
-    return unsupported("too many rows and heads for one launch");
+  // a launch has a block for every part and head, and 8 (16) for every tile and head to join them
+  const gdr::AttnShare q = gdr::attn_q_share(*p), k = gdr::attn_k_share(*p);
+  const int64_t q_blocks = std::max(q.blocks, q.parts > 1 ? (int64_t)plan.n_q_tiles * 8 : 0);
+  const int64_t k_blocks = std::max(k.blocks, k.parts > 1 ? (int64_t)plan.n_k_tiles * 16 : 0);
+  if (!grid_ok(q_blocks * p->H_q, 256) || !grid_ok(k_blocks * p->H_kv, 512)) return unsupported("too many rows and heads for one launch");
   return GDR_OK;
 }
 
-int32_t attn_fwd(const gdr_attn *p, uint16_t *o, float *lse, void *stream) {
+int32_t attn_fwd(const gdr_attn *p, uint16_t *o, float *lse, void *ws, int64_t ws_bytes, void *stream) {
   int32_t rc = check_attn(p);
   if (rc) return rc;
   if (p->T_q > 0 && !o) return invalid("o is NULL");
   if (!aligned(o, 16) || !element_aligned(lse, GDR_F32)) return invalid("o must be 16-byte aligned and lse to its elements");
+  const gdr::AttnWorkspace w = gdr::attn_workspace(*p);
+  if (ws && (rc = check_workspace(ws, ws_bytes, w.fwd))) return rc;
   if (aliases({o, lse}, {p->q, p->k, p->v, p->tile_table})) return invalid("o or lse is an input");
   if ((rc = gdr::host_check_device())) return rc;
   if ((rc = launch(gdr::TK_ATTN_FWD, stream, "attention launch",
-                   [&](hipStream_t s) { return gdr::launch_attn_fwd(*p, o, lse, s); })))
+                   [&](hipStream_t s) { return gdr::launch_attn_fwd(*p, o, lse, ws, s); })))
+    return rc;
+  if (ws && w.q.parts > 1 && (rc = launch(gdr::TK_ATTN_JOIN, stream, "attention join launch", [&](hipStream_t s) {
+                                return gdr::launch_attn_fwd_join(*p, o, lse, ws, s);
+                              })))
     return rc;
   return host_status(GDR_OK, "");
 }
@@ -142,19 +152,22 @@ int32_t attn_bwd(const gdr_attn *p, const uint16_t *o, const float *lse, const u
     return invalid("o and dout must be 16-byte aligned and lse to its elements");
   if (!rows_ok(dq, dqs, p->H_q, p->T_q) || !rows_ok(dk, dks, p->H_kv, p->T_k) || !rows_ok(dv, dvs, p->H_kv, p->T_k))
     return invalid(kRows);
-  const gdr::AttnWorkspace w = gdr::attn_workspace(p->T_q, p->T_k, p->n_k_tiles, p->H_q, p->H_kv);
-  if ((rc = check_workspace(ws, ws_bytes, w.bytes))) return rc;
+  const gdr::AttnWorkspace w = gdr::attn_workspace(*p);
+  if ((rc = check_workspace(ws, ws_bytes, w.bwd))) return rc;
   if (aliases({dq, dk, dv}, {p->q, p->k, p->v, p->tile_table, o, lse, dout})) return invalid("dq, dk or dv is an input");
   if (aliases({dq}, {dk, dv}) || aliases({dk}, {dv})) return invalid("two of dq, dk and dv are the same memory");
   if ((rc = gdr::host_check_device())) return rc;
   if ((rc = launch(gdr::TK_ATTN_DQ, stream, "query gradient launch",
                    [&](hipStream_t s) { return gdr::launch_attn_dq(*p, o, lse, dout, dq, dqs, ws, s); })))
     return rc;
+  if (w.q.parts > 1 && (rc = launch(gdr::TK_ATTN_JOIN, stream, "query gradient sum launch",
+                                    [&](hipStream_t s) { return gdr::launch_attn_dq_join(*p, dq, dqs, ws, s); })))
+    return rc;
   if ((rc = launch(gdr::TK_ATTN_DKV, stream, "key gradient launch",
                    [&](hipStream_t s) { return gdr::launch_attn_dkv(*p, dout, dk, dks, dv, dvs, ws, s); })))
     return rc;
-  if (w.parts > 1 && (rc = launch(gdr::TK_ATTN_JOIN, stream, "key gradient sum launch",
-                                  [&](hipStream_t s) { return gdr::launch_attn_join(*p, dk, dks, dv, dvs, ws, s); })))
+  if (w.k.parts > 1 && (rc = launch(gdr::TK_ATTN_JOIN, stream, "key gradient sum launch",
+                                    [&](hipStream_t s) { return gdr::launch_attn_dkv_join(*p, dk, dks, dv, dvs, ws, s); })))
     return rc;
   return host_status(GDR_OK, "");
 }
@@ -165,57 +178,91 @@ struct Tile {
   int64_t cost;
 };
 int32_t plan_attn(const int32_t *cu_q, const int32_t *cu_k, int32_t N, bool causal, int32_t window, int32_t *table,
-                  int64_t capacity, int32_t *n_q, int32_t *n_k, int64_t *table_len) {
+                  int64_t capacity, gdr_attn_plan *plan) {
   if (N < 0) return invalid("N must be >= 0");
   if (!cu_q) return invalid("cu_q is NULL");
   if (!cu_k) cu_k = cu_q;
   if (window < 0) return invalid("window must be >= 0");
   if (window > 0 && !causal) return unsupported("a window needs causal");
   if (cu_q[0] != 0 || cu_k[0] != 0) return invalid("cu_q[0] and cu_k[0] must be 0");
-  constexpr int64_t TILE = gdr::ATT_TILE;
-  int64_t nq = 0, nk = 0;
+  if (!plan) return invalid("plan is NULL");
+  int64_t n_tiles[2] = {0, 0};
   for (int32_t n = 0; n < N; ++n) {
     const int64_t Lq = (int64_t)cu_q[n + 1] - cu_q[n], Lk = (int64_t)cu_k[n + 1] - cu_k[n];
     if (Lq < 0 || Lk < 0) return invalid("cu_q and cu_k must be non-decreasing");
-    nq += (Lq + TILE - 1) / TILE;
-    nk += (Lk + TILE - 1) / TILE;
+    n_tiles[0] += (Lq + gdr::ATT_QTILE - 1) / gdr::ATT_QTILE;
+    n_tiles[1] += (Lk + gdr::ATT_KTILE - 1) / gdr::ATT_KTILE;
   }
   if (cu_q[N] > kMostTokens || cu_k[N] > kMostTokens) return unsupported("more than 2^30 tokens");
-  if (nq + nk > INT32_MAX / gdr::ATT_ENTRY) return unsupported("too many tiles");
-  const int64_t len = (nq + nk) * gdr::ATT_ENTRY;
-  if (n_q) *n_q = (int32_t)nq;
-  if (n_k) *n_k = (int32_t)nk;
-  if (table_len) *table_len = len;
-  if (!table) return host_status(GDR_OK, "");
-  if (capacity < len) return invalid("table capacity too small");
-  std::vector<Tile> tiles;
-  tiles.reserve((size_t)std::max(nq, nk));
+  if (n_tiles[0] + n_tiles[1] > INT32_MAX / gdr::ATT_ENTRY) return unsupported("too many tiles");
+  gdr_attn_plan out{};
+  out.n_q_tiles = (int32_t)n_tiles[0];
+  out.n_k_tiles = (int32_t)n_tiles[1];
+  std::vector<Tile> tiles[2];
+  int64_t len = (n_tiles[0] + n_tiles[1]) * gdr::ATT_ENTRY;
   for (int side = 0; side < 2; ++side) {
-    tiles.clear();
+    std::vector<Tile> &list = tiles[side];
+    list.reserve((size_t)n_tiles[side]);
+    int64_t steps = 0, longest = 0;
     for (int32_t n = 0; n < N; ++n) {
       const int64_t Lq = cu_q[n + 1] - cu_q[n], Lk = cu_k[n + 1] - cu_k[n], shift = Lk - Lq;
-      const int64_t mine = side ? Lk : Lq;
-      for (int64_t r = 0; r < mine; r += TILE) {
-        const int64_t rows = std::min(TILE, mine - r);
+      const int64_t mine = side ? Lk : Lq, rows_of_tile = side ? gdr::ATT_KTILE : gdr::ATT_QTILE;
+      for (int64_t r = 0; r < mine; r += rows_of_tile) {
+        const int64_t rows = std::min(rows_of_tile, mine - r);
         int64_t from = 0, to = side ? Lq : Lk;
         if (causal && side == 0) to = std::min(to, r + rows + shift);
         if (causal && side == 1) from = std::max<int64_t>(0, r - shift);
         if (window && side == 0) from = std::max<int64_t>(0, r + shift - window + 1);
         if (window && side == 1) to = std::min(to, r + rows - 1 - shift + window);
+        from = from / 64 * 64;
+        if (to < from) from = to = 0;
         Tile t{};
-        t.entry[0] = (int32_t)((side ? cu_k[n] : cu_q[n]) + r);
-        t.entry[1] = (int32_t)rows;
-        t.entry[2] = side ? cu_q[n] : cu_k[n];
-        t.entry[3] = (int32_t)(side ? Lq : Lk);
-        t.entry[4] = (int32_t)r;
-        t.entry[5] = (int32_t)shift;
-        t.cost = to > from ? (to + 63) / 64 - from / 64 : 0;
-        tiles.push_back(t);
+        const int64_t e[gdr::ATT_ENTRY] = {(side ? cu_k[n] : cu_q[n]) + r, rows, side ? cu_q[n] : cu_k[n], side ? Lq : Lk, r, shift, from, to};
+        for (int i = 0; i < gdr::ATT_ENTRY; ++i) t.entry[i] = (int32_t)e[i];
+        t.cost = (to - from + 63) / 64;
+        steps += t.cost;
+        longest = std::max(longest, t.cost);
+        list.push_back(t);
       }
     }
-    std::stable_sort(tiles.begin(), tiles.end(), [](const Tile &a, const Tile &b) { return a.cost > b.cost; });
-    for (const Tile &t : tiles) table = std::copy(t.entry, t.entry + gdr::ATT_ENTRY, table);
+    std::stable_sort(list.begin(), list.end(), [](const Tile &a, const Tile &b) { return a.cost > b.cost; });
+    (side ? out.k_steps : out.q_steps) = steps;
+    (side ? out.k_longest : out.q_longest) = (int32_t)longest;
+    // lists of parts: those that a launch of one head or more can come to take
+    const int slots = side ? gdr::ATT_K_SLOTS : gdr::ATT_Q_SLOTS;
+    int32_t(&items)[GDR_ATTN_LEVELS] = side ? out.k_items : out.q_items;
+    for (int level = 0; level < GDR_ATTN_LEVELS; ++level) {
+      if ((int64_t(1) << level) >= longest || (int64_t(3) << level) < 2 * (steps / slots)) continue;
+      int64_t n = 0;
+      for (const Tile &t : list) n += gdr::attn_parts(t.cost, level);
+      if (n > INT32_MAX / 4) continue;
+      items[level] = (int32_t)n;
+      len += 2 * n;
+    }
   }
+  if (len > INT32_MAX) return unsupported("too many tiles");
+  out.table_len = len;
+  *plan = out;
+  if (!table) return host_status(GDR_OK, "");
+  if (capacity < len) return invalid("table capacity too small");
+  for (const std::vector<Tile> &list : tiles)
+    for (const Tile &t : list) table = std::copy(t.entry, t.entry + gdr::ATT_ENTRY, table);
+  struct Part {
+    int32_t tile, part;
+    int64_t cost;
+  };
+  std::vector<Part> parts;
+  for (int side = 0; side < 2; ++side)
+    for (int level = 0; level < GDR_ATTN_LEVELS; ++level) {
+      if (!(side ? out.k_items : out.q_items)[level]) continue;
+      parts.clear();
+      for (size_t i = 0; i < tiles[side].size(); ++i) {
+        const int n = gdr::attn_parts(tiles[side][i].cost, level);
+        for (int x = 0; x < n; ++x) parts.push_back(Part{(int32_t)i, x | n << 16, (tiles[side][i].cost + n - 1) / n});
+      }
+      std::stable_sort(parts.begin(), parts.end(), [](const Part &a, const Part &b) { return a.cost > b.cost; });
+      for (const Part &x : parts) *table++ = x.tile, *table++ = x.part;
+    }
   return host_status(GDR_OK, "");
 }
 
@@ -335,17 +382,21 @@ int32_t gdr_rope_bwd(const gdr_rope *p, const void *dq_out, int64_t dq_out_strid
 }
 
 int32_t gdr_plan_attn(const int32_t *cu_q, const int32_t *cu_k, int32_t N, int32_t causal, int32_t window, int32_t *table,
-                      int64_t capacity, int32_t *n_q_tiles, int32_t *n_k_tiles, int64_t *table_len) {
+                      int64_t capacity, gdr_attn_plan *plan) {
   try {
-    return plan_attn(cu_q, cu_k, N, causal != 0, window, table, capacity, n_q_tiles, n_k_tiles, table_len);
+    return plan_attn(cu_q, cu_k, N, causal != 0, window, table, capacity, plan);
   } catch (...) {
     return unsupported("no host memory for the tiles");
   }
 }
-int32_t gdr_attn_fwd(const gdr_attn *p, uint16_t *o, float *lse, void *stream) { return attn_fwd(p, o, lse, stream); }
-int64_t gdr_attn_workspace_bytes(int32_t T_q, int32_t T_k, int32_t n_k_tiles, int32_t H_q, int32_t H_kv) {
-  const int32_t rc = check_attn_sizes(T_q, T_k, n_k_tiles, H_q, H_kv);
-  return rc ? -(int64_t)rc : gdr::attn_workspace(T_q, T_k, n_k_tiles, H_q, H_kv).bytes;
+int64_t gdr_attn_workspace_bytes(const gdr_attn *p, int32_t backward) {
+  const int32_t rc = check_attn(p);
+  if (rc) return -(int64_t)rc;
+  const gdr::AttnWorkspace w = gdr::attn_workspace(*p);
+  return backward ? w.bwd : w.fwd;
+}
+int32_t gdr_attn_fwd(const gdr_attn *p, uint16_t *o, float *lse, void *workspace, int64_t workspace_bytes, void *stream) {
+  return attn_fwd(p, o, lse, workspace, workspace_bytes, stream);
 }
 int32_t gdr_attn_bwd(const gdr_attn *p, const uint16_t *o, const float *lse, const uint16_t *dout, uint16_t *dq,
                      int64_t dq_stride, uint16_t *dk, int64_t dk_stride, uint16_t *dv, int64_t dv_stride, void *workspace,

@@ -21,11 +21,11 @@ namespace {
 struct BwdArgs {
   const u16 *q, *k, *v, *o, *go;
   const float *lse;
-  const int32_t *tiles;
+  const int32_t *tiles, *items;
   u16 *dq, *dk, *dv;
-  float *lse2, *delta, *pk, *pv;
-  int64_t qs, ks, vs, dqs, dks, dvs, partial;  // partial: floats of one part's sums
-  int Hq, Hkv, group, Tq, Tk, parts, causal, window;
+  float *lse2, *delta, *pq, *pk, *pv;
+  int64_t qs, ks, vs, dqs, dks, dvs, part_size;  // part_size: floats of one part's sums
+  int Hq, Hkv, group, Tq, Tk, level, causal, window;
   float scale;
 };
 
@@ -36,40 +36,19 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(BwdArgs a) {
   __shared__ __align__(16) unsigned char lds[4 * TILE_BYTES];  // K, V; twice
   const int lane = threadIdx.x & 63, lr = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int tile, head;
-  tile_of(blockIdx.x, a.Hq, tile, head);
-  const TileEntry e(a.tiles, tile);
-  const int kvh = head / a.group;
+  const Share x(a.items, blockIdx.x, a.Hq);
+  const TileEntry e(a.tiles, x.tile);
+  const int head = x.head, kvh = head / a.group, steps = e.steps();
   const u16 *kb = a.k + e.other0 * a.ks + kvh * HD, *vb = a.v + e.other0 * a.vs + kvh * HD;
   const int Lk = e.other;
   const int rmax = min(32 * wave + 31, e.rows - 1);
   const int p0 = e.first + 32 * wave + e.shift, p1 = e.first + rmax + e.shift;
-  const int end = a.causal ? min(Lk, e.first + e.rows + e.shift) : Lk;
-  const int begin = a.window ? max(0, e.first + e.shift - a.window + 1) & ~(KT - 1) : 0;
+  const int begin = e.begin + (int)((int64_t)steps * x.part / x.parts) * KT;
+  const int end = min(e.end, e.begin + (int)((int64_t)steps * (x.part + 1) / x.parts) * KT);
   const int row = min(32 * wave + lr, e.rows - 1);
   const bool live = 32 * wave + lr < e.rows;
   const int p = e.first + row + e.shift;
   const int hi = a.causal ? min(p, Lk - 1) : Lk - 1, lo = a.window ? p - a.window + 1 : 0;
-
-  bf16x8 Q[8], G[8];
-  float delta = 0.f;
-  const int64_t at = ((int64_t)(e.row0 + row) * a.Hq + head) * HD + 8 * h;
-  {
-    const u16 *qp = a.q + (int64_t)(e.row0 + row) * a.qs + head * HD + 8 * h;
-#pragma unroll
-    for (int kk = 0; kk < 8; ++kk) {
-      Q[kk] = ld8(qp + 16 * kk);
-      G[kk] = ld8(a.go + at + 16 * kk);
-      const bf16x8 o = ld8(a.o + at + 16 * kk);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) delta = fmaf((float)G[kk][j], (float)o[j], delta);
-    }
-  }
-  delta += other_half(delta);
-  const int64_t stat = (int64_t)head * a.Tq + e.row0 + row;
-  const float given = a.lse[stat];
-  const float lse = given == -INFINITY ? NO_KEYS : given * LOG2E;
-  if (live && h == 0) a.lse2[stat] = lse, a.delta[stat] = delta;
 
   f32x16 D[4];
 #pragma unroll
@@ -88,23 +67,43 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(BwdArgs a) {
     copy4(kb + t * a.ks, ko, to);
     copy4(vb + t * a.vs, vo, to + TILE_BYTES);
   };
-  drain_vmem();
   if (begin < end) copy(begin, 0);
+  bf16x8 Q[8], G[8];
+  float delta = 0.f;
+  const int64_t at = ((int64_t)(e.row0 + row) * a.Hq + head) * HD + 8 * h;
+  {
+    const u16 *qp = a.q + (int64_t)(e.row0 + row) * a.qs + head * HD + 8 * h;
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) {
+      Q[kk] = ld8(qp + 16 * kk);
+      G[kk] = ld8(a.go + at + 16 * kk);
+      const bf16x8 o = ld8(a.o + at + 16 * kk);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) delta = fmaf((float)G[kk][j], (float)o[j], delta);
+    }
+  }
+  delta += other_half(delta);
+  const int64_t stat = (int64_t)head * a.Tq + e.row0 + row;
+  const float given = a.lse[stat];
+  const float lse = given == -INFINITY ? NO_KEYS : given * LOG2E;
+  if (live && h == 0 && x.part == 0) a.lse2[stat] = lse, a.delta[stat] = delta;
+
   int buf = 0;
   for (int t = begin; t < end; t += KT, buf ^= 1) {
     drain_vmem();
     lds_barrier();
     if (t + KT < end) copy(t + KT, buf ^ 1);
-    const unsigned char *kt = lds + buf * 2 * TILE_BYTES, *vt = kt + TILE_BYTES;
-    if ((a.causal && t > p1) || (a.window && t + KT <= p0 - a.window + 1)) continue;
+    const uint32_t k0 = lds0 + buf * 2 * TILE_BYTES;
+    const uint32_t kt = row_base(k0, lane), vt = row_base(k0 + TILE_BYTES, lane), kc = col_base(k0, lane);
+    if ((a.causal && t > p1) || (a.window && t + KT <= p0 - a.window + 1) || 32 * wave >= e.rows) continue;
     const bool masked = t + KT > Lk || (a.causal && t + KT - 1 > p0) || (a.window && t <= p1 - a.window);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       f32x16 S = zero16(), P = zero16();
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
-        S = mfma32(row_frag(kt, half, kk, lr, h), Q[kk], S);
-        P = mfma32(row_frag(vt, half, kk, lr, h), G[kk], P);
+        S = mfma32(row_frag(kt, half, kk), Q[kk], S);
+        P = mfma32(row_frag(vt, half, kk), G[kk], P);
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i) P[i] = __builtin_amdgcn_exp2f(fmaf(S[i], c, -lse)) * (P[i] - delta);
@@ -119,83 +118,104 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(BwdArgs a) {
       for (int s = 0; s < 2; ++s) {
         const bf16x8 dS = acc_frag(P, s);
 #pragma unroll
-        for (int dt = 0; dt < 4; ++dt) D[dt] = mfma32(col_frag(kt, 2 * half + s, dt, lane), dS, D[dt]);
+        for (int dt = 0; dt < 4; ++dt) D[dt] = mfma32(col_frag(kc, 2 * half + s, dt), dS, D[dt]);
       }
     }
   }
-  store_row(a.dq + (int64_t)(e.row0 + row) * a.dqs + head * HD, D, a.scale, h, live);
+  if (x.parts == 1) store_row(a.dq + (int64_t)(e.row0 + row) * a.dqs + head * HD, D, a.scale, h, live);
+  else if (live) store_floats(a.pq + x.part * a.part_size + ((int64_t)(e.row0 + row) * a.Hq + head) * HD, D, h);
 }
 
-__global__ __launch_bounds__(256, 2) void attn_dkv_kernel(BwdArgs a) {
-  __shared__ __align__(16) unsigned char lds[4 * TILE_BYTES];  // Q, dO; twice
+// A lane's value as one that the compiler cannot keep from before: what follows from it is formed again
+// here, for one or two instructions, where kept in a register it would be spilled.
+__device__ __forceinline__ int afresh(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+// Eight wavefronts, 32 keys each, share the tiles in LDS; the keys' sums take half of a wavefront's
+// registers and the keys another eighth, and the values, which there is no room for, stay in LDS.
+__global__ __launch_bounds__(512, 2) void attn_dkv_kernel(BwdArgs a) {
+  __shared__ __align__(16) unsigned char lds[8 * TILE_BYTES];  // Q, dO; twice; the block's values
   __shared__ __align__(16) float stats[2][2][KT];              // lse, delta; twice
   const int lane = threadIdx.x & 63, lr = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int tile, hp;
-  tile_of(blockIdx.x, a.Hkv * a.parts, tile, hp);
-  const int kvh = hp / a.parts, part = hp - kvh * a.parts;
-  const TileEntry e(a.tiles, tile);
-  const int Lq = e.other, per = a.group / a.parts;
-  const int head0 = kvh * a.group + part * per;
-  const int kmax = min(32 * wave + 31, e.rows - 1);
-  const int row = min(32 * wave + lr, e.rows - 1);
-  const bool live = 32 * wave + lr < e.rows;
+  const Share x(a.items, blockIdx.x, a.Hkv);
+  const TileEntry e(a.tiles, x.tile);
+  const int kvh = x.head, Lq = e.other, key0 = 32 * wave;
   // the query rows that see key `first + x`: from f0 + x, and below f0 + x + window
   const int f0 = e.first - e.shift;
-  const int begin = a.causal ? max(0, f0) & ~(KT - 1) : 0;
-  const int end = a.window ? (int)min((int64_t)Lq, (int64_t)f0 + e.rows - 1 + a.window) : Lq;
-  const int lo = a.causal ? f0 + row : 0, hi = a.window ? (int)min((int64_t)Lq - 1, (int64_t)f0 + row + a.window - 1) : Lq - 1;
+  const int begin = e.begin, end = e.end;
+  // this part's share of the steps: KT rows of one of the kv head's query heads each
+  const int steps = e.steps();
+  const int64_t all = (int64_t)steps * a.group;
+  int64_t it = all * x.part / x.parts;
+  const int64_t last_it = all * (x.part + 1) / x.parts;
+  const uint32_t lds0 = lds_addr(lds), stat0 = lds_addr(&stats[0][0][0]);
+  const uint32_t v0 = lds0 + (4 + (wave >> 1)) * TILE_BYTES;
 
-  bf16x8 K[8], V[8];
-  {
-    const u16 *kp = a.k + (int64_t)(e.row0 + row) * a.ks + kvh * HD + 8 * h;
-    const u16 *vp = a.v + (int64_t)(e.row0 + row) * a.vs + kvh * HD + 8 * h;
+  {  // the copies first: what is loaded to registers after them is not waited for apart
+    const u16 *vb = a.v + (int64_t)(e.row0 + (key0 & ~63)) * a.vs + kvh * HD;
+    const int last = e.rows - 1 - (key0 & ~63);
+    if (key0 < e.rows) {
 #pragma unroll
-    for (int kk = 0; kk < 8; ++kk) K[kk] = ld8(kp + 16 * kk), V[kk] = ld8(vp + 16 * kk);
+      for (int y = 0; y < 2; ++y) {
+        const int sub = 2 * (wave & 1) + y;
+        uint32_t vo[4];
+        copy_offsets(vo, sub, lane, last, (uint32_t)(a.vs * 2));
+        copy4(vb, vo, v0 + sub * 4096);
+      }
+    }
   }
   f32x16 dK[4], dV[4];
 #pragma unroll
   for (int dt = 0; dt < 4; ++dt) dK[dt] = zero16(), dV[dt] = zero16();
   const float c = a.scale * LOG2E;
   const int64_t gs = (int64_t)a.Hq * HD;
-  const uint32_t lds0 = lds_addr(lds), stat0 = lds_addr(&stats[0][0][0]);
-  uint32_t qo[4], go[4];
-  auto copy = [&](int g, int t, int buf) {
-    const int last = min(KT, Lq - t) - 1, head = head0 + g;
-    copy_offsets(qo, wave, lane, last, (uint32_t)(a.qs * 2));
-    copy_offsets(go, wave, lane, last, (uint32_t)(gs * 2));
-    const uint32_t to = lds0 + buf * 2 * TILE_BYTES + wave * 4096;
-    const int64_t r = e.other0 + t;
-    copy4(a.q + r * a.qs + head * HD, qo, to);
-    copy4(a.go + r * gs + head * HD, go, to + TILE_BYTES);
-    if (wave < 2) lds_dma<4>((wave ? a.delta : a.lse2) + (int64_t)head * a.Tq + r + min(lane, last), stat0 + (buf * 2 + wave) * KT * 4);
+  auto copy = [&](int g, int t, int buf) {  // the first four wavefronts bring Q, the others dO
+    uint32_t off[4];
+    const int ln = afresh(lane), last = min(KT, Lq - t) - 1, head = kvh * a.group + g, part = wave & 3;
+    const bool q = wave < 4;
+    const int64_t r = e.other0 + t, stride = q ? a.qs : gs;
+    copy_offsets(off, part, ln, last, (uint32_t)(stride * 2));
+    copy4((q ? a.q : a.go) + r * stride + head * HD, off, lds0 + (buf * 2 + !q) * TILE_BYTES + part * 4096);
+    if (part == 0) lds_dma<4>((q ? a.lse2 : a.delta) + (int64_t)head * a.Tq + r + min(ln, last), stat0 + (buf * 2 + !q) * KT * 4);
   };
-  drain_vmem();
-  int g = 0, t = begin, buf = 0;
-  if (begin < end) copy(0, begin, 0);
-  else g = per;
-  while (g < per) {
+  int g = steps ? (int)(it / steps) : 0, t = steps ? begin + (int)(it - (int64_t)g * steps) * KT : 0, buf = 0;
+  if (it < last_it) copy(g, t, 0);
+  bf16x8 K[8];
+  {
+    const int row = min(key0 + lr, e.rows - 1);
+    const u16 *kp = a.k + (int64_t)(e.row0 + row) * a.ks + kvh * HD + 8 * h;
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) K[kk] = ld8(kp + 16 * kk);
+  }
+  // rows that see this wavefront's first and last key, first ones
+  const int x0 = f0 + key0, x1 = f0 + min(key0 + 31, e.rows - 1);
+  for (; it < last_it; ++it, buf ^= 1) {
     drain_vmem();
     lds_barrier();
     int g2 = g, t2 = t + KT;
     if (t2 >= end) t2 = begin, ++g2;
-    if (g2 < per) copy(g2, t2, buf ^ 1);
-    const unsigned char *qt = lds + buf * 2 * TILE_BYTES, *gt = qt + TILE_BYTES;
-    const float *ls = stats[buf][0], *dl = stats[buf][1];
-    const int x0 = f0 + 32 * wave, x1 = f0 + kmax;  // the first rows that see this wavefront's first and last key
-    if (!((a.causal && t + KT - 1 < x0) || (a.window && (int64_t)t > (int64_t)x1 + a.window - 1) || 32 * wave >= e.rows)) {
+    if (it + 1 < last_it) copy(g2, t2, buf ^ 1);
+    const uint32_t q0 = lds0 + buf * 2 * TILE_BYTES;
+    if (!((a.causal && t + KT - 1 < x0) || (a.window && (int64_t)t > (int64_t)x1 + a.window - 1) || key0 >= e.rows)) {
       const bool masked = t + KT > Lq || (a.causal && t < x1) || (a.window && (int64_t)t + KT > (int64_t)x0 + a.window);
+      const uint32_t qt = row_base(q0, lane), qc = col_base(q0, lane), vt = row_base(v0, lane) + 8192 * (wave & 1);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         f32x16 S = zero16(), P = zero16();
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) S = mfma32(row_frag(qt, half, kk, lr, h), K[kk], S);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) P = mfma32(row_frag(gt, half, kk, lr, h), V[kk], P);
+        for (int kk = 0; kk < 8; ++kk) {
+          S = mfma32(row_frag(qt, half, kk), K[kk], S);
+          P = mfma32(row_frag(qt + TILE_BYTES, half, kk), row_frag(vt, 0, kk), P);
+        }
+        const int hh = afresh(lane >> 5);
+        const float *ls = stats[buf][0], *dl = stats[buf][1];
 #pragma unroll
         for (int i4 = 0; i4 < 4; ++i4) {
-          const float4 L = *reinterpret_cast<const float4 *>(ls + 32 * half + 8 * i4 + 4 * h);
-          const float4 E = *reinterpret_cast<const float4 *>(dl + 32 * half + 8 * i4 + 4 * h);
+          const float4 L = *reinterpret_cast<const float4 *>(ls + 32 * half + 8 * i4 + 4 * hh);
+          const float4 E = *reinterpret_cast<const float4 *>(dl + 32 * half + 8 * i4 + 4 * hh);
           const float ll[4] = {L.x, L.y, L.z, L.w}, ee[4] = {E.x, E.y, E.z, E.w};
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
@@ -205,6 +225,9 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(BwdArgs a) {
           }
         }
         if (masked) {
+          const int ln = afresh(lane), lr = ln & 31, h = ln >> 5;
+          const int y = x0 + lr;  // this lane's key; those past the last are not stored
+          const int lo = a.causal ? y : 0, hi = a.window ? (int)min((int64_t)Lq - 1, (int64_t)y + a.window - 1) : Lq - 1;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int r = t + 32 * half + 8 * (i >> 2) + 4 * h + (i & 3);
@@ -213,59 +236,77 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(BwdArgs a) {
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          const bf16x8 p = acc_frag(S, s), ds = acc_frag(P, s);
+          const bf16x8 p = acc_frag(S, s);
 #pragma unroll
-          for (int dt = 0; dt < 4; ++dt) dV[dt] = mfma32(col_frag(gt, 2 * half + s, dt, lane), p, dV[dt]);
+          for (int dt = 0; dt < 4; ++dt) dV[dt] = mfma32(col_frag(qc + TILE_BYTES, 2 * half + s, dt), p, dV[dt]);
+        }
 #pragma unroll
-          for (int dt = 0; dt < 4; ++dt) dK[dt] = mfma32(col_frag(qt, 2 * half + s, dt, lane), ds, dK[dt]);
+        for (int s = 0; s < 2; ++s) {
+          const bf16x8 d = acc_frag(P, s);
+#pragma unroll
+          for (int dt = 0; dt < 4; ++dt) dK[dt] = mfma32(col_frag(qc, 2 * half + s, dt), d, dK[dt]);
         }
       }
     }
-    g = g2, t = t2, buf ^= 1;
+    g = g2, t = t2;
   }
-  if (a.parts == 1) {
-    store_row(a.dk + (int64_t)(e.row0 + row) * a.dks + kvh * HD, dK, a.scale, h, live);
-    store_row(a.dv + (int64_t)(e.row0 + row) * a.dvs + kvh * HD, dV, 1.f, h, live);
+  drain_vmem();  // a block without steps has its values' copies still in flight
+  const int ln = afresh(lane), lr2 = ln & 31, h2 = ln >> 5, row = min(key0 + lr2, e.rows - 1);
+  const bool live = key0 + lr2 < e.rows;
+  if (x.parts == 1) {
+    store_row(a.dk + (int64_t)(e.row0 + row) * a.dks + kvh * HD, dK, a.scale, h2, live);
+    store_row(a.dv + (int64_t)(e.row0 + row) * a.dvs + kvh * HD, dV, 1.f, h2, live);
   } else if (live) {
-    const int64_t to = part * a.partial + ((int64_t)(e.row0 + row) * a.Hkv + kvh) * HD + 4 * h;
-#pragma unroll
-    for (int dt = 0; dt < 4; ++dt)
-#pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        const int64_t x = to + 32 * dt + 2 * i;
-        *reinterpret_cast<f32x4 *>(a.pk + x) = f32x4{dK[dt][i], dK[dt][i + 1], dK[dt][i + 2], dK[dt][i + 3]};
-        *reinterpret_cast<f32x4 *>(a.pv + x) = f32x4{dV[dt][i], dV[dt][i + 1], dV[dt][i + 2], dV[dt][i + 3]};
-      }
+    const int64_t to = x.part * a.part_size + ((int64_t)(e.row0 + row) * a.Hkv + kvh) * HD;
+    store_floats(a.pk + to, dK, h2);
+    store_floats(a.pv + to, dV, h2);
   }
 }
 
-// The parts' sums, added in order; a thread takes 4 channels of a row of dk or dv.
-__global__ __launch_bounds__(256) void attn_join_kernel(BwdArgs a) {
-  const int64_t n = (int64_t)a.Tk * a.Hkv * (HD / 4), i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= 2 * n) return;
-  const bool v = i >= n;
-  const int64_t x = v ? i - n : i;
-  const float *src = (v ? a.pv : a.pk) + 4 * x;
-  f32x4 s = *reinterpret_cast<const f32x4 *>(src);
-  for (int part = 1; part < a.parts; ++part) s += *reinterpret_cast<const f32x4 *>(src + part * a.partial);
-  const float f = v ? 1.f : a.scale;
-  const int64_t r = x / (a.Hkv * (HD / 4)), y = x - r * (a.Hkv * (HD / 4));
-  *reinterpret_cast<uint2 *>((v ? a.dv + r * a.dvs : a.dk + r * a.dks) + 4 * y) = make_uint2(pk2bf(s[0] * f, s[1] * f), pk2bf(s[2] * f, s[3] * f));
+// Adds the parts of a tile's rows in order: 16 threads a row, 8 channels each.  KEYS: dk and dv
+// of a tile of keys, otherwise dq of a tile of query rows.
+template <bool KEYS>
+__global__ __launch_bounds__(256) void attn_bwd_join_kernel(BwdArgs a) {
+  const int rows = (KEYS ? ATT_KTILE : ATT_QTILE) / 16;  // blocks a tile
+  const int heads = KEYS ? a.Hkv : a.Hq;
+  const int64_t b = blockIdx.x / rows;
+  const int head = (int)(b % heads);
+  const TileEntry e(a.tiles, (int)(b / heads));
+  const int parts = e.parts(a.level);
+  const int r = (blockIdx.x % rows) * 16 + (threadIdx.x >> 4), c = (threadIdx.x & 15) * 8;
+  if (parts == 1 || r >= e.rows) return;
+  const int64_t row = e.row0 + r, at = (row * heads + head) * HD + c;
+#pragma unroll
+  for (int side = 0; side < (KEYS ? 2 : 1); ++side) {
+    const float *src = (KEYS ? (side ? a.pv : a.pk) : a.pq) + at;
+    const float f = side ? 1.f : a.scale;
+    f32x4 u = zero4(), v = zero4();
+    for (int x = 0; x < parts; ++x) {
+      const f32x4 *p = reinterpret_cast<const f32x4 *>(src + x * a.part_size);
+      u += p[0], v += p[1];
+    }
+    u16 *to = KEYS ? (side ? a.dv + row * a.dvs : a.dk + row * a.dks) : a.dq + row * a.dqs;
+    *reinterpret_cast<u32x4 *>(to + head * HD + c) =
+        u32x4{pk2bf(u[0] * f, u[1] * f), pk2bf(u[2] * f, u[3] * f), pk2bf(v[0] * f, v[1] * f), pk2bf(v[2] * f, v[3] * f)};
+  }
 }
 
-BwdArgs args(const gdr_attn &p, void *ws) {
-  const AttnWorkspace w = attn_workspace(p.T_q, p.T_k, p.n_k_tiles, p.H_q, p.H_kv);
+BwdArgs args(const gdr_attn &p, bool keys, void *ws) {
+  const AttnWorkspace w = attn_workspace(p);
   char *base = static_cast<char *>(ws);
   BwdArgs a{};
   a.q = p.q, a.k = p.k, a.v = p.v;
-  a.tiles = p.tile_table;
+  a.tiles = p.tile_table + (keys ? (int64_t)p.plan.n_q_tiles * ATT_ENTRY : 0);
   a.lse2 = reinterpret_cast<float *>(base);
   a.delta = reinterpret_cast<float *>(base + w.stats);
-  a.pk = reinterpret_cast<float *>(base + 2 * w.stats);
-  a.pv = reinterpret_cast<float *>(base + 2 * w.stats + w.parts * w.partial);
-  a.partial = w.partial / 4;
+  a.pq = a.pk = reinterpret_cast<float *>(base + 2 * w.stats);
+  a.pv = a.pk + w.k.parts * (w.k_part / 4);
+  a.part_size = (keys ? w.k_part : w.q_part) / 4;
+  const AttnShare &share = keys ? w.k : w.q;
+  a.level = share.level;
+  a.items = share.level < 0 ? nullptr : p.tile_table + share.items;
   a.qs = p.q_stride, a.ks = p.k_stride, a.vs = p.v_stride;
-  a.Hq = p.H_q, a.Hkv = p.H_kv, a.group = p.H_q / p.H_kv, a.Tq = p.T_q, a.Tk = p.T_k, a.parts = w.parts;
+  a.Hq = p.H_q, a.Hkv = p.H_kv, a.group = p.H_q / p.H_kv, a.Tq = p.T_q, a.Tk = p.T_k;
   a.causal = p.causal, a.window = p.window < p.T_k ? p.window : 0, a.scale = p.scale;
   return a;
 }
@@ -274,30 +315,34 @@ BwdArgs args(const gdr_attn &p, void *ws) {
 
 hipError_t launch_attn_dq(const gdr_attn &p, const uint16_t *o, const float *lse, const uint16_t *dout, uint16_t *dq,
                           int64_t dq_stride, void *ws, hipStream_t stream) {
-  if (p.n_q_tiles == 0) return hipSuccess;
-  BwdArgs a = args(p, ws);
+  if (p.plan.n_q_tiles == 0) return hipSuccess;
+  BwdArgs a = args(p, false, ws);
   a.o = o, a.lse = lse, a.go = dout, a.dq = dq, a.dqs = dq_stride;
-  attn_dq_kernel<<<dim3((uint32_t)((int64_t)p.n_q_tiles * p.H_q)), 256, 0, stream>>>(a);
+  attn_dq_kernel<<<dim3((uint32_t)(attn_q_share(p).blocks * p.H_q)), 256, 0, stream>>>(a);
+  return hipGetLastError();
+}
+hipError_t launch_attn_dq_join(const gdr_attn &p, uint16_t *dq, int64_t dq_stride, void *ws, hipStream_t stream) {
+  if (p.plan.n_q_tiles == 0) return hipSuccess;
+  BwdArgs a = args(p, false, ws);
+  a.dq = dq, a.dqs = dq_stride;
+  attn_bwd_join_kernel<false><<<dim3((uint32_t)((int64_t)p.plan.n_q_tiles * p.H_q * (ATT_QTILE / 16))), 256, 0, stream>>>(a);
   return hipGetLastError();
 }
 
 hipError_t launch_attn_dkv(const gdr_attn &p, const uint16_t *dout, uint16_t *dk, int64_t dk_stride, uint16_t *dv,
                            int64_t dv_stride, void *ws, hipStream_t stream) {
-  if (p.n_k_tiles == 0) return hipSuccess;
-  BwdArgs a = args(p, ws);
-  a.tiles += (int64_t)p.n_q_tiles * ATT_ENTRY;
+  if (p.plan.n_k_tiles == 0) return hipSuccess;
+  BwdArgs a = args(p, true, ws);
   a.go = dout, a.dk = dk, a.dv = dv, a.dks = dk_stride, a.dvs = dv_stride;
-  attn_dkv_kernel<<<dim3((uint32_t)((int64_t)p.n_k_tiles * p.H_kv * a.parts)), 256, 0, stream>>>(a);
+  attn_dkv_kernel<<<dim3((uint32_t)(attn_k_share(p).blocks * p.H_kv)), 512, 0, stream>>>(a);
   return hipGetLastError();
 }
-
-hipError_t launch_attn_join(const gdr_attn &p, uint16_t *dk, int64_t dk_stride, uint16_t *dv, int64_t dv_stride, void *ws,
-                            hipStream_t stream) {
-  BwdArgs a = args(p, ws);
-  if (a.parts == 1 || p.T_k == 0) return hipSuccess;
+hipError_t launch_attn_dkv_join(const gdr_attn &p, uint16_t *dk, int64_t dk_stride, uint16_t *dv, int64_t dv_stride, void *ws,
+                                hipStream_t stream) {
+  if (p.plan.n_k_tiles == 0) return hipSuccess;
+  BwdArgs a = args(p, true, ws);
   a.dk = dk, a.dv = dv, a.dks = dk_stride, a.dvs = dv_stride;
-  const int64_t n = 2 * (int64_t)p.T_k * p.H_kv * (HD / 4);
-  attn_join_kernel<<<dim3((uint32_t)((n + 255) / 256)), 256, 0, stream>>>(a);
+  attn_bwd_join_kernel<true><<<dim3((uint32_t)((int64_t)p.plan.n_k_tiles * p.H_kv * (ATT_KTILE / 16))), 256, 0, stream>>>(a);
   return hipGetLastError();
 }
 

@@ -59,22 +59,29 @@ __device__ __forceinline__ void copy_offsets(uint32_t (&off)[4], int wave, int l
   }
 }
 
-// A operand along the rows: channels 16 kk + 8 h .. +7 of row 32 half + lr.
-__device__ __forceinline__ bf16x8 row_frag(const unsigned char *tile, int half, int kk, int lr, int h) {
-  return ld8(reinterpret_cast<const u16 *>(tile + (32 * half + lr) * 256 + ((2 * kk + h) ^ swz(lr)) * 16));
+// A lane's LDS byte address in a tile that begins at `tile`, from which its pieces for all
+// kk, dt and steps follow by one exclusive or and a constant: the tile's bytes are
+// 256 r + 16 (c ^ swz(r)), and kk or dt enter c as bits of their own.
+__device__ __forceinline__ uint32_t row_base(uint32_t tile, int lane) {
+  const int lr = lane & 31, h = lane >> 5;
+  return tile + lr * 256 + (h ^ swz(lr)) * 16;
 }
-// A operand across the rows (the tile's transpose): channel 32 dt + lr of rows
-// 16 step + kacc(h, j).  ds_read_b64_tr_b16 hands lane 4 a + e of each 16 lanes element e of
-// the 8-byte pieces that lanes a, 4 + a, 8 + a and 12 + a of them address.
-__device__ __forceinline__ bf16x8 col_frag(const unsigned char *tile, int step, int dt, int lane) {
+// ds_read_b64_tr_b16 hands lane 4 a + e of each 16 lanes element e of the 8-byte pieces that
+// lanes a, 4 + a, 8 + a and 12 + a of them address.
+__device__ __forceinline__ uint32_t col_base(uint32_t tile, int lane) {
+  const int i = lane & 15, b = (lane >> 4) & 1, r = 4 * (lane >> 5) + (i >> 2);  // row within 8
+  return tile + r * 256 + ((2 * b + ((i >> 1) & 1)) ^ (2 * r)) * 16 + 8 * (i & 1);
+}
+// A operand along the rows: channels 16 kk + 8 h .. +7 of row 32 half + lr.
+__device__ __forceinline__ bf16x8 row_frag(uint32_t base, int half, int kk) {
+  return *(const __attribute__((address_space(3))) bf16x8 *)((base ^ (32u * kk)) + 8192u * half);
+}
+// A operand across the rows (the tile's transpose): channel 32 dt + lr of rows 16 step + kacc(h, j).
+__device__ __forceinline__ bf16x8 col_frag(uint32_t base, int step, int dt) {
   typedef __attribute__((address_space(3))) bf16x4v *lds_v4;
-  const int i = lane & 15, b = (lane >> 4) & 1, h = lane >> 5;
-  const int r = 4 * h + (i >> 2);                     // row within 8
-  const int c = (4 * dt + 2 * b + ((i >> 1) & 1)) ^ (2 * r);  // piece, for rows whose bit 3 is clear
-  unsigned char *lo = const_cast<unsigned char *>(tile) + (16 * step + r) * 256 + c * 16 + 8 * (i & 1);
-  unsigned char *hi = const_cast<unsigned char *>(tile) + (16 * step + 8 + r) * 256 + (c ^ 1) * 16 + 8 * (i & 1);
-  const bf16x4v x = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_v4)lo);
-  const bf16x4v y = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_v4)hi);
+  const uint32_t at = base ^ (64u * dt);
+  const bf16x4v x = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_v4)(at + 4096u * step));
+  const bf16x4v y = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_v4)((at ^ 16u) + 4096u * step + 2048u));
   const uint2 u = __builtin_bit_cast(uint2, x), v = __builtin_bit_cast(uint2, y);
   return __builtin_bit_cast(bf16x8, u32x4{u.x, u.y, v.x, v.y});
 }
@@ -105,19 +112,43 @@ __device__ __forceinline__ void store_row(u16 *row, const f32x16 (&acc)[4], floa
     }
 }
 
-// The tile and query head of a block.  Block ids go round the 8 XCDs; where the
-// heads divide by 8 an XCD takes neighbouring heads, which share keys in its L2.
-__device__ __forceinline__ void tile_of(int b, int heads, int &tile, int &head) {
-  tile = b / heads;
-  const int r = b - tile * heads;
-  head = (heads & 7) == 0 ? (r & 7) * (heads >> 3) + (r >> 3) : r;
+// The same in fp32, to a row of a part.
+__device__ __forceinline__ void store_floats(float *row, const f32x16 (&acc)[4], int h) {
+#pragma unroll
+  for (int dt = 0; dt < 4; ++dt)
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+      *reinterpret_cast<f32x4 *>(row + 32 * dt + 8 * a + 4 * h) =
+          f32x4{acc[dt][4 * a], acc[dt][4 * a + 1], acc[dt][4 * a + 2], acc[dt][4 * a + 3]};
 }
 
+// The tile, its part and the head of a block.  Block ids go round the 8 XCDs; where the
+// heads divide by 8 an XCD takes neighbouring heads, which share keys in its L2.
+struct Share {
+  int tile, part, parts, head;
+  __device__ __forceinline__ Share(const int32_t *items, int b, int heads) {
+    tile = b / heads;
+    const int r = b - tile * heads;
+    head = (heads & 7) == 0 ? (r & 7) * (heads >> 3) + (r >> 3) : r;
+    part = 0, parts = 1;
+    if (items) {
+      ConstI32 it = (ConstI32)(items + 2 * (int64_t)tile);
+      tile = it[0];
+      part = it[1] & 0xffff, parts = it[1] >> 16;
+    }
+  }
+};
+
 struct TileEntry {
-  int row0, rows, other0, other, first, shift;
+  int row0, rows, other0, other, first, shift, begin, end;
   __device__ __forceinline__ TileEntry(const int32_t *table, int i) {
     ConstI32 e = (ConstI32)(table + (int64_t)i * ATT_ENTRY);
-    row0 = e[0], rows = e[1], other0 = e[2], other = e[3], first = e[4], shift = e[5];
+    row0 = e[0], rows = e[1], other0 = e[2], other = e[3], first = e[4], shift = e[5], begin = e[6], end = e[7];
+  }
+  // Steps of 64 of the other side's rows, and into how many parts a list deals them.
+  __device__ __forceinline__ int steps() const { return begin < end ? (end - begin + KT - 1) / KT : 0; }
+  __device__ __forceinline__ int parts(int level) const {
+    return min(max((steps() + (1 << level) - 1) >> level, 1), ATT_PARTS);
   }
 };
 

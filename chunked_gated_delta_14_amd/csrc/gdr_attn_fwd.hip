@@ -18,11 +18,13 @@ namespace {
 
 struct FwdArgs {
   const u16 *q, *k, *v;
-  const int32_t *tiles;
+  const int32_t *tiles, *items;
   u16 *o;
   float *lse;
+  float *part, *ml;  // [part][T_q][H_q][128], [part][H_q][T_q][2]
   int64_t qs, ks, vs;
-  int Hq, group, Tq, causal, window;
+  int64_t part_size, ml_size;  // floats of one part's
+  int Hq, group, Tq, causal, window, level;
   float scale;
 };
 
@@ -30,28 +32,21 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdArgs a) {
   __shared__ __align__(16) unsigned char lds[4 * TILE_BYTES];  // K, V; twice
   const int lane = threadIdx.x & 63, lr = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int tile, head;
-  tile_of(blockIdx.x, a.Hq, tile, head);
-  const TileEntry e(a.tiles, tile);
-  const int kvh = head / a.group;
+  const Share x(a.items, blockIdx.x, a.Hq);
+  const TileEntry e(a.tiles, x.tile);
+  const int head = x.head, kvh = head / a.group, steps = e.steps();
   const u16 *kb = a.k + e.other0 * a.ks + kvh * HD, *vb = a.v + e.other0 * a.vs + kvh * HD;
   const int Lk = e.other;
 
-  // the keys this block's rows see: begin .. end - 1; those of this wavefront's first and last row
+  // the keys that this wavefront's first and last row see last, and this part's share of the tile's keys
   const int rmax = min(32 * wave + 31, e.rows - 1);
   const int p0 = e.first + 32 * wave + e.shift, p1 = e.first + rmax + e.shift;
-  const int end = a.causal ? min(Lk, e.first + e.rows + e.shift) : Lk;
-  const int begin = a.window ? max(0, e.first + e.shift - a.window + 1) & ~(KT - 1) : 0;
+  const int begin = e.begin + (int)((int64_t)steps * x.part / x.parts) * KT;
+  const int end = min(e.end, e.begin + (int)((int64_t)steps * (x.part + 1) / x.parts) * KT);
   const int row = min(32 * wave + lr, e.rows - 1);
   const int p = e.first + row + e.shift;
   const int hi = a.causal ? min(p, Lk - 1) : Lk - 1, lo = a.window ? p - a.window + 1 : 0;  // this lane's row
 
-  bf16x8 Q[8];
-  {
-    const u16 *qp = a.q + (int64_t)(e.row0 + row) * a.qs + head * HD + 8 * h;
-#pragma unroll
-    for (int kk = 0; kk < 8; ++kk) Q[kk] = ld8(qp + 16 * kk);
-  }
   f32x16 O[4];
 #pragma unroll
   for (int dt = 0; dt < 4; ++dt) O[dt] = zero16();
@@ -71,21 +66,26 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdArgs a) {
     copy4(kb + t * a.ks, ko, to);
     copy4(vb + t * a.vs, vo, to + TILE_BYTES);
   };
-  drain_vmem();  // the query rows are settled before the copies, which the compiler does not count
   if (begin < end) copy(begin, 0);
+  bf16x8 Q[8];
+  {
+    const u16 *qp = a.q + (int64_t)(e.row0 + row) * a.qs + head * HD + 8 * h;
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) Q[kk] = ld8(qp + 16 * kk);
+  }
   int buf = 0;
   for (int t = begin; t < end; t += KT, buf ^= 1) {
     drain_vmem();
     lds_barrier();  // tile t is there, and everyone is through with the other buffer
     if (t + KT < end) copy(t + KT, buf ^ 1);
-    const unsigned char *kt = lds + buf * 2 * TILE_BYTES, *vt = kt + TILE_BYTES;
-    // a wavefront none of whose rows sees a key of this tile
-    if ((a.causal && t > p1) || (a.window && t + KT <= p0 - a.window + 1)) continue;
+    const uint32_t kt = row_base(lds0 + buf * 2 * TILE_BYTES, lane), vt = col_base(lds0 + (buf * 2 + 1) * TILE_BYTES, lane);
+    // a wavefront without rows, or none of whose rows sees a key of this tile
+    if ((a.causal && t > p1) || (a.window && t + KT <= p0 - a.window + 1) || 32 * wave >= e.rows) continue;
     f32x16 S[2] = {zero16(), zero16()};
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
-      for (int half = 0; half < 2; ++half) S[half] = mfma32(row_frag(kt, half, kk, lr, h), Q[kk], S[half]);
+      for (int half = 0; half < 2; ++half) S[half] = mfma32(row_frag(kt, half, kk), Q[kk], S[half]);
     const bool masked = t + KT > Lk || (a.causal && t + KT - 1 > p0) || (a.window && t <= p1 - a.window);
     if (masked) {
 #pragma unroll
@@ -121,24 +121,68 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdArgs a) {
     for (int step = 0; step < 4; ++step) {
       const bf16x8 P = acc_frag(S[step >> 1], step & 1);
 #pragma unroll
-      for (int dt = 0; dt < 4; ++dt) O[dt] = mfma32(col_frag(vt, step, dt, lane), P, O[dt]);
+      for (int dt = 0; dt < 4; ++dt) O[dt] = mfma32(col_frag(vt, step, dt), P, O[dt]);
     }
   }
   l += other_half(l);
   const bool live = 32 * wave + lr < e.rows;
-  const float f = l == 0.f ? 0.f : 1.f / l;
-  store_row(a.o + ((int64_t)(e.row0 + row) * a.Hq + head) * HD, O, f, h, live);
-  if (a.lse && live && h == 0)
-    a.lse[(int64_t)head * a.Tq + e.row0 + row] = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * LN2;
+  if (x.parts == 1) {
+    store_row(a.o + ((int64_t)(e.row0 + row) * a.Hq + head) * HD, O, l == 0.f ? 0.f : 1.f / l, h, live);
+    if (a.lse && live && h == 0)
+      a.lse[(int64_t)head * a.Tq + e.row0 + row] = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * LN2;
+  } else if (live) {
+    store_floats(a.part + x.part * a.part_size + ((int64_t)(e.row0 + row) * a.Hq + head) * HD, O, h);
+    if (h == 0) *reinterpret_cast<float2 *>(a.ml + x.part * a.ml_size + 2 * ((int64_t)head * a.Tq + e.row0 + row)) = make_float2(m, l);
+  }
+}
+
+// Joins the parts of a tile's rows: 16 threads a row, 8 channels each.
+__global__ __launch_bounds__(256) void attn_fwd_join_kernel(FwdArgs a) {
+  const int rows = ATT_QTILE / 16;  // blocks a tile
+  const int64_t b = blockIdx.x / rows;
+  const int head = (int)(b % a.Hq);
+  const TileEntry e(a.tiles, (int)(b / a.Hq));
+  const int parts = e.parts(a.level), r = (blockIdx.x % rows) * 16 + (threadIdx.x >> 4);
+  if (parts == 1 || r >= e.rows) return;
+  const int c = (threadIdx.x & 15) * 8;
+  const int64_t row = e.row0 + r, at = (row * a.Hq + head) * HD + c;
+  const float *ml = a.ml + 2 * ((int64_t)head * a.Tq + row);
+  float M = -1.5e38f, L = 0.f, y[8] = {};
+  for (int x = 0; x < parts; ++x) M = fmaxf(M, ml[x * a.ml_size]);
+  for (int x = 0; x < parts; ++x) {
+    const float f = __builtin_amdgcn_exp2f(ml[x * a.ml_size] - M);
+    L = fmaf(ml[x * a.ml_size + 1], f, L);
+    const f32x4 *src = reinterpret_cast<const f32x4 *>(a.part + x * a.part_size + at);
+    const f32x4 u = src[0], v = src[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = fmaf(u[i], f, y[i]), y[4 + i] = fmaf(v[i], f, y[4 + i]);
+  }
+  const float f = L == 0.f ? 0.f : 1.f / L;
+  *reinterpret_cast<u32x4 *>(a.o + at) =
+      u32x4{pk2bf(y[0] * f, y[1] * f), pk2bf(y[2] * f, y[3] * f), pk2bf(y[4] * f, y[5] * f), pk2bf(y[6] * f, y[7] * f)};
+  if (a.lse && c == 0) a.lse[(int64_t)head * a.Tq + row] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * LN2;
+}
+
+FwdArgs args(const gdr_attn &p, uint16_t *o, float *lse, void *ws) {
+  const AttnWorkspace w = attn_workspace(p);
+  const AttnShare share = ws ? w.q : AttnShare{-1, 1, p.plan.n_q_tiles, 0};
+  float *part = static_cast<float *>(ws);
+  return FwdArgs{p.q, p.k, p.v, p.tile_table, share.level < 0 ? nullptr : p.tile_table + share.items, o, lse, part, part + share.parts * (w.q_part / 4), p.q_stride, p.k_stride, p.v_stride,
+                 w.q_part / 4, ((int64_t)p.T_q * p.H_q * 8 + 255) / 256 * 64, p.H_q, p.H_q / p.H_kv, p.T_q, p.causal,
+                 p.window < p.T_k ? p.window : 0, share.level, p.scale};
 }
 
 }  // namespace
 
-hipError_t launch_attn_fwd(const gdr_attn &p, uint16_t *o, float *lse, hipStream_t stream) {
-  if (p.n_q_tiles == 0) return hipSuccess;
-  const FwdArgs a{p.q, p.k, p.v, p.tile_table, o, lse, p.q_stride, p.k_stride, p.v_stride, p.H_q, p.H_q / p.H_kv, p.T_q,
-                  p.causal, p.window < p.T_k ? p.window : 0, p.scale};
-  attn_fwd_kernel<<<dim3((uint32_t)((int64_t)p.n_q_tiles * p.H_q)), 256, 0, stream>>>(a);
+hipError_t launch_attn_fwd(const gdr_attn &p, uint16_t *o, float *lse, void *ws, hipStream_t stream) {
+  if (p.plan.n_q_tiles == 0) return hipSuccess;
+  const int64_t blocks = ws ? attn_q_share(p).blocks : p.plan.n_q_tiles;
+  attn_fwd_kernel<<<dim3((uint32_t)(blocks * p.H_q)), 256, 0, stream>>>(args(p, o, lse, ws));
+  return hipGetLastError();
+}
+hipError_t launch_attn_fwd_join(const gdr_attn &p, uint16_t *o, float *lse, void *ws, hipStream_t stream) {
+  if (p.plan.n_q_tiles == 0) return hipSuccess;
+  attn_fwd_join_kernel<<<dim3((uint32_t)((int64_t)p.plan.n_q_tiles * p.H_q * (ATT_QTILE / 16))), 256, 0, stream>>>(args(p, o, lse, ws));
   return hipGetLastError();
 }
 

@@ -472,17 +472,28 @@ int32_t gdr_rope_bwd(const gdr_rope *p, const void *dq_out, int64_t dq_out_strid
  * or value does not reach a row's forward output, finite or not; the backward takes finite operands: a
  * value that is not may reach gradients up to 127 rows or keys away in its document.
  *
- * gdr_plan_attn: host planner of the tiles, the longest first.  cu_k NULL: cu_q's.
- * A first call with table NULL gives *table_len (int32s), *n_q_tiles and *n_k_tiles.
- * The table depends on causal and window; the problem has the same ones. */
+ * gdr_plan_attn: host planner of the tiles of 128 query rows and of 256 keys, those with the
+ * most work first.  cu_k NULL: cu_q's.  A first call with table NULL fills *plan, whose table_len is
+ * the int32s that the table takes.  The plan depends on causal and window; the problem has the
+ * same ones. */
+#define GDR_ATTN_LEVELS 12
+typedef struct gdr_attn_plan {
+  int32_t n_q_tiles, n_k_tiles;
+  int32_t q_longest, k_longest; /* steps (64 keys, 64 rows of one query head) of the longest tile of either kind */
+  int64_t q_steps, k_steps;     /* steps of all tiles */
+  int64_t table_len;
+  /* Entries of the table's lists of parts: list i deals out tiles of more than 2^i steps evenly in as few
+   * parts of at most that as it takes (64 at most).  0: there is no list i. */
+  int32_t q_items[GDR_ATTN_LEVELS], k_items[GDR_ATTN_LEVELS];
+} gdr_attn_plan;
 int32_t gdr_plan_attn(const int32_t *cu_q, const int32_t *cu_k, int32_t N, int32_t causal, int32_t window, int32_t *table,
-                      int64_t capacity, int32_t *n_q_tiles, int32_t *n_k_tiles, int64_t *table_len);
+                      int64_t capacity, gdr_attn_plan *plan);
 
 typedef struct gdr_attn {
   int32_t T_q, T_k, N;
   int32_t H_q, H_kv, D;      /* D == 128 */
   int32_t causal, window;    /* window 0: none */
-  int32_t n_q_tiles, n_k_tiles;
+  gdr_attn_plan plan;
   float scale;
   int64_t q_stride, k_stride, v_stride;
   const uint16_t *q;         /* bf16 [T_q, H_q, D] */
@@ -490,9 +501,11 @@ typedef struct gdr_attn {
   const int32_t *tile_table; /* device copy of the gdr_plan_attn table */
 } gdr_attn;
 
-/* o: bf16 [T_q, H_q, D]; lse: fp32 [H_q, T_q], or NULL to skip. */
-int32_t gdr_attn_fwd(const gdr_attn *p, uint16_t *o, float *lse, void *stream);
-int64_t gdr_attn_workspace_bytes(int32_t T_q, int32_t T_k, int32_t n_k_tiles, int32_t H_q, int32_t H_kv);
+/* Workspace bytes of the forward (backward == 0) or of the backward, or minus a gdr_status. */
+int64_t gdr_attn_workspace_bytes(const gdr_attn *p, int32_t backward);
+/* o: bf16 [T_q, H_q, D]; lse: fp32 [H_q, T_q], or NULL to skip.  With a workspace, few rows with
+ * many keys are shared by more blocks, whose results a second kernel joins; NULL: never. */
+int32_t gdr_attn_fwd(const gdr_attn *p, uint16_t *o, float *lse, void *workspace, int64_t workspace_bytes, void *stream);
 /* o, lse: as the forward wrote them; dout: bf16 [T_q, H_q, D].  Writes dq [T_q, H_q, D] and
  * dk, dv [T_k, H_kv, D] (bf16; dk and dv sum over the query heads of a kv head in fp32).
  * No atomics: results repeat bit for bit. */

@@ -90,6 +90,11 @@ CASES = [
     ([100, 40], [700, 20], 2, 1, True, 50, 0),
     ([1, 1, 1], [1000, 64, 65], 8, 2, True, 0, 0),
     ([1100], None, 2, 2, True, 0, 0),
+    # few tiles with many steps: shared by several blocks
+    ([2000, 30, 0, 700], None, 4, 1, True, 0, 64),
+    ([40, 3], [5000, 1], 8, 2, True, 0, 0),
+    ([1500], [2500], 2, 1, False, 0, 8),
+    ([3000], None, 1, 1, True, 1500, 0),
 ]
 
 
