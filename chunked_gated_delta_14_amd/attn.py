@@ -71,6 +71,13 @@ def declare(L) -> None:
     L.gdr_attn_step_workspace_bytes.argtypes, L.gdr_attn_step_workspace_bytes.restype = [_i32] * 6, _i64
 
 
+def _heads(t, name, shape, dtype, device):
+    """Rows of [T, H, D] at any stride, as _rows checks them; whole tensors and single tokens pass first."""
+    if t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous():
+        return shape[1] * shape[2] or 1
+    return _rows(t, name, shape, dtype, device)
+
+
 # ---- rotary positions ----
 
 
@@ -129,7 +136,7 @@ def _rope_side(prob, t, H, name):
         return None, 0
     if t is None:
         _bad("%s is None" % name)
-    return _p(t), _rows(t, name, (prob.T, H, prob.D), prob.dtype, prob.device)
+    return t.data_ptr(), _heads(t, name, (prob.T, H, prob.D), prob.dtype, prob.device)
 
 
 def rope_fwd(prob, q_out, k_out=None, stream=None):
@@ -231,7 +238,7 @@ def attn_bwd(prob, o, lse, dout, dq, dk, dv, workspace, stream=None):
     _need(o, "o", q, bf, dev)
     _need(dout, "dout", q, bf, dev)
     _need(lse, "lse", (prob.H_q, prob.T_q), torch.float32, dev)
-    dqs, dks, dvs = _rows(dq, "dq", q, bf, dev), _rows(dk, "dk", kv, bf, dev), _rows(dv, "dv", kv, bf, dev)
+    dqs, dks, dvs = _heads(dq, "dq", q, bf, dev), _heads(dk, "dk", kv, bf, dev), _heads(dv, "dv", kv, bf, dev)
     ws, nbytes = prob._workspace(workspace)
     _call(prob, stream, "gdr_attn_bwd", _p(o), _p(lse), _p(dout), _p(dq), dqs, _p(dk), dks, _p(dv), dvs, ws, nbytes)
 
@@ -305,7 +312,7 @@ def _kv(name, prob, k, v, stream):
     import torch
 
     shape = (prob.T, prob.cache.H_kv, prob.cache.D)
-    ks, vs = (_rows(t, n, shape, torch.bfloat16, prob.device) for t, n in ((k, "k"), (v, "v")))
+    ks, vs = (_heads(t, n, shape, torch.bfloat16, prob.device) for t, n in ((k, "k"), (v, "v")))
     _call(prob, stream, name, prob.T, _p(prob.cu_seqlens), _p(prob.start), _p(k), ks, _p(v), vs)
 
 

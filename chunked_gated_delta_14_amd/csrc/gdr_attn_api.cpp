@@ -332,7 +332,7 @@ int32_t step(const gdr_kv *c, const gdr_attn_step *p, uint16_t *o, void *ws, int
   if (!element_aligned(p->q, GDR_BF16) || !element_aligned(p->lens, GDR_F32) || !element_aligned(p->cu_seqlens, GDR_F32) || !aligned(o, 16))
     return invalid("q, lens and cu_seqlens must be aligned to their elements, o to 16 bytes");
   const gdr::StepPlan plan = gdr::step_plan(p->T, c->N, p->H_q, c->H_kv, c->max_pages, c->page);
-  if (!grid_ok(plan.blocks, 256) || !grid_ok((int64_t)c->N * p->H_q, 128)) return unsupported("too many sequences and heads for one launch");
+  if (!grid_ok(plan.blocks, 256) || !grid_ok((int64_t)c->N * p->H_q, 256)) return unsupported("too many sequences and heads for one launch");
   if ((rc = check_workspace(ws, ws_bytes, plan.bytes))) return rc;
   if (aliases({o}, {p->q, p->lens, p->cu_seqlens, c->page_table, c->k_codes, c->v_codes, c->k_scale, c->v_scale}))
     return invalid("o is an input");

@@ -47,10 +47,6 @@ struct Span {
   }
 };
 
-struct Loaded {
-  u32x4 k[2], vs[2];
-  uint32_t ks[2], v[8];
-};
 typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
 template <int SEL>
 __device__ __forceinline__ uint32_t pair(uint32_t c, float s) {
@@ -58,7 +54,7 @@ __device__ __forceinline__ uint32_t pair(uint32_t c, float s) {
 }
 __device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
 
-__global__ __launch_bounds__(256) void attn_step_kernel(StepArgs a) {
+__global__ __launch_bounds__(256, 3) void attn_step_kernel(StepArgs a) {
   constexpr int PITCH = 132;
   __shared__ __align__(16) float so[4][16][PITCH];
   __shared__ float sm[4][16], sl[4][16];
@@ -102,46 +98,57 @@ __global__ __launch_bounds__(256) void attn_step_kernel(StepArgs a) {
         if (p >= 0 && p < a.n_pages) pv = p;
       }
     };
-    auto load = [&](int it, Loaded &x) {
-      const int j = from + 32 * (wave + 4 * it);
+    // Keys and values of a tile as they lie in memory.  The next tile's are loaded as soon as this one's
+    // are used, the keys before the softmax and the values after it, into the same registers.
+    u32x4 kc[2], vs[2];
+    uint32_t ks[2], vc[8];
+    auto place = [&](int it, int u) {
+      const int p = max(__builtin_amdgcn_readlane(pv, 2 * (it & 31) + u), 0), j = from + 32 * (wave + 4 * it) + 16 * u;
+      return (((int64_t)p * a.Hkv + kvh) << a.page_shift) + (j & ((1 << a.page_shift) - 1));
+    };
+    auto load_keys = [&](int it) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int p = max(__builtin_amdgcn_readlane(pv, 2 * (it & 31) + u), 0);
-        const int64_t at = ((((int64_t)p * a.Hkv + kvh) << a.page_shift) + ((j + 16 * u) & ((1 << a.page_shift) - 1)));
-        const uint8_t *kc = a.kc + at * 64, *vc = a.vc + at * 64, *ks = a.ksc + at * 4, *vs = a.vsc + at * 4;
-        x.k[u] = *reinterpret_cast<const u32x4 *>(kc + lr * 64 + g * 16);
-        x.ks[u] = ks[lr * 4 + g];
+        const int64_t at = place(it, u);
+        kc[u] = *reinterpret_cast<const u32x4 *>(a.kc + at * 64 + (lr * 64 + g * 16));
+        ks[u] = (a.ksc + at * 4)[lr * 4 + g];
+      }
+    };
+    auto load_values = [&](int it) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) x.v[4 * u + r] = *reinterpret_cast<const uint32_t *>(vc + (4 * g + r) * 64 + lr * 4);
-        x.vs[u] = *reinterpret_cast<const u32x4 *>(vs + g * 16);
+      for (int u = 0; u < 2; ++u) {
+        const int64_t at = place(it, u);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) vc[4 * u + r] = *reinterpret_cast<const uint32_t *>(a.vc + at * 64 + ((4 * g + r) * 64 + lr * 4));
+        vs[u] = *reinterpret_cast<const u32x4 *>(a.vsc + at * 4 + g * 16);
       }
     };
     const int tiles = (to - from + 31) / 32, mine = tiles > wave ? (tiles - wave + 3) / 4 : 0;
-    Loaded x, next;
+    int pg0 = 0, pg1 = 0;
     if (mine > 0) {
       load_pages(0);
-      load(0, x);
+      pg0 = __builtin_amdgcn_readlane(pv, 0), pg1 = __builtin_amdgcn_readlane(pv, 1);
+      load_keys(0);
+      load_values(0);
     }
     for (int it = 0; it < mine; ++it) {
       const int j = from + 32 * (wave + 4 * it);
-      const int pg0 = __builtin_amdgcn_readlane(pv, 2 * (it & 31)), pg1 = __builtin_amdgcn_readlane(pv, 2 * (it & 31) + 1);
-      if (it + 1 < mine) {
-        if (((it + 1) & 31) == 0) load_pages(it + 1);
-        load(it + 1, next);
-      }
+      const bool more = it + 1 < mine;
+      if (more && ((it + 1) & 31) == 0) load_pages(it + 1);
       // tiles whose tokens not every row sees
       const bool masked = j + 32 > s.len - s.run + 1 || j < s.begin || (a.window && j < s.len - a.window) || pg0 < 0 || pg1 < 0;
       f32x4 S[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         S[u] = zero4();
-        const float sc = scale_of(x.ks[u]);
+        const float sc = scale_of(ks[u]);
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-          const uint32_t w = x.k[u][y];
+          const uint32_t w = kc[u][y];
           S[u] = mfma(__builtin_bit_cast(bf16x8, u32x4{pair<0>(w, sc), pair<1>(w, sc), pair<2>(w, sc), pair<3>(w, sc)}), Q[y], S[u]);
         }
       }
+      if (more) load_keys(it + 1);
       if (masked) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -150,7 +157,7 @@ __global__ __launch_bounds__(256) void attn_step_kernel(StepArgs a) {
             const int t = j + 16 * u + 4 * g + r;
             const bool there = (u ? pg1 : pg0) >= 0;
             if (!there || t > hi || t < lo) S[u][r] = -INFINITY;
-            if (!there || t >= s.len || t < s.begin) x.v[4 * u + r] = 0, x.vs[u][r] = 0x7f7f7f7fu;  // whatever lies there
+            if (!there || t >= s.len || t < s.begin) vc[4 * u + r] = 0, vs[u][r] = 0x7f7f7f7fu;  // whatever lies there
           }
       }
       float top = fmaxf(fmaxf(fmaxf(S[0][0], S[0][1]), fmaxf(S[0][2], S[0][3])), fmaxf(fmaxf(S[1][0], S[1][1]), fmaxf(S[1][2], S[1][3])));
@@ -174,12 +181,12 @@ __global__ __launch_bounds__(256) void attn_step_kernel(StepArgs a) {
           bf16x8, u32x4{pk2bf(S[0][0], S[0][1]), pk2bf(S[0][2], S[0][3]), pk2bf(S[1][0], S[1][1]), pk2bf(S[1][2], S[1][3])});
       float sc[8];
 #pragma unroll
-      for (int t = 0; t < 8; ++t) sc[t] = scale_of((x.vs[t >> 2][t & 3] >> (8 * (lr >> 2))) & 0xffu);
+      for (int t = 0; t < 8; ++t) sc[t] = scale_of((vs[t >> 2][t & 3] >> (8 * (lr >> 2))) & 0xffu);
       auto channels = [&](auto sel) {  // two channels of all tokens
         constexpr int SEL = decltype(sel)::value;
         uint32_t w[8];
 #pragma unroll
-        for (int t = 0; t < 8; ++t) w[t] = pair<SEL>(x.v[t], sc[t]);
+        for (int t = 0; t < 8; ++t) w[t] = pair<SEL>(vc[t], sc[t]);
         u32x4 even, odd;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -193,7 +200,10 @@ __global__ __launch_bounds__(256) void attn_step_kernel(StepArgs a) {
       channels(std::integral_constant<int, 1>{});
       channels(std::integral_constant<int, 2>{});
       channels(std::integral_constant<int, 3>{});
-      x = next;
+      if (more) {
+        load_values(it + 1);
+        pg0 = __builtin_amdgcn_readlane(pv, 2 * ((it + 1) & 31)), pg1 = __builtin_amdgcn_readlane(pv, 2 * ((it + 1) & 31) + 1);
+      }
     }
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
@@ -235,23 +245,42 @@ __global__ __launch_bounds__(256) void attn_step_kernel(StepArgs a) {
   }
 }
 
-// Joins the splits of a sequence's rows: a block takes one head, a thread a channel.
-__global__ __launch_bounds__(128) void attn_step_join_kernel(StepArgs a) {
-  const int head = blockIdx.x % a.Hq, n = blockIdx.x / a.Hq, c = threadIdx.x;
+// Joins the splits of a sequence's rows: a block takes one head, 16 threads 8 channels each of every
+// 16th split, and the 16 sums are joined in LDS.
+__global__ __launch_bounds__(256) void attn_step_join_kernel(StepArgs a) {
+  __shared__ float so[16][HD + 4], sm[16], sl[16];
+  const int head = blockIdx.x % a.Hq, n = blockIdx.x / a.Hq, c = (threadIdx.x & 15) * 8, y = threadIdx.x >> 4;
   const Span s(a, n);
   const int used = (s.len - (s.begin & ~31) + s.per - 1) / s.per;
   for (int i = 0; i < s.run; ++i) {
     const int64_t row = (int64_t)(s.t0 + i) * a.Hq + head, at = row * a.splits;
-    float M = -1.5e38f;
-    for (int x = 0; x < used; ++x) M = fmaxf(M, a.ml[2 * (at + x)]);
-    float L = 0.f, y = 0.f;
-#pragma unroll 4
-    for (int x = 0; x < used; ++x) {
-      const float f = __builtin_amdgcn_exp2f(a.ml[2 * (at + x)] - M);
-      L = fmaf(a.ml[2 * (at + x) + 1], f, L);
-      y = fmaf(a.part[(at + x) * HD + c], f, y);
+    float m = -1.5e38f, l = 0.f, o[8] = {};
+    for (int x = y; x < used; x += 16) {
+      const float mx = a.ml[2 * (at + x)], lx = a.ml[2 * (at + x) + 1];
+      const f32x4 *src = reinterpret_cast<const f32x4 *>(a.part + (at + x) * HD + c);
+      const f32x4 u = src[0], v = src[1];
+      const float up = fmaxf(m, mx), f = __builtin_amdgcn_exp2f(m - up), e = __builtin_amdgcn_exp2f(mx - up);
+      m = up;
+      l = fmaf(l, f, lx * e);
+#pragma unroll
+      for (int z = 0; z < 4; ++z) o[z] = fmaf(o[z], f, u[z] * e), o[4 + z] = fmaf(o[4 + z], f, v[z] * e);
     }
-    a.o[row * HD + c] = f2bf(L == 0.f ? 0.f : y / L);
+#pragma unroll
+    for (int z = 0; z < 8; ++z) so[y][c + z] = o[z];
+    if (c == 0) sm[y] = m, sl[y] = l;
+    __syncthreads();
+    if (threadIdx.x < HD) {
+      const int groups = min(used, 16);
+      float M = -1.5e38f, L = 0.f, z = 0.f;
+      for (int x = 0; x < groups; ++x) M = fmaxf(M, sm[x]);
+      for (int x = 0; x < groups; ++x) {
+        const float f = __builtin_amdgcn_exp2f(sm[x] - M);
+        L = fmaf(sl[x], f, L);
+        z = fmaf(so[x][threadIdx.x], f, z);
+      }
+      a.o[row * HD + threadIdx.x] = f2bf(L == 0.f ? 0.f : z / L);
+    }
+    __syncthreads();
   }
 }
 
@@ -274,7 +303,7 @@ hipError_t launch_attn_step(const gdr_kv &c, const gdr_attn_step &p, uint16_t *o
 hipError_t launch_attn_step_join(const gdr_kv &c, const gdr_attn_step &p, uint16_t *o, void *ws, const StepPlan &plan,
                                  hipStream_t stream) {
   if (p.T == 0 || c.N == 0) return hipSuccess;
-  attn_step_join_kernel<<<dim3((uint32_t)((int64_t)c.N * p.H_q)), 128, 0, stream>>>(args(c, p, o, ws, plan));
+  attn_step_join_kernel<<<dim3((uint32_t)((int64_t)c.N * p.H_q)), 256, 0, stream>>>(args(c, p, o, ws, plan));
   return hipGetLastError();
 }
 

@@ -21,17 +21,7 @@ struct KvArgs {
   int T, H, N, n_pages, page_shift, max_pages;
 };
 
-// The sequence of token t: the last n with cu[n] <= t (cu clipped to [0, T]); -1 without one.
-__device__ __forceinline__ int sequence_of(const int32_t *cu, int N, int T, int t) {
-  int lo = 0, hi = N;  // cu[lo] <= t is open for lo == 0, cu[hi] > t for hi == N
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (min(max(cu[mid], 0), T) <= t) lo = mid;
-    else hi = mid;
-  }
-  return N > 0 && max(cu[lo], 0) <= t && t < min(cu[lo + 1], T) ? lo : -1;
-}
-
+typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
 // Eight bf16 to eight codes; the block's exponent is over the quad of lanes.
 __device__ __forceinline__ uint32_t to_codes(const u32x4 x, uint32_t &scale) {
   uint32_t m = 0;
@@ -46,20 +36,19 @@ __device__ __forceinline__ uint32_t to_codes(const u32x4 x, uint32_t &scale) {
   // 6 2^e is 1.5 2^(e+2): the largest's exponent less 2, one more if its mantissa is past 1.5
   const int e = (int)(m >> 7) - 2 + ((m & 0x7f) > 0x40);
   scale = (uint32_t)max(e, 1);
-  const float by = __uint_as_float((254u - scale) << 23);  // 2^-e; scale is 253 at most
-  const uint32_t most = scale == 253 ? 5 : 7;  // 4 2^126 is past bf16
-  uint32_t out = 0;
+  const float s = __uint_as_float(scale << 23);
+  uint32_t w[4] = {x[0], x[1], x[2], x[3]};
+  if (scale == 253) {  // 4 2^126 is past bf16: magnitudes past 3 2^126 count as that
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t h = i & 1 ? x[i >> 1] >> 16 : x[i >> 1] & 0xffffu;
-    const float a = __uint_as_float((h & 0x7fffu) << 16) * by;
-    // the code is the number of borders passed; a tie goes up where the code above is even
-    const uint32_t c = (a > 0.25f) + (a >= 0.75f) + (a > 1.25f) + (a >= 1.75f) + (a > 2.5f) + (a >= 3.5f) + (a > 5.f);
-    out |= (min(c, most) | ((h >> 12) & 8u)) << (4 * i);
+    for (int i = 0; i < 4; ++i)
+      w[i] = (w[i] & 0x80008000u) | min(w[i] & 0x7fffu, 0x7f40u) | min(w[i] & 0x7fff0000u, 0x7f400000u);
   }
-  return out;
+  uint32_t out = 0;  // the hardware's conversion of w / s: to nearest, ties to the even code
+  out = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(out, __builtin_bit_cast(bf16x2v, w[0]), s, 0);
+  out = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(out, __builtin_bit_cast(bf16x2v, w[1]), s, 1);
+  out = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(out, __builtin_bit_cast(bf16x2v, w[2]), s, 2);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(out, __builtin_bit_cast(bf16x2v, w[3]), s, 3);
 }
-typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ u32x4 from_codes(uint32_t c, uint32_t scale) {
   const float s = __uint_as_float(scale << 23);
   u32x4 r;
@@ -71,42 +60,89 @@ __device__ __forceinline__ u32x4 from_codes(uint32_t c, uint32_t scale) {
   return r;
 }
 
-template <bool STORE>
-__global__ __launch_bounds__(256) void kv_kernel(KvArgs a) {
-  const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
-  const int x = threadIdx.x & 15;
-  if (row >= (int64_t)a.T * a.H) return;  // whole quads leave together
-  const int t = (int)(row / a.H), h = (int)(row - (int64_t)t * a.H);
-  u32x4_any k8, v8;
-  u16 *kp = a.k + t * a.ks + h * HD + 8 * x, *vp = a.v + t * a.vs + h * HD + 8 * x;
-  if constexpr (STORE) {  // these do not wait for the place
-    k8 = *reinterpret_cast<const u32x4_any *>(kp);
-    v8 = *reinterpret_cast<const u32x4_any *>(vp);
-  }
-  int n = t;
-  int64_t at = 0;
+// Places of tokens t of kv heads h in the pool, in tokens; -1 where there is none (or t < 0).  The sequence
+// is the last n with cu[n] <= t (cu clipped to [0, T]); ROWS searches go side by side.
+template <int ROWS>
+__device__ __forceinline__ void places_of(const KvArgs &a, const int (&t)[ROWS], const int (&h)[ROWS], int64_t (&place)[ROWS]) {
+  int n[ROWS], end[ROWS];  // n: cu[n] <= t but for n == 0; cu[end] > t but for end == N
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) n[r] = a.cu ? 0 : max(t[r], 0), end[r] = a.N, place[r] = t[r] < 0 ? -1 : 0;
   if (a.cu) {
-    n = sequence_of(a.cu, a.N, a.T, t);
-    if (n < 0) return;
-    at = t - max(a.cu[n], 0);
+    for (int left = a.N; left > 1; left = (left + 1) >> 1)
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        const int mid = (n[r] + end[r]) >> 1;
+        if (min(max(a.cu[mid], 0), a.T) <= t[r]) n[r] = mid;
+        else end[r] = max(mid, n[r] + 1);
+      }
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const int from = max(a.cu[n[r]], 0);
+      if (t[r] < from || t[r] >= min(a.cu[n[r] + 1], a.T)) place[r] = -1;
+      else place[r] = t[r] - from;
+    }
   }
-  if (a.start) at += a.start[n];
-  const int64_t col = at >> a.page_shift;
-  if (at < 0 || col >= a.max_pages) return;
-  const int page = a.table[(int64_t)n * a.max_pages + col];
-  if (page < 0 || page >= a.n_pages) return;
-  const int64_t place = ((((int64_t)page * a.H + h) << a.page_shift) + (at & ((1 << a.page_shift) - 1)));
-  uint32_t *kc = reinterpret_cast<uint32_t *>(a.kc + place * 64) + x, *vc = reinterpret_cast<uint32_t *>(a.vc + place * 64) + x;
-  uint8_t *ksc = a.ksc + place * 4 + (x >> 2), *vsc = a.vsc + place * 4 + (x >> 2);
+  int page[ROWS];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    bool there = place[r] >= 0;
+    if (a.start) place[r] += a.start[n[r]];
+    there = there && place[r] >= 0 && place[r] >> a.page_shift < a.max_pages;
+    if (!there) place[r] = -1;
+    page[r] = a.table[(int64_t)n[r] * a.max_pages + (there ? place[r] >> a.page_shift : 0)];
+  }
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    if (place[r] < 0 || page[r] < 0 || page[r] >= a.n_pages) place[r] = -1;
+    else place[r] = (((int64_t)page[r] * a.H + h[r]) << a.page_shift) + (place[r] & ((1 << a.page_shift) - 1));
+  }
+}
+
+// A thread takes ROWS rows, 16 apart, so that their places' chains of loads run side by side.  Reading back, whose
+// bytes wait for the place, takes 4; storing, which reads its rows meanwhile, one.
+template <bool STORE, int ROWS>
+__global__ __launch_bounds__(256) void kv_kernel(KvArgs a) {
+  const int x = threadIdx.x & 15;
+  const int64_t row0 = (int64_t)blockIdx.x * (16 * ROWS) + (threadIdx.x >> 4), rows = (int64_t)a.T * a.H;
+  u32x4_any k8[ROWS], v8[ROWS];
+  u16 *kp[ROWS], *vp[ROWS];
+  int64_t place[ROWS];
+  int t[ROWS], h[ROWS];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    const int64_t row = row0 + 16 * r;
+    t[r] = row < rows ? (int)(row / a.H) : -1, h[r] = (int)(row - (int64_t)t[r] * a.H);
+    if (row >= rows) continue;  // whole quads go together
+    kp[r] = a.k + t[r] * a.ks + h[r] * HD + 8 * x, vp[r] = a.v + t[r] * a.vs + h[r] * HD + 8 * x;
+    if constexpr (STORE) {
+      k8[r] = *reinterpret_cast<const u32x4_any *>(kp[r]);
+      v8[r] = *reinterpret_cast<const u32x4_any *>(vp[r]);
+    }
+  }
+  places_of(a, t, h, place);
   if constexpr (STORE) {
-    uint32_t s, u;
-    *kc = to_codes(k8, s);
-    *vc = to_codes(v8, u);
-    if ((x & 3) == 0) *ksc = (uint8_t)s, *vsc = (uint8_t)u;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      if (place[r] < 0) continue;
+      uint32_t s, u;
+      reinterpret_cast<uint32_t *>(a.kc + place[r] * 64)[x] = to_codes(k8[r], s);
+      reinterpret_cast<uint32_t *>(a.vc + place[r] * 64)[x] = to_codes(v8[r], u);
+      if ((x & 3) == 0) a.ksc[place[r] * 4 + (x >> 2)] = (uint8_t)s, a.vsc[place[r] * 4 + (x >> 2)] = (uint8_t)u;
+    }
   } else {
-    const uint32_t kw = *kc, vw = *vc, s = *ksc, u = *vsc;
-    *reinterpret_cast<u32x4_any *>(kp) = from_codes(kw, s);
-    *reinterpret_cast<u32x4_any *>(vp) = from_codes(vw, u);
+    uint32_t kw[ROWS], vw[ROWS], s[ROWS], u[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const int64_t at = max(place[r], (int64_t)0);  // a token without a place reads the first one's
+      kw[r] = reinterpret_cast<const uint32_t *>(a.kc + at * 64)[x], vw[r] = reinterpret_cast<const uint32_t *>(a.vc + at * 64)[x];
+      s[r] = a.ksc[at * 4 + (x >> 2)], u[r] = a.vsc[at * 4 + (x >> 2)];
+    }
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      if (place[r] < 0) continue;
+      *reinterpret_cast<u32x4_any *>(kp[r]) = from_codes(kw[r], s[r]);
+      *reinterpret_cast<u32x4_any *>(vp[r]) = from_codes(vw[r], u[r]);
+    }
   }
 }
 
@@ -117,9 +153,9 @@ hipError_t launch_kv(const gdr_kv &p, bool store, int32_t T, const int32_t *cu, 
   if (T == 0 || p.N == 0 || p.max_pages == 0 || p.n_pages == 0) return hipSuccess;
   const KvArgs a{p.k_codes, p.v_codes, p.k_scale, p.v_scale, p.page_table, cu, start, k, v, k_stride, v_stride, T, p.H_kv, p.N,
                  p.n_pages, __builtin_ctz((unsigned)p.page), p.max_pages};
-  const dim3 grid((uint32_t)(((int64_t)T * p.H_kv + 15) / 16));
-  if (store) kv_kernel<true><<<grid, 256, 0, stream>>>(a);
-  else kv_kernel<false><<<grid, 256, 0, stream>>>(a);
+  const int64_t rows = (int64_t)T * p.H_kv;
+  if (store) kv_kernel<true, 1><<<dim3((uint32_t)((rows + 15) / 16)), 256, 0, stream>>>(a);
+  else kv_kernel<false, 4><<<dim3((uint32_t)((rows + 63) / 64)), 256, 0, stream>>>(a);
   return hipGetLastError();
 }
 
