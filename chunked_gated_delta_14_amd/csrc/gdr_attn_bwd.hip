@@ -87,6 +87,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(BwdArgs a) {
   const float given = a.lse[stat];
   const float lse = given == -INFINITY ? NO_KEYS : given * LOG2E;
   if (live && h == 0 && x.part == 0) a.lse2[stat] = lse, a.delta[stat] = delta;
+  settle_loads();
 
   int buf = 0;
   for (int t = begin; t < end; t += KT, buf ^= 1) {
@@ -124,13 +125,6 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(BwdArgs a) {
   }
   if (x.parts == 1) store_row(a.dq + (int64_t)(e.row0 + row) * a.dqs + head * HD, D, a.scale, h, live);
   else if (live) store_floats(a.pq + x.part * a.part_size + ((int64_t)(e.row0 + row) * a.Hq + head) * HD, D, h);
-}
-
-// A lane's value as one that the compiler cannot keep from before: what follows from it is formed again
-// here, for one or two instructions, where kept in a register it would be spilled.
-__device__ __forceinline__ int afresh(int x) {
-  asm volatile("" : "+v"(x));
-  return x;
 }
 
 // Eight wavefronts, 32 keys each, share the tiles in LDS; the keys' sums take half of a wavefront's
@@ -190,6 +184,7 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_kernel(BwdArgs a) {
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk) K[kk] = ld8(kp + 16 * kk);
   }
+  settle_loads();
   // rows that see this wavefront's first and last key, first ones
   const int x0 = f0 + key0, x1 = f0 + min(key0 + 31, e.rows - 1);
   for (; it < last_it; ++it, buf ^= 1) {

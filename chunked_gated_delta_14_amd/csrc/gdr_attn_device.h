@@ -85,6 +85,15 @@ __device__ __forceinline__ bf16x8 col_frag(uint32_t base, int step, int dt) {
   const uint2 u = __builtin_bit_cast(uint2, x), v = __builtin_bit_cast(uint2, y);
   return __builtin_bit_cast(bf16x8, u32x4{u.x, u.y, v.x, v.y});
 }
+// Waits for every load, in a form that the compiler counts too: behind it, a loop holds no waits for
+// registers loaded before it, which would wait for the loop's copies as well.
+__device__ __forceinline__ void settle_loads() { __builtin_amdgcn_s_waitcnt(0x0f70); }
+// A value as one that the compiler cannot keep from before: what follows from it is formed again here, for
+// an instruction or two, where kept in a register it would be spilled.
+__device__ __forceinline__ int afresh(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
 // Registers 8 s .. 8 s + 7 of a D tile as a B operand.
 __device__ __forceinline__ bf16x8 acc_frag(const f32x16 &x, int s) {
   return __builtin_bit_cast(bf16x8, u32x4{pk2bf(x[8 * s], x[8 * s + 1]), pk2bf(x[8 * s + 2], x[8 * s + 3]),

@@ -28,6 +28,39 @@ struct FwdArgs {
   float scale;
 };
 
+// Whether a tile holds an infinity or NaN: the largest magnitude's bits, over all its values.
+__device__ __forceinline__ bool any_not_finite(uint32_t tile, int lane) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  u16x2 m = {0, 0};
+#pragma unroll
+  for (int i = 0; i < TILE_BYTES / 1024; ++i) {
+    const u32x4 w = *(const __attribute__((address_space(3))) u32x4 *)(tile + i * 1024 + lane * 16);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, w[j] & 0x7fff7fffu));
+  }
+  return __any(max(m[0], m[1]) >= 0x7f80);
+}
+
+// For a tile with infinities or NaN, some of which not every row sees (0 times one of them would reach
+// the rows it is hidden from), V^T P^T is formed in three goes: the finite values, with zeros in the
+// others' places; then 2^127 for every +infinity or NaN, and -2^127 for every -infinity or NaN,
+// times 2^127 where a row sees the key, which adds an infinity where it does and 0 where it does not.
+__device__ __forceinline__ bf16x8 values_of_go(bf16x8 v, int go) {
+  u32x4 w = __builtin_bit_cast(u32x4, v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t r = 0;
+#pragma unroll
+    for (int x = 0; x < 32; x += 16) {
+      const uint32_t b = (w[i] >> x) & 0xffffu, mag = b & 0x7fffu;
+      if (go == 0) r |= mag < 0x7f80u ? b << x : 0u;
+      else if (mag > 0x7f80u || b == (go == 1 ? 0x7f80u : 0xff80u)) r |= (go == 1 ? 0x7f00u : 0xff00u) << x;
+    }
+    w[i] = r;
+  }
+  return __builtin_bit_cast(bf16x8, w);
+}
+
 __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdArgs a) {
   __shared__ __align__(16) unsigned char lds[4 * TILE_BYTES];  // K, V; twice
   const int lane = threadIdx.x & 63, lr = lane & 31, h = lane >> 5;
@@ -73,21 +106,25 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdArgs a) {
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk) Q[kk] = ld8(qp + 16 * kk);
   }
-  int buf = 0;
-  for (int t = begin; t < end; t += KT, buf ^= 1) {
+  settle_loads();
+  // A tile's copies are there, and everyone is through with the other buffer, which the next tile's go to.
+  auto arrive = [&](int t, int buf) {
     drain_vmem();
-    lds_barrier();  // tile t is there, and everyone is through with the other buffer
+    lds_barrier();
     if (t + KT < end) copy(t + KT, buf ^ 1);
-    const uint32_t kt = row_base(lds0 + buf * 2 * TILE_BYTES, lane), vt = col_base(lds0 + (buf * 2 + 1) * TILE_BYTES, lane);
-    // a wavefront without rows, or none of whose rows sees a key of this tile
-    if ((a.causal && t > p1) || (a.window && t + KT <= p0 - a.window + 1) || 32 * wave >= e.rows) continue;
-    f32x16 S[2] = {zero16(), zero16()};
+  };
+  // a wavefront without rows, or none of whose rows sees a key of this tile
+  auto idle = [&](int t) { return (a.causal && t > p1) || (a.window && t + KT <= p0 - a.window + 1) || 32 * wave >= e.rows; };
+  auto is_masked = [&](int t) { return t + KT > Lk || (a.causal && t + KT - 1 > p0) || (a.window && t <= p1 - a.window); };
+  // S^T of a tile, hidden scores at -infinity, and the row's largest over both of its lanes.
+  auto scores = [&](f32x16 (&S)[2], int t, int buf) {
+    const uint32_t kt = row_base(lds0 + buf * 2 * TILE_BYTES, lane);
+    S[0] = zero16(), S[1] = zero16();
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
       for (int half = 0; half < 2; ++half) S[half] = mfma32(row_frag(kt, half, kk), Q[kk], S[half]);
-    const bool masked = t + KT > Lk || (a.causal && t + KT - 1 > p0) || (a.window && t <= p1 - a.window);
-    if (masked) {
+    if (is_masked(t)) {
 #pragma unroll
       for (int half = 0; half < 2; ++half)
 #pragma unroll
@@ -99,7 +136,30 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdArgs a) {
     float top = S[0][0];
 #pragma unroll
     for (int i = 0; i < 16; ++i) top = fmaxf(fmaxf(top, S[0][i]), S[1][i]);
-    top = fmaxf(top, other_half(top)) * c;
+    return fmaxf(top, other_half(top)) * c;
+  };
+  auto probabilities = [&](f32x16 (&S)[2]) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float x = __builtin_amdgcn_exp2f(fmaf(S[half][i], c, -m));
+        S[half][i] = x;
+        l += x;
+      }
+  };
+  // the loop, until a masked tile holds a value that is not finite
+  int t = begin, buf = 0;
+  bool careful = false;
+  for (; t < end; t += KT, buf ^= 1) {
+    arrive(t, buf);
+    if (idle(t)) continue;
+    const uint32_t v0 = lds0 + (buf * 2 + 1) * TILE_BYTES;
+    careful = is_masked(t) && any_not_finite(v0, lane);
+    if (careful) break;
+    const uint32_t vt = col_base(v0, lane);
+    f32x16 S[2];
+    const float top = scores(S, t, buf);
     if (__any(top > m + 8.f)) {
       const float to = fmaxf(top, m), f = __builtin_amdgcn_exp2f(m - to);
       m = to;
@@ -109,20 +169,56 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdArgs a) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) O[dt][i] *= f;
     }
-#pragma unroll
-    for (int half = 0; half < 2; ++half)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float x = __builtin_amdgcn_exp2f(fmaf(S[half][i], c, -m));
-        S[half][i] = x;
-        l += x;
-      }
+    probabilities(S);
 #pragma unroll
     for (int step = 0; step < 4; ++step) {
       const bf16x8 P = acc_frag(S[step >> 1], step & 1);
 #pragma unroll
       for (int dt = 0; dt < 4; ++dt) O[dt] = mfma32(col_frag(vt, step, dt), P, O[dt]);
     }
+  }
+  if (careful) {  // from there on: the same with care, its sums in memory, so that it takes no registers from the loop above
+    f32x16 X[4];
+#pragma unroll
+    for (int dt = 0; dt < 4; ++dt) X[dt] = O[dt];
+    for (bool first = true; t < end; t += KT, buf ^= 1, first = false) {
+      if (!first) arrive(t, buf);
+      if (idle(t)) continue;
+      const uint32_t vt = col_base(lds0 + (buf * 2 + 1) * TILE_BYTES, lane);
+      f32x16 S[2];
+      const float top = scores(S, t, buf), to = __any(top > m + 8.f) ? fmaxf(top, m) : m, f = __builtin_amdgcn_exp2f(m - to);
+      m = to;
+      l *= f;
+      probabilities(S);
+      const int goes = is_masked(t) ? 3 : 0;  // 0: every row sees every key
+#pragma unroll 1
+      for (int go = 0; go < max(goes, 1); ++go) {
+        bf16x8 P[4];
+#pragma unroll
+        for (int step = 0; step < 4; ++step) P[step] = acc_frag(S[step >> 1], step & 1);
+#pragma unroll 1
+        for (int dt = 0; dt < 4; ++dt) {
+          f32x16 x = X[dt];
+          if (go == 0) x *= f;
+#pragma unroll
+          for (int step = 0; step < 4; ++step) {
+            const bf16x8 v = col_frag(vt, step, dt);
+            x = mfma32(goes ? values_of_go(v, go) : v, P[step], x);
+          }
+          X[dt] = x;
+        }
+        const int j0 = afresh(t + 4 * h);
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int j = j0 + 32 * half + 8 * (i >> 2) + (i & 3);
+            S[half][i] = j > hi || j < lo ? 0.f : 0x1p127f;
+          }
+      }
+    }
+#pragma unroll
+    for (int dt = 0; dt < 4; ++dt) O[dt] = X[dt];
   }
   l += other_half(l);
   const bool live = 32 * wave + lr < e.rows;

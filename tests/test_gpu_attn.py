@@ -135,6 +135,43 @@ def test_attention(case):
         assert x.equal(y)
 
 
+@pytest.mark.parametrize("docs,window,at", [([300, 40], 0, 130), ([300, 40], 0, 63), ([200, 90], 70, 64), ([1, 1, 129], 0, 1), ([700], 0, 699)])
+def test_hidden_values_stay_hidden(docs, window, at):
+    """An infinity or NaN in k or v reaches the rows that see it, in the channels that hold it, and no others."""
+    cu, inf, nan = cu_of(docs), float("inf"), float("nan")
+    g = gen(at)
+    q, k, v = heads(g, cu[-1], 2), heads(g, cu[-1], 1), heads(g, cu[-1], 1)
+    p = gdr.AttnPlan(cu, window=window)
+    doc = next(n for n in range(len(docs)) if cu[n] <= at < cu[n + 1])
+    sees = torch.zeros(cu[-1], dtype=torch.bool, device="cuda")
+    sees[at: min(cu[doc + 1], at + window) if window else cu[doc + 1]] = True
+
+    def forward(k, v):
+        o, lse = torch.empty_like(q), torch.empty(2, cu[-1], device="cuda")
+        gdr.attn_fwd(gdr.AttnProblem(q, k, v, p), o, lse)
+        return o, lse
+
+    o0, lse0 = forward(k, v)
+    poison = {3: inf, 40: -inf, 77: nan, 127: inf}
+    v1 = v.clone()
+    for c, x in poison.items():
+        v1[at, 0, c] = x
+    o, lse = forward(k, v1)
+    assert lse.equal(lse0) and o[~sees].equal(o0[~sees])
+    for c in range(128):
+        if c not in poison:
+            assert torch.isfinite(o[sees, :, c]).all()
+        elif poison[c] != poison[c]:
+            assert torch.isnan(o[sees, :, c]).all()
+        else:
+            assert (o[sees, :, c] == poison[c]).all()
+    k1 = k.clone()
+    k1[at, 0, 5] = nan
+    o, lse = forward(k1, v)
+    assert o[~sees].equal(o0[~sees]) and lse[:, ~sees].equal(lse0[:, ~sees])
+    assert torch.isnan(o[sees]).all() and torch.isnan(lse[:, sees]).all()
+
+
 # ---- the cache in 4 bits ----
 
 
