@@ -91,8 +91,8 @@ inline AttnShare attn_k_share(const gdr_attn &p) {
 }
 // The workspace.  Forward: the parts' rows [part][T_q][H_q][128], then their maxima and sums
 // [part][H_q][T_q][2].  Backward: lse and delta of every row and head as the
-// matrix kernels take them, [H_q][T_q] each; the parts of dq [part][T_q][H_q][128] or, later and in the
-// same place, those of dk and of dv [part][T_k][H_kv][128].
+// matrix kernels take them, [H_q][T_q] each; the parts of dq [part][T_q][H_q][128], of dk and of dv
+// [part][T_k][H_kv][128].
 struct AttnWorkspace {
   int64_t stats, q_part, k_part, fwd, bwd;  // bytes: a row of stats, a part's, the whole
   AttnShare q, k;
@@ -106,18 +106,17 @@ inline AttnWorkspace attn_workspace(const gdr_attn &p) {
   w.q_part = w.q.parts > 1 ? up((int64_t)p.T_q * p.H_q * 128 * 4) : 0;
   w.k_part = w.k.parts > 1 ? up((int64_t)p.T_k * p.H_kv * 128 * 4) : 0;
   w.fwd = w.q.parts > 1 ? w.q.parts * (w.q_part + up((int64_t)p.T_q * p.H_q * 8)) : 0;
-  w.bwd = 2 * w.stats + std::max(w.q.parts * w.q_part, 2 * w.k.parts * w.k_part);
+  w.bwd = 2 * w.stats + w.q.parts * w.q_part + 2 * w.k.parts * w.k_part;
   return w;
 }
 hipError_t launch_attn_fwd(const gdr_attn &p, uint16_t *o, float *lse, void *ws, hipStream_t stream);
 hipError_t launch_attn_fwd_join(const gdr_attn &p, uint16_t *o, float *lse, void *ws, hipStream_t stream);
 hipError_t launch_attn_dq(const gdr_attn &p, const uint16_t *o, const float *lse, const uint16_t *dout, uint16_t *dq,
                           int64_t dq_stride, void *ws, hipStream_t stream);
-hipError_t launch_attn_dq_join(const gdr_attn &p, uint16_t *dq, int64_t dq_stride, void *ws, hipStream_t stream);
 hipError_t launch_attn_dkv(const gdr_attn &p, const uint16_t *dout, uint16_t *dk, int64_t dk_stride, uint16_t *dv,
                            int64_t dv_stride, void *ws, hipStream_t stream);
-hipError_t launch_attn_dkv_join(const gdr_attn &p, uint16_t *dk, int64_t dk_stride, uint16_t *dv, int64_t dv_stride, void *ws,
-                                hipStream_t stream);
+hipError_t launch_attn_bwd_join(const gdr_attn &p, uint16_t *dq, int64_t dq_stride, uint16_t *dk, int64_t dk_stride, uint16_t *dv,
+                                int64_t dv_stride, void *ws, hipStream_t stream);
 
 // ---- the cache and the attention over it ----
 

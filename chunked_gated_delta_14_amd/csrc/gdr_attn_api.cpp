@@ -119,7 +119,7 @@ int32_t check_attn(const gdr_attn *p) {
   const gdr::AttnShare q = gdr::attn_q_share(*p), k = gdr::attn_k_share(*p);
   const int64_t q_blocks = std::max(q.blocks, q.parts > 1 ? (int64_t)plan.n_q_tiles * 8 : 0);
   const int64_t k_blocks = std::max(k.blocks, k.parts > 1 ? (int64_t)plan.n_k_tiles * 16 : 0);
-  if (!grid_ok(q_blocks * p->H_q, 256) || !grid_ok(k_blocks * p->H_kv, 512)) return unsupported("too many rows and heads for one launch");
+  if (!grid_ok(q_blocks * p->H_q + k_blocks * p->H_kv, 512)) return unsupported("too many rows and heads for one launch");
   return GDR_OK;
 }
 
@@ -160,14 +160,12 @@ int32_t attn_bwd(const gdr_attn *p, const uint16_t *o, const float *lse, const u
   if ((rc = launch(gdr::TK_ATTN_DQ, stream, "query gradient launch",
                    [&](hipStream_t s) { return gdr::launch_attn_dq(*p, o, lse, dout, dq, dqs, ws, s); })))
     return rc;
-  if (w.q.parts > 1 && (rc = launch(gdr::TK_ATTN_JOIN, stream, "query gradient sum launch",
-                                    [&](hipStream_t s) { return gdr::launch_attn_dq_join(*p, dq, dqs, ws, s); })))
-    return rc;
   if ((rc = launch(gdr::TK_ATTN_DKV, stream, "key gradient launch",
                    [&](hipStream_t s) { return gdr::launch_attn_dkv(*p, dout, dk, dks, dv, dvs, ws, s); })))
     return rc;
-  if (w.k.parts > 1 && (rc = launch(gdr::TK_ATTN_JOIN, stream, "key gradient sum launch",
-                                    [&](hipStream_t s) { return gdr::launch_attn_dkv_join(*p, dk, dks, dv, dvs, ws, s); })))
+  if ((w.q.parts > 1 || w.k.parts > 1) && (rc = launch(gdr::TK_ATTN_JOIN, stream, "gradient sum launch", [&](hipStream_t s) {
+                                             return gdr::launch_attn_bwd_join(*p, dq, dqs, dk, dks, dv, dvs, ws, s);
+                                           })))
     return rc;
   return host_status(GDR_OK, "");
 }

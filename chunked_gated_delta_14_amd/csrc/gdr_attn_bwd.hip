@@ -258,31 +258,36 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_kernel(BwdArgs a) {
   }
 }
 
-// Adds the parts of a tile's rows in order: 16 threads a row, 8 channels each.  KEYS: dk and dv
-// of a tile of keys, otherwise dq of a tile of query rows.
-template <bool KEYS>
-__global__ __launch_bounds__(256) void attn_bwd_join_kernel(BwdArgs a) {
-  const int rows = (KEYS ? ATT_KTILE : ATT_QTILE) / 16;  // blocks a tile
-  const int heads = KEYS ? a.Hkv : a.Hq;
-  const int64_t b = blockIdx.x / rows;
-  const int head = (int)(b % heads);
+// Adds the parts of a tile's rows in order: 16 threads a row, 8 channels each.  Blocks of both
+// sides: dq of the query tiles (`qblocks` blocks, if they have parts), then dk and dv of the key tiles.
+struct JoinArgs {
+  BwdArgs q, k;
+  int64_t qblocks;
+};
+__device__ __forceinline__ void join_row(const float *src, int64_t part_size, int parts, float f, u16 *to) {
+  f32x4 u = zero4(), v = zero4();
+  for (int x = 0; x < parts; ++x) {
+    const f32x4 *p = reinterpret_cast<const f32x4 *>(src + x * part_size);
+    u += p[0], v += p[1];
+  }
+  *reinterpret_cast<u32x4 *>(to) =
+      u32x4{pk2bf(u[0] * f, u[1] * f), pk2bf(u[2] * f, u[3] * f), pk2bf(v[0] * f, v[1] * f), pk2bf(v[2] * f, v[3] * f)};
+}
+__global__ __launch_bounds__(256) void attn_bwd_join_kernel(JoinArgs j) {
+  const bool keys = blockIdx.x >= j.qblocks;
+  const BwdArgs &a = keys ? j.k : j.q;
+  const int per = (keys ? ATT_KTILE : ATT_QTILE) / 16, heads = keys ? a.Hkv : a.Hq;  // blocks a tile
+  const int64_t x = blockIdx.x - (keys ? j.qblocks : 0), b = x / per;
+  const int head = (int)(b % heads), r = (int)(x % per) * 16 + (threadIdx.x >> 4), c = (threadIdx.x & 15) * 8;
   const TileEntry e(a.tiles, (int)(b / heads));
   const int parts = e.parts(a.level);
-  const int r = (blockIdx.x % rows) * 16 + (threadIdx.x >> 4), c = (threadIdx.x & 15) * 8;
   if (parts == 1 || r >= e.rows) return;
   const int64_t row = e.row0 + r, at = (row * heads + head) * HD + c;
-#pragma unroll
-  for (int side = 0; side < (KEYS ? 2 : 1); ++side) {
-    const float *src = (KEYS ? (side ? a.pv : a.pk) : a.pq) + at;
-    const float f = side ? 1.f : a.scale;
-    f32x4 u = zero4(), v = zero4();
-    for (int x = 0; x < parts; ++x) {
-      const f32x4 *p = reinterpret_cast<const f32x4 *>(src + x * a.part_size);
-      u += p[0], v += p[1];
-    }
-    u16 *to = KEYS ? (side ? a.dv + row * a.dvs : a.dk + row * a.dks) : a.dq + row * a.dqs;
-    *reinterpret_cast<u32x4 *>(to + head * HD + c) =
-        u32x4{pk2bf(u[0] * f, u[1] * f), pk2bf(u[2] * f, u[3] * f), pk2bf(v[0] * f, v[1] * f), pk2bf(v[2] * f, v[3] * f)};
+  if (keys) {
+    join_row(a.pk + at, a.part_size, parts, a.scale, a.dk + row * a.dks + head * HD + c);
+    join_row(a.pv + at, a.part_size, parts, 1.f, a.dv + row * a.dvs + head * HD + c);
+  } else {
+    join_row(a.pq + at, a.part_size, parts, a.scale, a.dq + row * a.dqs + head * HD + c);
   }
 }
 
@@ -294,7 +299,8 @@ BwdArgs args(const gdr_attn &p, bool keys, void *ws) {
   a.tiles = p.tile_table + (keys ? (int64_t)p.plan.n_q_tiles * ATT_ENTRY : 0);
   a.lse2 = reinterpret_cast<float *>(base);
   a.delta = reinterpret_cast<float *>(base + w.stats);
-  a.pq = a.pk = reinterpret_cast<float *>(base + 2 * w.stats);
+  a.pq = reinterpret_cast<float *>(base + 2 * w.stats);
+  a.pk = a.pq + w.q.parts * (w.q_part / 4);
   a.pv = a.pk + w.k.parts * (w.k_part / 4);
   a.part_size = (keys ? w.k_part : w.q_part) / 4;
   const AttnShare &share = keys ? w.k : w.q;
@@ -316,13 +322,6 @@ hipError_t launch_attn_dq(const gdr_attn &p, const uint16_t *o, const float *lse
   attn_dq_kernel<<<dim3((uint32_t)(attn_q_share(p).blocks * p.H_q)), 256, 0, stream>>>(a);
   return hipGetLastError();
 }
-hipError_t launch_attn_dq_join(const gdr_attn &p, uint16_t *dq, int64_t dq_stride, void *ws, hipStream_t stream) {
-  if (p.plan.n_q_tiles == 0) return hipSuccess;
-  BwdArgs a = args(p, false, ws);
-  a.dq = dq, a.dqs = dq_stride;
-  attn_bwd_join_kernel<false><<<dim3((uint32_t)((int64_t)p.plan.n_q_tiles * p.H_q * (ATT_QTILE / 16))), 256, 0, stream>>>(a);
-  return hipGetLastError();
-}
 
 hipError_t launch_attn_dkv(const gdr_attn &p, const uint16_t *dout, uint16_t *dk, int64_t dk_stride, uint16_t *dv,
                            int64_t dv_stride, void *ws, hipStream_t stream) {
@@ -332,12 +331,15 @@ hipError_t launch_attn_dkv(const gdr_attn &p, const uint16_t *dout, uint16_t *dk
   attn_dkv_kernel<<<dim3((uint32_t)(attn_k_share(p).blocks * p.H_kv)), 512, 0, stream>>>(a);
   return hipGetLastError();
 }
-hipError_t launch_attn_dkv_join(const gdr_attn &p, uint16_t *dk, int64_t dk_stride, uint16_t *dv, int64_t dv_stride, void *ws,
-                                hipStream_t stream) {
-  if (p.plan.n_k_tiles == 0) return hipSuccess;
-  BwdArgs a = args(p, true, ws);
-  a.dk = dk, a.dv = dv, a.dks = dk_stride, a.dvs = dv_stride;
-  attn_bwd_join_kernel<true><<<dim3((uint32_t)((int64_t)p.plan.n_k_tiles * p.H_kv * (ATT_KTILE / 16))), 256, 0, stream>>>(a);
+hipError_t launch_attn_bwd_join(const gdr_attn &p, uint16_t *dq, int64_t dq_stride, uint16_t *dk, int64_t dk_stride, uint16_t *dv,
+                                int64_t dv_stride, void *ws, hipStream_t stream) {
+  JoinArgs j{args(p, false, ws), args(p, true, ws), 0};
+  j.q.dq = dq, j.q.dqs = dq_stride;
+  j.k.dk = dk, j.k.dv = dv, j.k.dks = dk_stride, j.k.dvs = dv_stride;
+  j.qblocks = attn_q_share(p).parts > 1 ? (int64_t)p.plan.n_q_tiles * p.H_q * (ATT_QTILE / 16) : 0;
+  const int64_t kblocks = attn_k_share(p).parts > 1 ? (int64_t)p.plan.n_k_tiles * p.H_kv * (ATT_KTILE / 16) : 0;
+  if (j.qblocks + kblocks == 0) return hipSuccess;
+  attn_bwd_join_kernel<<<dim3((uint32_t)(j.qblocks + kblocks)), 256, 0, stream>>>(j);
   return hipGetLastError();
 }
 

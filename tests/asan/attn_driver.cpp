@@ -25,9 +25,8 @@ hipError_t launch_rope(const gdr_rope &, bool, const void *, int64_t, const void
 hipError_t launch_attn_fwd(const gdr_attn &, uint16_t *, float *, void *, hipStream_t) { return count(); }
 hipError_t launch_attn_fwd_join(const gdr_attn &, uint16_t *, float *, void *, hipStream_t) { return count(); }
 hipError_t launch_attn_dq(const gdr_attn &, const uint16_t *, const float *, const uint16_t *, uint16_t *, int64_t, void *, hipStream_t) { return count(); }
-hipError_t launch_attn_dq_join(const gdr_attn &, uint16_t *, int64_t, void *, hipStream_t) { return count(); }
 hipError_t launch_attn_dkv(const gdr_attn &, const uint16_t *, uint16_t *, int64_t, uint16_t *, int64_t, void *, hipStream_t) { return count(); }
-hipError_t launch_attn_dkv_join(const gdr_attn &, uint16_t *, int64_t, uint16_t *, int64_t, void *, hipStream_t) { return count(); }
+hipError_t launch_attn_bwd_join(const gdr_attn &, uint16_t *, int64_t, uint16_t *, int64_t, uint16_t *, int64_t, void *, hipStream_t) { return count(); }
 hipError_t launch_kv(const gdr_kv &, bool, int32_t, const int32_t *, const int32_t *, uint16_t *, int64_t, uint16_t *, int64_t, hipStream_t) { return count(); }
 hipError_t launch_attn_step(const gdr_kv &, const gdr_attn_step &, uint16_t *, void *, const StepPlan &, hipStream_t) { return count(); }
 hipError_t launch_attn_step_join(const gdr_kv &, const gdr_attn_step &, uint16_t *, void *, const StepPlan &, hipStream_t) { return count(); }
