@@ -188,7 +188,7 @@ class AttnProblem(_Base):
     q: bf16 [T_q, H_q, 128]; k, v: bf16 [T_k, H_kv, 128], rows 16-byte aligned at any stride; plan: the batch's AttnPlan.
     The problem holds the forward's workspace (none unless few rows have many keys).  What it holds follows from the problem's
     inputs alone, so calls that overlap without those changing write the same there; overlapping calls on changing
-    inputs would race on the inputs already."""
+    inputs would race on the inputs already.  Keep the problem until its calls are done."""
 
     def __init__(self, q, k, v, plan, scale=None):
         import torch

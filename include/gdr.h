@@ -464,7 +464,7 @@ int32_t gdr_rope_bwd(const gdr_rope *p, const void *dq_out, int64_t dq_out_strid
  * Document n holds queries cu_q[n] .. cu_q[n+1] - 1 and keys cu_k[n] .. cu_k[n+1] - 1;
  * with Lq and Lk of them, row i stands at p = i + Lk - Lq among the keys and sees key j if
  *     j <= p (causal),   j > p - window (window > 0, causal only),
- * every key of the document without `causal`.  Query head h reads kv head h / (H_q / H_kv).
+ * every key of the document without `causal`.  0 < scale <= 2^64.  Query head h reads kv head h / (H_q / H_kv).
  *     o_i = sum_j P_ij v_j,   P_ij = exp(scale q_i k_j - lse_i),   lse_i = log sum_j exp(scale q_i k_j)
  * A row that sees no key has o = 0 and lse = -inf, and its gradients are zero.
  * Probabilities and their gradients are rounded to bf16 for the matrix products, which

@@ -176,7 +176,7 @@ def bwd(L, r, o=PTR, lse=PTR, dout=PTR, dq=OUT, dqs=512, dk=OUT2, dks=256, dv=OU
 
 @pytest.mark.parametrize("kw,code,word", [
     (dict(T_q=-1), 1, "T_q, T_k"), (dict(N=-1), 1, "N must"), (dict(Hq=0), 1, "head counts"), (dict(Hq=3), 2, "multiple"), (dict(D=64), 2, "D = 128"),
-    (dict(window=-1), 1, "window"), (dict(window=4, causal=0), 2, "causal"), (dict(scale=0.0), 1, "scale"), (dict(scale=float("inf")), 1, "scale"),
+    (dict(window=-1), 1, "window"), (dict(window=4, causal=0), 2, "causal"), (dict(scale=0.0), 1, "scale"), (dict(scale=float("inf")), 1, "scale"), (dict(scale=1e30), 1, "scale"),
     (dict(scale=-1.0), 1, "scale"), (dict(scale=float("nan")), 1, "scale"), (dict(q=None), 1, "q must"), (dict(v=None), 1, "k and v"),
     (dict(tile_table=None), 1, "tile_table"), (dict(tile_table=PTR + 2), 1, "aligned"), (dict(q=PTR + 8), 1, "16-byte"), (dict(q_stride=516), 1, "16-byte"),
     (dict(k_stride=248), 1, "16-byte"), (dict(v_stride=1 << 24), 1, "16-byte"), (dict(T_k=1), 1, "plan"), (dict(T_q=600), 1, "plan"),
