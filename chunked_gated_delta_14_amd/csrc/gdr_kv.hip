@@ -7,7 +7,7 @@
 // Bound by the bytes, 256 + 68 a token, head and side.  16 lanes take a row of 128 channels,
 // 8 each: 16 bytes of bf16 and 4 of codes, so both sides' accesses are whole lines; four
 // lanes share a block, whose maximum they find by two lane swaps.  32674 tokens of 4 heads: stored in
-// KVS us, KVSR TB/s, read back in 17 us, 5.0 TB/s.  (Codes by comparing with every border instead of the hardware's
+// 20 us, 4.2 TB/s, read back in 17 us, 5.1 TB/s.  (Codes by comparing with every border instead of the hardware's
 // conversion: 35 us, the vector units' time.)
 #include "gdr_attn.h"
 #include "gdr_vec.h"
@@ -100,8 +100,9 @@ __device__ __forceinline__ void places_of(const KvArgs &a, const int (&t)[ROWS],
   }
 }
 
-// A thread takes ROWS rows, 16 apart, so that their places' chains of loads run side by side.  Reading back, whose
-// bytes wait for the place, takes 4; storing, which reads its rows meanwhile, one.
+// A thread takes ROWS rows, 16 apart, so that their places' chains of loads run side by side: 2 to read
+// back and to store many rows, 1 to store few (32674 tokens of 4 heads stored and read back 35.8 us; stored with
+// 1 37.0; 10600 rows stored and 66000 read back 16.6 us, stored with 2 17.2).
 template <bool STORE, int ROWS>
 __global__ __launch_bounds__(256) void kv_kernel(KvArgs a) {
   const int x = threadIdx.x & 15;
@@ -156,8 +157,11 @@ hipError_t launch_kv(const gdr_kv &p, bool store, int32_t T, const int32_t *cu, 
   const KvArgs a{p.k_codes, p.v_codes, p.k_scale, p.v_scale, p.page_table, cu, start, k, v, k_stride, v_stride, T, p.H_kv, p.N,
                  p.n_pages, __builtin_ctz((unsigned)p.page), p.max_pages};
   const int64_t rows = (int64_t)T * p.H_kv;
-  if (store) kv_kernel<true, 1><<<dim3((uint32_t)((rows + 15) / 16)), 256, 0, stream>>>(a);
-  else kv_kernel<false, 4><<<dim3((uint32_t)((rows + 63) / 64)), 256, 0, stream>>>(a);
+  auto blocks = [&](int each) { return dim3((uint32_t)((rows + 16 * each - 1) / (16 * each))); };
+  const bool many = rows >= 65536;  // more than a round of blocks with 2 rows a thread
+  if (store && many) kv_kernel<true, 2><<<blocks(2), 256, 0, stream>>>(a);
+  else if (store) kv_kernel<true, 1><<<blocks(1), 256, 0, stream>>>(a);
+  else kv_kernel<false, 2><<<blocks(2), 256, 0, stream>>>(a);
   return hipGetLastError();
 }
 
