@@ -125,9 +125,12 @@ hipError_t launch_kv(const gdr_kv &p, bool store, int32_t T, const int32_t *cu, 
 
 // A sequence's tokens are shared by `splits` blocks for every kv head and 16 rows of
 // its run (`row_tiles` of them are launched; longer runs loop).  A block takes at least
-// STEP_UNIT tokens; a launch has about STEP_BLOCKS blocks.
-constexpr int STEP_UNIT = 128;
-constexpr int STEP_BLOCKS = 8192;
+// STEP_UNIT tokens.  Two rounds of blocks (768 run at once) fill the chip, and more of them only add
+// starts and parts (256 sequences of 1000, 16 heads on 4: 29 us unsplit, 39 with 4096 blocks, 49 with 8192); where
+// a table has room for sequences so long that each of them still gets STEP_LONG tokens, up to STEP_MOST
+// blocks even out sequences of different lengths (64 of 1 to 32000, 32 heads on 8: 235 us with 1536, 221 with 4096).
+constexpr int STEP_UNIT = 128, STEP_LONG = 1024;
+constexpr int STEP_BLOCKS = 1536, STEP_MOST = 4096;
 struct StepPlan {
   int splits, row_tiles;
   int64_t blocks;
@@ -138,8 +141,9 @@ inline StepPlan step_plan(int32_t T, int32_t N, int32_t H_q, int32_t H_kv, int32
   const int64_t run = N > 0 ? std::max<int64_t>(1, ((int64_t)T + N - 1) / N) : 1;
   s.row_tiles = (int)std::min<int64_t>((run * (H_q / H_kv) + 15) / 16, 4096);
   const int64_t items = std::max<int64_t>(1, (int64_t)N * H_kv * s.row_tiles);
-  const int64_t most = ((int64_t)max_pages * page + STEP_UNIT - 1) / STEP_UNIT;
-  s.splits = (int)std::max<int64_t>(1, std::min<int64_t>(most, STEP_BLOCKS / items));
+  const int64_t room = (int64_t)max_pages * page, most = (room + STEP_UNIT - 1) / STEP_UNIT;
+  const int64_t want = std::max<int64_t>(STEP_BLOCKS / items, std::min<int64_t>(STEP_MOST / items, room / STEP_LONG));
+  s.splits = (int)std::max<int64_t>(1, std::min(most, want));
   s.blocks = items * s.splits;
   s.bytes = s.splits > 1 ? ((int64_t)T * H_q * s.splits * 130 * 4 + 255) / 256 * 256 : 0;
   return s;

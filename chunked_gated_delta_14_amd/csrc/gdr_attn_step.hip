@@ -13,9 +13,9 @@
 //
 // A sequence's tokens are split over blocks, and over a block's wavefronts; each keeps a running
 // maximum and sum, the block joins its wavefronts' in LDS, and a second kernel
-// joins the blocks' where there are several.  64 sequences of 1 to 32000 tokens, 32 heads on 8: 223 us,
-// 5.2 TB/s past a copy's rate, vector units half busy, and 6 us for the join; one of 4096, 16 heads on 2: 5.0 us, its
-// chain of loads, and 3.5.  (Two tiles' registers, the next loaded whole while one is worked on, leave two
+// joins the blocks' where there are several.  64 sequences of 1 to 32000 tokens, 32 heads on 8: a call
+// 221 us, 5.1 TB/s of the cache's bytes, a copy's rate, vector units half busy; one of 4096, 16 heads on 2: 5.0 us, its
+// chain of loads, and 3.5 for the join.  (Two tiles' registers, the next loaded whole while one is worked on, leave two
 // wavefronts to a SIMD instead of three: 276 us.  Four, which spills: 303.)
 #include "gdr_attn_device.h"
 #include "gdr_vec.h"
