@@ -73,20 +73,24 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(BwdArgs a) {
   };
   if (begin < end) copy(begin, 0);
   bf16x8 Q[8], G[8];
-  float delta = 0.f;
   const int64_t at = ((int64_t)(e.row0 + row) * a.Hq + head) * HD + 8 * h;
+  // delta is the diagonal of O dO^T by the products that give dP, in their order: where a row sees one key, and o is
+  // that key's v, dP - delta is then zero as the formula has it, not the difference of two sums' roundings.
+  f32x16 OG = zero16();
   {
     const u16 *qp = a.q + (int64_t)(e.row0 + row) * a.qs + head * HD + 8 * h;
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk) {
       Q[kk] = ld8(qp + 16 * kk);
       G[kk] = ld8(a.go + at + 16 * kk);
-      const bf16x8 o = ld8(a.o + at + 16 * kk);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) delta = fmaf((float)G[kk][j], (float)o[j], delta);
+      OG = mfma32(ld8(a.o + at + 16 * kk), G[kk], OG);
     }
   }
-  delta += other_half(delta);
+  float delta = 0.f;  // row lr of column lr: register 4 (lr >> 3) + (lr & 3) of half (lr >> 2) & 1
+#pragma unroll
+  for (int i = 0; i < 16; ++i) delta = i == 4 * (lr >> 3) + (lr & 3) ? OG[i] : delta;
+  const float other = other_half(delta);
+  delta = h == ((lr >> 2) & 1) ? delta : other;
   const int64_t stat = (int64_t)head * a.Tq + e.row0 + row;
   const float given = a.lse[stat];
   const float lse = given == -INFINITY ? NO_KEYS : given * LOG2E;
