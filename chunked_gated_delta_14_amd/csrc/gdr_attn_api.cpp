@@ -314,6 +314,8 @@ int32_t check_step_sizes(int32_t T, int32_t N, int32_t H_q, int32_t H_kv, int32_
   if (H_q % H_kv) return unsupported("H_q must be a multiple of H_kv");
   if (H_q > 65536) return unsupported("H above 65536");
   if ((int64_t)T * H_q > (int64_t(1) << 36)) return unsupported("more than 2^36 rows and heads");
+  // places and rows are 32-bit in the kernel, sums of two of them and a block's share past the last among them
+  if (T > kMostTokens || (int64_t)max_pages * page > kMostTokens) return unsupported("more than 2^30 rows, or places of a sequence");
   return GDR_OK;
 }
 int32_t step(const gdr_kv *c, const gdr_attn_step *p, uint16_t *o, void *ws, int64_t ws_bytes, void *stream) {
