@@ -7,8 +7,8 @@
 //   S^T (token, row) = K Q^T:    A lane: 32 channels 32 g .. of token lr, one 16-byte load;
 //   O^T (channel, row) += V^T P^T: A lane: channels 8 lr .. 8 lr + 7 of tokens 4 g .. 4 g + 3
 //       of either half of the 32, which is where S^T's registers hold the probabilities.
-// Codes become bf16, exactly, by the hardware's scaled conversion; V's are then regrouped
-// from pairs of channels to pairs of tokens.  The order of channels within a product is
+// Codes become bf16, exactly, by the hardware's scaled conversion, which makes NaN of the infinite scale that a byte
+// of 255 gives; V's are then regrouped from pairs of channels to pairs of tokens.  The order of channels within a product is
 // free, so both sides read the cache as it lies: row by row.
 //
 // A sequence's tokens are split over blocks, and over a block's wavefronts; each keeps a running
@@ -57,6 +57,9 @@ __device__ __forceinline__ uint32_t pair(uint32_t c, float s) {
 }
 __device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
 
+// RUNS: sequences may have several rows, which see different tokens (a row a sequence without: 256 sequences of 1000, 16
+// heads on 4, 27.7 us for 28.2 with).
+template <bool RUNS>
 __global__ __launch_bounds__(256, 3) void attn_step_kernel(StepArgs a) {
   constexpr int PITCH = 132;
   __shared__ __align__(16) float so[4][16][PITCH];
@@ -90,6 +93,9 @@ __global__ __launch_bounds__(256, 3) void attn_step_kernel(StepArgs a) {
 #pragma unroll
     for (int d = 0; d < 8; ++d) O[d] = zero4();
     float m = -1.5e38f, l = 0.f;
+    // Values that are NaN (a scale byte of 255) in tiles that not every row sees all of: there they count as finite, as 0
+    // times them would reach rows that they are hidden from.  Bit 8 b + 7: this lane's row sees one in its channels 32 b .. .
+    uint32_t bad = 0;
 
     // pages of this wavefront's next 32 tiles, two to a tile, one a lane
     int pv = -1;
@@ -158,9 +164,14 @@ __global__ __launch_bounds__(256, 3) void attn_step_kernel(StepArgs a) {
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int t = j + 16 * u + 4 * g + r;
-            const bool there = (u ? pg1 : pg0) >= 0;
-            if (!there || t > hi || t < lo) S[u][r] = -INFINITY;
+            const bool there = (u ? pg1 : pg0) >= 0, seen = there && t <= hi && t >= lo;
+            if (!seen) S[u][r] = -INFINITY;
             if (!there || t >= s.len || t < s.begin) vc[4 * u + r] = 0, vs[u][r] = 0x7f7f7f7fu;  // whatever lies there
+            if constexpr (RUNS) {
+              const uint32_t w = vs[u][r], nans = ((w & 0x7f7f7f7fu) + 0x01010101u) & w & 0x80808080u;
+              vs[u][r] = w ^ nans;
+              bad |= seen ? nans : 0u;
+            }
           }
       }
       float top = fmaxf(fmaxf(fmaxf(S[0][0], S[0][1]), fmaxf(S[0][2], S[0][3])), fmaxf(fmaxf(S[1][0], S[1][1]), fmaxf(S[1][2], S[1][3])));
@@ -211,6 +222,13 @@ __global__ __launch_bounds__(256, 3) void attn_step_kernel(StepArgs a) {
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
     // the wavefronts' results: lane (g, lr) holds channels 32 g + 8 r .. +7 of row lr in O[0..7][r]
+    if constexpr (RUNS) {
+      bad |= __shfl_xor(bad, 16);
+      bad |= __shfl_xor(bad, 32);
+      if (bad >> (8 * g + 7) & 1)
+#pragma unroll
+        for (int d = 0; d < 8; ++d) O[d] = zero4() + __builtin_nanf("");
+    }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       *reinterpret_cast<f32x4 *>(&so[wave][lr][32 * g + 8 * r]) = f32x4{O[0][r], O[1][r], O[2][r], O[3][r]};
@@ -300,7 +318,9 @@ StepArgs args(const gdr_kv &c, const gdr_attn_step &p, uint16_t *o, void *ws, co
 
 hipError_t launch_attn_step(const gdr_kv &c, const gdr_attn_step &p, uint16_t *o, void *ws, const StepPlan &plan, hipStream_t stream) {
   if (p.T == 0 || c.N == 0) return hipSuccess;
-  attn_step_kernel<<<dim3((uint32_t)plan.blocks), 256, 0, stream>>>(args(c, p, o, ws, plan));
+  const StepArgs a = args(c, p, o, ws, plan);
+  if (p.cu_seqlens) attn_step_kernel<true><<<dim3((uint32_t)plan.blocks), 256, 0, stream>>>(a);
+  else attn_step_kernel<false><<<dim3((uint32_t)plan.blocks), 256, 0, stream>>>(a);
   return hipGetLastError();
 }
 hipError_t launch_attn_step_join(const gdr_kv &c, const gdr_attn_step &p, uint16_t *o, void *ws, const StepPlan &plan,

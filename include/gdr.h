@@ -547,8 +547,8 @@ int32_t gdr_kv_load(const gdr_kv *p, int32_t T, const int32_t *cu_seqlens, const
  * the last row sees all of them, the one before all but the last, and so on, each within
  * `window` tokens up to its own (0: all).  lens is clipped to [0, max_pages * page], which is at most
  * 2^30 here, and cu_seqlens to [0, T].  Keys of a page outside [0, n_pages) are hidden.  A row that sees no key gets 0;
- * rows that no sequence covers are left as they were.  A non-finite value held by a later
- * token of the same run may reach a row's output.  Workspace: gdr_attn_step_workspace_bytes. */
+ * rows that no sequence covers are left as they were.  Channels that read as NaN reach the rows that see
+ * their token, and no others.  Workspace: gdr_attn_step_workspace_bytes. */
 typedef struct gdr_attn_step {
   int32_t T, H_q, window;
   float scale;

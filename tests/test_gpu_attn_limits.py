@@ -1,11 +1,11 @@
 """The attention layers' operators where a formula's terms cancel or leave the ordinary
-range: rows that see one key."""
+range: rows that see one key, values in the cache that are not finite."""
 import pytest
 import torch
 
 import attn_ref as ref
 import chunked_gated_delta_14_amd as gdr
-from test_gpu_attn import BF, cu_of, gen, heads
+from test_gpu_attn import BF, cu_of, gen, heads, ints, pool
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +45,44 @@ def test_rows_that_see_one_key(docs, docs_k, Hq, Hkv, window):
     want = ref.attention(q, k, v, cu, ck, True, window, dout=do)
     for name, x in (("o", o), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv)):
         ref.check(name, x, *want[name])
+
+
+@pytest.mark.parametrize("lens,runs,Hq,Hkv,page,window,poison", [
+    ([20], None, 2, 1, 16, 0, [7]),                                  # a token that every row sees
+    ([12], [3], 2, 1, 16, 3, [7]),                                   # in the first row's window only
+    ([12], [3], 2, 1, 16, 0, [11]),                                  # the last row's own
+    ([300, 45], [8, 5], 4, 2, 16, 40, [254, 293, 299, 300 + 2, 300 + 41]),
+    ([1000, 70], [6, 1], 16, 1, 64, 100, [0, 895, 897, 899, 996, 1000 + 69]),
+    ([3000, 500], [1, 9], 6, 3, 128, 0, [5, 2999, 3000 + 495, 3000 + 33]),
+    ([700], [30], 2, 2, 32, 25, list(range(640, 700, 7))),
+])
+@pytest.mark.parametrize("side", ["k", "v"])
+def test_held_values_that_are_not_finite(lens, runs, Hq, Hkv, page, window, poison, side):
+    """32 channels with a NaN or infinity among them read as NaN, in attention as in a load, and reach the rows that see their
+    token and no others: a key all of a row's channels, a value its own 32."""
+    g, rows = gen(sum(lens) + Hq), runs or [1] * len(lens)
+    cache, table = pool(g, lens, Hkv, page)
+    cu, held = cu_of(rows), cu_of(lens)
+    x = {n: heads(g, held[-1], Hkv) for n in ("k", "v")}
+    for i, t in enumerate(poison):
+        x[side][t, i % Hkv, (37 * i + 5) % 128] = [float("nan"), float("inf"), -float("inf")][i % 3]
+    every = gdr.KvProblem(cache, table, None, held[-1], ints(held))
+    gdr.kv_store(every, x["k"], x["v"])
+    K, V = torch.empty_like(x["k"]), torch.empty_like(x["v"])
+    gdr.kv_load(every, K, V)
+    q = heads(g, cu[-1], Hq)
+    p = gdr.AttnStep(q, cache, table, ints(lens), ints(cu) if runs else None, window=window)
+    o = torch.empty(cu[-1], Hq, 128, dtype=BF, device="cuda")
+    gdr.attn_step(p, o, p.alloc_workspace().fill_(0xFF))
+    nan = torch.zeros(cu[-1], Hkv, 128, dtype=torch.bool, device="cuda")
+    for n in range(len(lens)):
+        seen = ref.seen_mask(rows[n], lens[n], True, window, "cuda").float()
+        bad = torch.isnan((K if side == "k" else V)[held[n]: held[n + 1]]).float()
+        assert bad.sum() % 32 == 0
+        if side == "k":
+            bad = bad.amax(2, keepdim=True).expand(-1, -1, 128)
+        nan[cu[n]: cu[n + 1]] = torch.mm(seen, bad.flatten(1)).unflatten(1, (Hkv, 128)) > 0
+    nan = nan.repeat_interleave(Hq // Hkv, 1)
+    assert nan.any() and torch.isnan(o).equal(nan)
+    want, bound = ref.attention(q, K.nan_to_num(0.0), V.nan_to_num(0.0), cu, held, True, window)["o"]
+    ref.check("o", o[~nan], want[~nan], bound[~nan])
