@@ -186,11 +186,14 @@ class AttnProblem(_Base):
     """Softmax attention over a packed batch.
 
     q: bf16 [T_q, H_q, 128]; k, v: bf16 [T_k, H_kv, 128], rows 16-byte aligned at any stride; plan: the batch's AttnPlan.
-    The problem holds the forward's workspace (none unless few rows have many keys).  What it holds follows from the problem's
-    inputs alone, so calls that overlap without those changing write the same there; overlapping calls on changing
-    inputs would race on the inputs already.  Keep the problem until its calls are done."""
+    The problem holds the forward's workspace: none unless tiles of 128 rows and 64 keys differ so much in number of keys, or are
+    so few, that long ones are shared by several blocks; then 65 KB a part and head, 182 MB at most (below 2^11 steps of
+    64 keys a part).  What it holds follows from the problem's inputs alone, so calls that overlap without those changing write
+    the same there; overlapping calls on changing inputs would race on the inputs already.  Keep the problem until its calls
+    are done.  share: another problem, whose forward's workspace this one uses too, as the layers of a model can, whose calls
+    follow each other (those of problems that share must not overlap)."""
 
-    def __init__(self, q, k, v, plan, scale=None):
+    def __init__(self, q, k, v, plan, scale=None, share=None):
         import torch
 
         self._device_of(q, "q")
@@ -212,7 +215,13 @@ class AttnProblem(_Base):
                          self.scale, qs, ks, vs, _p(q), _p(k), _p(v), _p(plan.table))
         self.cstruct = ctypes.byref(self._c)
         self._fwd_bytes = _bytes(lib().gdr_attn_workspace_bytes(self.cstruct, 0))
-        self._fwd_ws = torch.empty(self._fwd_bytes, dtype=torch.uint8, device=dev) if self._fwd_bytes else None
+        self._fwd_ws = None
+        if self._fwd_bytes and share is not None:
+            if share.device != dev or share._fwd_bytes < self._fwd_bytes:
+                _bad("the shared workspace must be on %s and hold %d bytes, not %d" % (dev, self._fwd_bytes, share._fwd_bytes))
+            self._fwd_ws = share._fwd_ws
+        elif self._fwd_bytes:
+            self._fwd_ws = torch.empty(self._fwd_bytes, dtype=torch.uint8, device=dev)
 
     def workspace_bytes(self) -> int:
         return _bytes(lib().gdr_attn_workspace_bytes(self.cstruct, 1))

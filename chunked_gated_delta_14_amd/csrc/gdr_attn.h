@@ -45,7 +45,8 @@ constexpr int ATT_QTILE = 128, ATT_KTILE = 256;
 constexpr int ATT_ENTRY = 8;
 
 // The table: the entries of the query tiles and of the key tiles, then the lists of parts of
-// either kind by level, an item of 2 int32: the tile, and the part + its tile's parts << 16.
+// either kind by level, an item of 2 int32: the tile, and the part + its tile's parts << 16.  Items with the most
+// steps come first, a tile's parts in a row; an item's place in the list is its slot in the workspace.
 constexpr int ATT_PARTS = 64;
 inline int attn_parts(int64_t steps, int level) {
   return (int)std::min<int64_t>(std::max<int64_t>((steps + (int64_t(1) << level) - 1) >> level, 1), ATT_PARTS);
@@ -59,18 +60,19 @@ inline int64_t attn_items(const int32_t (&items)[GDR_ATTN_LEVELS], int levels) {
 // idle, or a few long tiles would run on after the others, it takes the list of parts whose
 // steps come nearest the mean load of `slots` blocks, but not fewer than `least`, which a block's start and
 // its part's way through memory outweigh; a second kernel then joins the parts' fp32
-// results in order.
+// results in order, a block for a slot and head, which takes its share of its tile's rows.
 struct AttnShare {
   int level;        // -1: whole tiles
   int parts;        // the longest tile's
   int64_t blocks;   // tiles or parts, of one head
   int64_t items;    // the list's place in the table, in int32
+  int64_t slots;    // the list's first items, which hold all that are one of several parts
 };
 inline AttnShare attn_share(const gdr_attn_plan &p, bool keys, int64_t heads, int slots, int least) {
   const int32_t (&items)[GDR_ATTN_LEVELS] = keys ? p.k_items : p.q_items;
   const int32_t tiles = keys ? p.n_k_tiles : p.n_q_tiles, longest = keys ? p.k_longest : p.q_longest;
   const int64_t mean = std::max<int64_t>(least, ((keys ? p.k_steps : p.q_steps) * heads + slots - 1) / slots);
-  AttnShare s{-1, 1, tiles, 0};
+  AttnShare s{-1, 1, tiles, 0, 0};
   if (longest <= mean + mean / 2) return s;
   int level = 0;
   while (level < GDR_ATTN_LEVELS - 1 && (int64_t(4) << level) <= 3 * mean) ++level;  // the power of two within 3/4 and 3/2 of it
@@ -79,6 +81,8 @@ inline AttnShare attn_share(const gdr_attn_plan &p, bool keys, int64_t heads, in
   s.parts = attn_parts(longest, level);
   s.blocks = items[level];
   s.items = ((int64_t)p.n_q_tiles + p.n_k_tiles) * ATT_ENTRY + 2 * ((keys ? attn_items(p.q_items, GDR_ATTN_LEVELS) : 0) + attn_items(items, level));
+  // one of several parts has more than half of 2^level steps, and so has what stands before it
+  s.slots = std::min<int64_t>(items[level], 2 * (keys ? p.k_steps : p.q_steps) >> level);
   return s;
 }
 // Blocks of 128 query rows run two to a compute unit, and two rounds of them even out; blocks of 256 keys, whose
@@ -89,12 +93,14 @@ inline AttnShare attn_k_share(const gdr_attn &p) {
   const int group = p.H_q / p.H_kv;
   return attn_share(p.plan, true, p.H_kv, ATT_K_SLOTS, std::max(1, 4 / group));
 }
-// The workspace.  Forward: the parts' rows [part][T_q][H_q][128], then their maxima and sums
-// [part][H_q][T_q][2].  Backward: lse and delta of every row and head as the
-// matrix kernels take them, [H_q][T_q] each; the parts of dq [part][T_q][H_q][128], of dk and of dv
-// [part][T_k][H_kv][128].
+// The workspace.  Forward: the parts' rows [slot][H_q][128][128], then their maxima and sums
+// [slot][H_q][128][2].  Backward: lse and delta of every row and head as the
+// matrix kernels take them, [H_q][T_q] each; the parts of dq [slot][H_q][128][128], of dk and of dv
+// [slot][H_kv][256][128].  2^level is more than 3/4 of a block's mean load, so slots times heads are below 2731 (8/3 of
+// 1024 blocks) and 1024: 182 MB forward, and 447 MB beside lse and delta backward, whatever a batch holds (of parts of up to 2^11 steps).
+constexpr int64_t ATT_QPART = ATT_QTILE * 128, ATT_KPART = ATT_KTILE * 128;  // floats of a slot's head
 struct AttnWorkspace {
-  int64_t stats, q_part, k_part, fwd, bwd;  // bytes: a row of stats, a part's, the whole
+  int64_t stats, fwd, bwd;  // bytes: a row of stats, the whole
   AttnShare q, k;
 };
 inline AttnWorkspace attn_workspace(const gdr_attn &p) {
@@ -103,10 +109,8 @@ inline AttnWorkspace attn_workspace(const gdr_attn &p) {
   w.q = attn_q_share(p);
   w.k = attn_k_share(p);
   w.stats = up((int64_t)p.T_q * p.H_q * 4);
-  w.q_part = w.q.parts > 1 ? up((int64_t)p.T_q * p.H_q * 128 * 4) : 0;
-  w.k_part = w.k.parts > 1 ? up((int64_t)p.T_k * p.H_kv * 128 * 4) : 0;
-  w.fwd = w.q.parts > 1 ? w.q.parts * (w.q_part + up((int64_t)p.T_q * p.H_q * 8)) : 0;
-  w.bwd = 2 * w.stats + w.q.parts * w.q_part + 2 * w.k.parts * w.k_part;
+  w.fwd = w.q.slots * p.H_q * (ATT_QPART + 2 * ATT_QTILE) * 4;
+  w.bwd = 2 * w.stats + (w.q.slots * p.H_q * ATT_QPART + 2 * w.k.slots * p.H_kv * ATT_KPART) * 4;
   return w;
 }
 hipError_t launch_attn_fwd(const gdr_attn &p, uint16_t *o, float *lse, void *ws, hipStream_t stream);

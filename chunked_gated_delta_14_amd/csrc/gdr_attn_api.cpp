@@ -115,10 +115,9 @@ int32_t check_attn(const gdr_attn *p) {
       !rows_ok(p->v, p->v_stride, p->H_kv, p->T_k))
     return invalid(kRows);
   if ((int64_t)p->H_q * 128 >= (1 << 24)) return unsupported("H_q * 128 of 2^24 or more");
-  // a launch has a block for every part and head, and 8 (16) for every tile and head to join them
+  // a launch has a block for every part and head, and a block, or four, for every slot and head to join them
   const gdr::AttnShare q = gdr::attn_q_share(*p), k = gdr::attn_k_share(*p);
-  const int64_t q_blocks = std::max(q.blocks, q.parts > 1 ? (int64_t)plan.n_q_tiles * 8 : 0);
-  const int64_t k_blocks = std::max(k.blocks, k.parts > 1 ? (int64_t)plan.n_k_tiles * 16 : 0);
+  const int64_t q_blocks = std::max(q.blocks, q.slots), k_blocks = std::max(k.blocks, 4 * k.slots);
   if (!grid_ok(q_blocks * p->H_q + k_blocks * p->H_kv, 512)) return unsupported("too many rows and heads for one launch");
   return GDR_OK;
 }
@@ -258,6 +257,7 @@ int32_t plan_attn(const int32_t *cu_q, const int32_t *cu_k, int32_t N, bool caus
         const int n = gdr::attn_parts(tiles[side][i].cost, level);
         for (int x = 0; x < n; ++x) parts.push_back(Part{(int32_t)i, x | n << 16, (tiles[side][i].cost + n - 1) / n});
       }
+      // a tile's parts cost the same, so a stable order keeps them in a row
       std::stable_sort(parts.begin(), parts.end(), [](const Part &a, const Part &b) { return a.cost > b.cost; });
       for (const Part &x : parts) *table++ = x.tile, *table++ = x.part;
     }

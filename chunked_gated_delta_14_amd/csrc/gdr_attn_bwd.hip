@@ -28,8 +28,8 @@ struct BwdArgs {
   const int32_t *tiles, *items;
   u16 *dq, *dk, *dv;
   float *lse2, *delta, *pq, *pk, *pv;
-  int64_t qs, ks, vs, dqs, dks, dvs, part_size;  // part_size: floats of one part's sums
-  int Hq, Hkv, group, Tq, Tk, level, causal, window;
+  int64_t qs, ks, vs, dqs, dks, dvs;
+  int Hq, Hkv, group, Tq, Tk, causal, window;
   float scale;
 };
 
@@ -132,7 +132,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(BwdArgs a) {
     }
   }
   if (x.parts == 1) store_row(a.dq + (int64_t)(e.row0 + row) * a.dqs + head * HD, D, a.scale, h, live);
-  else if (live) store_floats(a.pq + x.part * a.part_size + ((int64_t)(e.row0 + row) * a.Hq + head) * HD, D, h);
+  else if (live) store_floats(a.pq + ((int64_t)x.slot * a.Hq + head) * ATT_QPART + row * HD, D, h);
 }
 
 // Eight wavefronts, 32 keys each, share the tiles in LDS; the keys' sums take half of a wavefront's
@@ -266,42 +266,43 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_kernel(BwdArgs a) {
     store_row(a.dk + (int64_t)(e.row0 + row) * a.dks + kvh * HD, dK, a.scale, h2, live);
     store_row(a.dv + (int64_t)(e.row0 + row) * a.dvs + kvh * HD, dV, 1.f, h2, live);
   } else if (live) {
-    const int64_t to = x.part * a.part_size + ((int64_t)(e.row0 + row) * a.Hkv + kvh) * HD;
+    const int64_t to = ((int64_t)x.slot * a.Hkv + kvh) * ATT_KPART + row * HD;
     store_floats(a.pk + to, dK, h2);
     store_floats(a.pv + to, dV, h2);
   }
 }
 
-// Adds the parts of a tile's rows in order: 16 threads a row, 8 channels each.  Blocks of both
-// sides: dq of the query tiles (`qblocks` blocks, if they have parts), then dk and dv of the key tiles.
+// Adds the parts of a tile's rows in order: a block takes its slot's share of the rows, 16 threads a row, 8 channels
+// each.  Blocks of both sides: dq of the query tiles (`qblocks` blocks, if they have parts), then the key tiles', which have
+// four to a slot and head, dk's and dv's halves of the share.
 struct JoinArgs {
   BwdArgs q, k;
   int64_t qblocks;
 };
-__device__ __forceinline__ void join_row(const float *src, int64_t part_size, int parts, float f, u16 *to) {
-  f32x4 u = zero4(), v = zero4();
-  for (int x = 0; x < parts; ++x) {
-    const f32x4 *p = reinterpret_cast<const f32x4 *>(src + x * part_size);
-    u += p[0], v += p[1];
-  }
-  *reinterpret_cast<u32x4 *>(to) =
-      u32x4{pk2bf(u[0] * f, u[1] * f), pk2bf(u[2] * f, u[3] * f), pk2bf(v[0] * f, v[1] * f), pk2bf(v[2] * f, v[3] * f)};
-}
-__global__ __launch_bounds__(256) void attn_bwd_join_kernel(JoinArgs j) {
+__global__ __launch_bounds__(ATT_JOIN) void attn_bwd_join_kernel(JoinArgs j) {
   const bool keys = blockIdx.x >= j.qblocks;
   const BwdArgs &a = keys ? j.k : j.q;
-  const int per = (keys ? ATT_KTILE : ATT_QTILE) / 16, heads = keys ? a.Hkv : a.Hq;  // blocks a tile
-  const int64_t x = blockIdx.x - (keys ? j.qblocks : 0), b = x / per;
-  const int head = (int)(b % heads), r = (int)(x % per) * 16 + (threadIdx.x >> 4), c = (threadIdx.x & 15) * 8;
-  const TileEntry e(a.tiles, (int)(b / heads));
-  const int parts = e.parts(a.level);
-  if (parts == 1 || r >= e.rows) return;
-  const int64_t row = e.row0 + r, at = (row * heads + head) * HD + c;
-  if (keys) {
-    join_row(a.pk + at, a.part_size, parts, a.scale, a.dk + row * a.dks + head * HD + c);
-    join_row(a.pv + at, a.part_size, parts, 1.f, a.dv + row * a.dvs + head * HD + c);
-  } else {
-    join_row(a.pq + at, a.part_size, parts, a.scale, a.dq + row * a.dqs + head * HD + c);
+  const int b = blockIdx.x - (keys ? (int)j.qblocks : 0), heads = keys ? a.Hkv : a.Hq;
+  const int pieces = keys ? 2 : 1;
+  const Share x(a.items, keys ? b >> 2 : b, heads);
+  if (x.parts == 1) return;
+  const TileEntry e(a.tiles, x.tile);
+  const int piece = x.part * pieces + (keys ? b & 1 : 0), c = (threadIdx.x & 15) * 8;
+  const int last = e.rows * (piece + 1) / (x.parts * pieces);
+  const bool values = keys && (b & 2);
+  const int64_t part = keys ? ATT_KPART : ATT_QPART, next = heads * part;
+  const float *src = (keys ? values ? a.pv : a.pk : a.pq) + ((int64_t)(x.slot - x.part) * heads + x.head) * part + c;
+  u16 *to = (keys ? values ? a.dv : a.dk : a.dq) + x.head * HD + c;
+  const int64_t stride = keys ? values ? a.dvs : a.dks : a.dqs;
+  const float f = values ? 1.f : a.scale;
+  for (int r = e.rows * piece / (x.parts * pieces) + (threadIdx.x >> 4); r < last; r += ATT_JOIN / 16) {
+    f32x4 u = zero4(), v = zero4();
+    for (int i = 0; i < x.parts; ++i) {
+      const f32x4 *p = reinterpret_cast<const f32x4 *>(src + i * next + r * HD);
+      u += p[0], v += p[1];
+    }
+    *reinterpret_cast<u32x4 *>(to + (int64_t)(e.row0 + r) * stride) =
+        u32x4{pk2bf(u[0] * f, u[1] * f), pk2bf(u[2] * f, u[3] * f), pk2bf(v[0] * f, v[1] * f), pk2bf(v[2] * f, v[3] * f)};
   }
 }
 
@@ -314,11 +315,9 @@ BwdArgs args(const gdr_attn &p, bool keys, void *ws) {
   a.lse2 = reinterpret_cast<float *>(base);
   a.delta = reinterpret_cast<float *>(base + w.stats);
   a.pq = reinterpret_cast<float *>(base + 2 * w.stats);
-  a.pk = a.pq + w.q.parts * (w.q_part / 4);
-  a.pv = a.pk + w.k.parts * (w.k_part / 4);
-  a.part_size = (keys ? w.k_part : w.q_part) / 4;
+  a.pk = a.pq + w.q.slots * p.H_q * ATT_QPART;
+  a.pv = a.pk + w.k.slots * p.H_kv * ATT_KPART;
   const AttnShare &share = keys ? w.k : w.q;
-  a.level = share.level;
   a.items = share.level < 0 ? nullptr : p.tile_table + share.items;
   a.qs = p.q_stride, a.ks = p.k_stride, a.vs = p.v_stride;
   a.Hq = p.H_q, a.Hkv = p.H_kv, a.group = p.H_q / p.H_kv, a.Tq = p.T_q, a.Tk = p.T_k;
@@ -350,10 +349,10 @@ hipError_t launch_attn_bwd_join(const gdr_attn &p, uint16_t *dq, int64_t dq_stri
   JoinArgs j{args(p, false, ws), args(p, true, ws), 0};
   j.q.dq = dq, j.q.dqs = dq_stride;
   j.k.dk = dk, j.k.dv = dv, j.k.dks = dk_stride, j.k.dvs = dv_stride;
-  j.qblocks = attn_q_share(p).parts > 1 ? (int64_t)p.plan.n_q_tiles * p.H_q * (ATT_QTILE / 16) : 0;
-  const int64_t kblocks = attn_k_share(p).parts > 1 ? (int64_t)p.plan.n_k_tiles * p.H_kv * (ATT_KTILE / 16) : 0;
+  j.qblocks = attn_q_share(p).slots * p.H_q;
+  const int64_t kblocks = attn_k_share(p).slots * p.H_kv * 4;
   if (j.qblocks + kblocks == 0) return hipSuccess;
-  attn_bwd_join_kernel<<<dim3((uint32_t)(j.qblocks + kblocks)), 256, 0, stream>>>(j);
+  attn_bwd_join_kernel<<<dim3((uint32_t)(j.qblocks + kblocks)), ATT_JOIN, 0, stream>>>(j);
   return hipGetLastError();
 }
 

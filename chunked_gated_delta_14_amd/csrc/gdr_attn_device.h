@@ -132,17 +132,17 @@ __device__ __forceinline__ void store_floats(float *row, const f32x16 (&acc)[4],
           f32x4{acc[dt][4 * a], acc[dt][4 * a + 1], acc[dt][4 * a + 2], acc[dt][4 * a + 3]};
 }
 
-// The tile, its part and the head of a block.  Block ids go round the 8 XCDs; where the
-// heads divide by 8 an XCD takes neighbouring heads, which share keys in its L2.
+// The tile, its part and the head of a block, and the part's slot in the workspace.  Block ids go round the 8
+// XCDs; where the heads divide by 8 an XCD takes neighbouring heads, which share keys in its L2.
 struct Share {
-  int tile, part, parts, head;
+  int tile, part, parts, head, slot;
   __device__ __forceinline__ Share(const int32_t *items, int b, int heads) {
-    tile = b / heads;
+    slot = tile = b / heads;
     const int r = b - tile * heads;
     head = (heads & 7) == 0 ? (r & 7) * (heads >> 3) + (r >> 3) : r;
     part = 0, parts = 1;
     if (items) {
-      ConstI32 it = (ConstI32)(items + 2 * (int64_t)tile);
+      ConstI32 it = (ConstI32)(items + 2 * (int64_t)slot);
       tile = it[0];
       part = it[1] & 0xffff, parts = it[1] >> 16;
     }
@@ -155,12 +155,12 @@ struct TileEntry {
     ConstI32 e = (ConstI32)(table + (int64_t)i * ATT_ENTRY);
     row0 = e[0], rows = e[1], other0 = e[2], other = e[3], first = e[4], shift = e[5], begin = e[6], end = e[7];
   }
-  // Steps of 64 of the other side's rows, and into how many parts a list deals them.
+  // Steps of 64 of the other side's rows.
   __device__ __forceinline__ int steps() const { return begin < end ? (end - begin + KT - 1) / KT : 0; }
-  __device__ __forceinline__ int parts(int level) const {
-    return min(max((steps() + (1 << level) - 1) >> level, 1), ATT_PARTS);
-  }
 };
+
+// The kernels that join parts: threads of a block, 16 to a row.
+constexpr int ATT_JOIN = 512;
 
 constexpr float LOG2E = 1.44269504088896341f;
 constexpr float LN2 = 0.693147180559945309f;

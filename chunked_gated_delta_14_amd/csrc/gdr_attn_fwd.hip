@@ -26,10 +26,9 @@ struct FwdArgs {
   const int32_t *tiles, *items;
   u16 *o;
   float *lse;
-  float *part, *ml;  // [part][T_q][H_q][128], [part][H_q][T_q][2]
+  float *part, *ml;  // [slot][H_q][128][128], [slot][H_q][128][2]
   int64_t qs, ks, vs;
-  int64_t part_size, ml_size;  // floats of one part's
-  int Hq, group, Tq, causal, window, level;
+  int Hq, group, Tq, causal, window;
   float scale;
 };
 
@@ -232,45 +231,45 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdArgs a) {
     if (a.lse && live && h == 0)
       a.lse[(int64_t)head * a.Tq + e.row0 + row] = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * LN2;
   } else if (live) {
-    store_floats(a.part + x.part * a.part_size + ((int64_t)(e.row0 + row) * a.Hq + head) * HD, O, h);
-    if (h == 0) *reinterpret_cast<float2 *>(a.ml + x.part * a.ml_size + 2 * ((int64_t)head * a.Tq + e.row0 + row)) = make_float2(m, l);
+    const int64_t to = ((int64_t)x.slot * a.Hq + head) * ATT_QTILE + row;
+    store_floats(a.part + to * HD, O, h);
+    if (h == 0) *reinterpret_cast<float2 *>(a.ml + 2 * to) = make_float2(m, l);
   }
 }
 
-// Joins the parts of a tile's rows: 16 threads a row, 8 channels each.
-__global__ __launch_bounds__(256) void attn_fwd_join_kernel(FwdArgs a) {
-  const int rows = ATT_QTILE / 16;  // blocks a tile
-  const int64_t b = blockIdx.x / rows;
-  const int head = (int)(b % a.Hq);
-  const TileEntry e(a.tiles, (int)(b / a.Hq));
-  const int parts = e.parts(a.level), r = (blockIdx.x % rows) * 16 + (threadIdx.x >> 4);
-  if (parts == 1 || r >= e.rows) return;
-  const int c = (threadIdx.x & 15) * 8;
-  const int64_t row = e.row0 + r, at = (row * a.Hq + head) * HD + c;
-  const float *ml = a.ml + 2 * ((int64_t)head * a.Tq + row);
-  float M = -1.5e38f, L = 0.f, y[8] = {};
-  for (int x = 0; x < parts; ++x) M = fmaxf(M, ml[x * a.ml_size]);
-  for (int x = 0; x < parts; ++x) {
-    const float f = __builtin_amdgcn_exp2f(ml[x * a.ml_size] - M);
-    L = fmaf(ml[x * a.ml_size + 1], f, L);
-    const f32x4 *src = reinterpret_cast<const f32x4 *>(a.part + x * a.part_size + at);
-    const f32x4 u = src[0], v = src[1];
+// Joins the parts of a tile's rows: a block takes its slot's share of the rows, 16 threads a row, 8 channels each.
+__global__ __launch_bounds__(ATT_JOIN) void attn_fwd_join_kernel(FwdArgs a) {
+  const Share x(a.items, blockIdx.x, a.Hq);
+  if (x.parts == 1) return;
+  const TileEntry e(a.tiles, x.tile);
+  const int head = x.head, c = (threadIdx.x & 15) * 8, last = e.rows * (x.part + 1) / x.parts;
+  const int64_t first = ((int64_t)(x.slot - x.part) * a.Hq + head) * ATT_QTILE, next = (int64_t)a.Hq * ATT_QTILE;  // rows of the parts
+  for (int r = e.rows * x.part / x.parts + (threadIdx.x >> 4); r < last; r += ATT_JOIN / 16) {
+    const int64_t row = e.row0 + r;
+    const float *ml = a.ml + 2 * (first + r);
+    float M = -1.5e38f, L = 0.f, y[8] = {};
+    for (int i = 0; i < x.parts; ++i) M = fmaxf(M, ml[2 * i * next]);
+    for (int i = 0; i < x.parts; ++i) {
+      const float f = __builtin_amdgcn_exp2f(ml[2 * i * next] - M);
+      L = fmaf(ml[2 * i * next + 1], f, L);
+      const f32x4 *src = reinterpret_cast<const f32x4 *>(a.part + (first + r + i * next) * HD + c);
+      const f32x4 u = src[0], v = src[1];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = fmaf(u[i], f, y[i]), y[4 + i] = fmaf(v[i], f, y[4 + i]);
+      for (int z = 0; z < 4; ++z) y[z] = fmaf(u[z], f, y[z]), y[4 + z] = fmaf(v[z], f, y[4 + z]);
+    }
+    const float f = L == 0.f ? 0.f : 1.f / L;
+    *reinterpret_cast<u32x4 *>(a.o + (row * a.Hq + head) * HD + c) =
+        u32x4{pk2bf(y[0] * f, y[1] * f), pk2bf(y[2] * f, y[3] * f), pk2bf(y[4] * f, y[5] * f), pk2bf(y[6] * f, y[7] * f)};
+    if (a.lse && c == 0) a.lse[(int64_t)head * a.Tq + row] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * LN2;
   }
-  const float f = L == 0.f ? 0.f : 1.f / L;
-  *reinterpret_cast<u32x4 *>(a.o + at) =
-      u32x4{pk2bf(y[0] * f, y[1] * f), pk2bf(y[2] * f, y[3] * f), pk2bf(y[4] * f, y[5] * f), pk2bf(y[6] * f, y[7] * f)};
-  if (a.lse && c == 0) a.lse[(int64_t)head * a.Tq + row] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * LN2;
 }
 
 FwdArgs args(const gdr_attn &p, uint16_t *o, float *lse, void *ws) {
-  const AttnWorkspace w = attn_workspace(p);
-  const AttnShare share = ws ? w.q : AttnShare{-1, 1, p.plan.n_q_tiles, 0};
+  const AttnShare share = ws ? attn_q_share(p) : AttnShare{-1, 1, p.plan.n_q_tiles, 0, 0};
   float *part = static_cast<float *>(ws);
-  return FwdArgs{p.q, p.k, p.v, p.tile_table, share.level < 0 ? nullptr : p.tile_table + share.items, o, lse, part, part + share.parts * (w.q_part / 4), p.q_stride, p.k_stride, p.v_stride,
-                 w.q_part / 4, ((int64_t)p.T_q * p.H_q * 8 + 255) / 256 * 64, p.H_q, p.H_q / p.H_kv, p.T_q, p.causal,
-                 p.window < p.T_k ? p.window : 0, share.level, p.scale};
+  return FwdArgs{p.q, p.k, p.v, p.tile_table, share.level < 0 ? nullptr : p.tile_table + share.items, o, lse, part,
+                 part + share.slots * p.H_q * ATT_QPART, p.q_stride, p.k_stride, p.v_stride, p.H_q, p.H_q / p.H_kv, p.T_q, p.causal,
+                 p.window < p.T_k ? p.window : 0, p.scale};
 }
 
 }  // namespace
@@ -283,7 +282,7 @@ hipError_t launch_attn_fwd(const gdr_attn &p, uint16_t *o, float *lse, void *ws,
 }
 hipError_t launch_attn_fwd_join(const gdr_attn &p, uint16_t *o, float *lse, void *ws, hipStream_t stream) {
   if (p.plan.n_q_tiles == 0) return hipSuccess;
-  attn_fwd_join_kernel<<<dim3((uint32_t)((int64_t)p.plan.n_q_tiles * p.H_q * (ATT_QTILE / 16))), 256, 0, stream>>>(args(p, o, lse, ws));
+  attn_fwd_join_kernel<<<dim3((uint32_t)(attn_q_share(p).slots * p.H_q)), ATT_JOIN, 0, stream>>>(args(p, o, lse, ws));
   return hipGetLastError();
 }
 

@@ -1,5 +1,6 @@
 """The attention layers' operators where a formula's terms cancel or leave the ordinary
-range: rows that see one key, values in the cache that are not finite."""
+range: rows that see one key, values in the cache that are not finite, long
+documents among many short ones."""
 import pytest
 import torch
 
@@ -86,3 +87,49 @@ def test_held_values_that_are_not_finite(lens, runs, Hq, Hkv, page, window, pois
     assert nan.any() and torch.isnan(o).equal(nan)
     want, bound = ref.attention(q, K.nan_to_num(0.0), V.nan_to_num(0.0), cu, held, True, window)["o"]
     ref.check("o", o[~nan], want[~nan], bound[~nan])
+
+
+@pytest.mark.parametrize("docs,docs_k,Hq,Hkv,window", [
+    ([16] + [100, 7] * 20, [9000] + [100, 7] * 20, 4, 2, 0), ([1500, 1, 129], None, 3, 1, 0), ([70] + [1] * 50, [20000] + [1] * 50, 2, 1, 0),
+    ([4000, 300], None, 2, 2, 700), ([5, 2500], [4000, 2600], 8, 1, 0),
+])
+def test_parts_stay_in_their_workspaces(docs, docs_k, Hq, Hkv, window):
+    """Shared tiles, both ways, in workspaces of just the bytes asked for: right, and nothing behind them is touched."""
+    cu, ck = cu_of(docs), cu_of(docs_k or docs)
+    g = gen(cu[-1] + Hq)
+    q, k, v, do = heads(g, cu[-1], Hq), heads(g, ck[-1], Hkv), heads(g, ck[-1], Hkv), heads(g, cu[-1], Hq).contiguous()
+    plan = gdr.AttnPlan(cu, ck, window=window)
+    first = gdr.AttnProblem(q, k, v, plan)
+    assert first._fwd_bytes > 0
+
+    def around(n):
+        return torch.full((n + 4096,), 0xFF, dtype=torch.uint8, device="cuda")
+
+    fwd, bwd = around(first._fwd_bytes), around(first.workspace_bytes())
+    first._fwd_ws = fwd
+    p = gdr.AttnProblem(q, k, v, plan, share=first)
+    assert p._fwd_ws is fwd
+    o, lse = torch.empty(q.shape, dtype=BF, device="cuda"), torch.empty(Hq, cu[-1], device="cuda")
+    gdr.attn_fwd(p, o, lse)
+    grads = [torch.empty(x.shape, dtype=BF, device="cuda") for x in (q, k, v)]
+    gdr.attn_bwd(p, o, lse, do, *grads, bwd[: p.workspace_bytes()])
+    assert (fwd[p._fwd_bytes:] == 0xFF).all() and (bwd[p.workspace_bytes():] == 0xFF).all()
+    want = ref.attention(q, k, v, cu, ck, True, window, dout=do)
+    for name, x in zip(("o", "lse", "dq", "dk", "dv"), (o, lse, *grads)):
+        ref.check(name, x, *want[name])
+
+
+def test_shared_workspaces():
+    g, cu = gen(31), [0, 2000]
+    q, k, v = heads(g, 2000, 4), heads(g, 2000, 2), heads(g, 2000, 2)
+    plan, small = gdr.AttnPlan(cu), gdr.AttnPlan([0, 40])
+    one = gdr.AttnProblem(q, k, v, plan)
+    two = gdr.AttnProblem(k, q[:, :2].contiguous(), v, plan, share=gdr.AttnProblem(k, v, v, plan))
+    for p in (one, two, gdr.AttnProblem(v, k, k, plan, share=one)):
+        o, lse = torch.empty(p.q.shape, dtype=BF, device="cuda"), torch.empty(p.H_q, 2000, device="cuda")
+        gdr.attn_fwd(p, o, lse)
+        ref.check("o", o, *ref.attention(p.q, p.k, p.v, cu, cu)["o"])
+    tiny = gdr.AttnProblem(q[:40], k[:40], v[:40], small)
+    assert gdr.AttnProblem(q[:40], k[:40], v[:40], small, share=one)._fwd_ws is None
+    with pytest.raises(gdr.GdrError, match="shared workspace"):
+        gdr.AttnProblem(q, k, v, plan, share=tiny)
