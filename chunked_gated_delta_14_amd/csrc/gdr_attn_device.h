@@ -162,6 +162,10 @@ struct TileEntry {
 // The kernels that join parts: threads of a block, 16 to a row.
 constexpr int ATT_JOIN = 512;
 
+// Where a running maximum m starts: finite, so that a hidden score, -infinity, less it stays -infinity and gives a
+// probability of 0, and below every score.  A probability's exponent S c - m is one fma and m a rounded product: what that
+// rounding cuts off scales all of a row's probabilities, by 2^64 at most for scores of up to 2^30, which sums and quotient hold.
+constexpr float LEAST = -3.402823466e38f;
 constexpr float LOG2E = 1.44269504088896341f;
 constexpr float LN2 = 0.693147180559945309f;
 

@@ -88,7 +88,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdArgs a) {
 #pragma unroll
   for (int dt = 0; dt < 4; ++dt) O[dt] = zero16();
   const float c = a.scale * LOG2E;
-  float m = -1.5e38f, l = 0.f;  // of scores in powers of two; finite, so that hidden scores stay at 0
+  float m = LEAST, l = 0.f;  // of scores in powers of two
 
   const uint32_t lds0 = lds_addr(lds);
   uint32_t ko[4], vo[4];
@@ -247,7 +247,7 @@ __global__ __launch_bounds__(ATT_JOIN) void attn_fwd_join_kernel(FwdArgs a) {
   for (int r = e.rows * x.part / x.parts + (threadIdx.x >> 4); r < last; r += ATT_JOIN / 16) {
     const int64_t row = e.row0 + r;
     const float *ml = a.ml + 2 * (first + r);
-    float M = -1.5e38f, L = 0.f, y[8] = {};
+    float M = LEAST, L = 0.f, y[8] = {};
     for (int i = 0; i < x.parts; ++i) M = fmaxf(M, ml[2 * i * next]);
     for (int i = 0; i < x.parts; ++i) {
       const float f = __builtin_amdgcn_exp2f(ml[2 * i * next] - M);

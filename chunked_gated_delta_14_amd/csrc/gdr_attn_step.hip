@@ -92,7 +92,7 @@ __global__ __launch_bounds__(256, 3) void attn_step_kernel(StepArgs a) {
     f32x4 O[8];
 #pragma unroll
     for (int d = 0; d < 8; ++d) O[d] = zero4();
-    float m = -1.5e38f, l = 0.f;
+    float m = LEAST, l = 0.f;
     // Values that are NaN (a scale byte of 255) in tiles that not every row sees all of: there they count as finite, as 0
     // times them would reach rows that they are hidden from.  Bit 8 b + 7: this lane's row sees one in its channels 32 b .. .
     uint32_t bad = 0;
@@ -275,7 +275,7 @@ __global__ __launch_bounds__(256) void attn_step_join_kernel(StepArgs a) {
   const int used = (s.len - (s.begin & ~31) + s.per - 1) / s.per;
   for (int i = 0; i < s.run; ++i) {
     const int64_t row = (int64_t)(s.t0 + i) * a.Hq + head, at = row * a.splits;
-    float m = -1.5e38f, l = 0.f, o[8] = {};
+    float m = LEAST, l = 0.f, o[8] = {};
     for (int x = y; x < used; x += 16) {
       const float mx = a.ml[2 * (at + x)], lx = a.ml[2 * (at + x) + 1];
       const f32x4 *src = reinterpret_cast<const f32x4 *>(a.part + (at + x) * HD + c);
@@ -292,7 +292,7 @@ __global__ __launch_bounds__(256) void attn_step_join_kernel(StepArgs a) {
     __syncthreads();
     if (threadIdx.x < HD) {
       const int groups = min(used, 16);
-      float M = -1.5e38f, L = 0.f, z = 0.f;
+      float M = LEAST, L = 0.f, z = 0.f;
       for (int x = 0; x < groups; ++x) M = fmaxf(M, sm[x]);
       for (int x = 0; x < groups; ++x) {
         const float f = __builtin_amdgcn_exp2f(sm[x] - M);

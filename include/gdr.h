@@ -467,6 +467,8 @@ int32_t gdr_rope_bwd(const gdr_rope *p, const void *dq_out, int64_t dq_out_strid
  * every key of the document without `causal`.  0 < scale <= 2^64.  Query head h reads kv head h / (H_q / H_kv).
  *     o_i = sum_j P_ij v_j,   P_ij = exp(scale q_i k_j - lse_i),   lse_i = log sum_j exp(scale q_i k_j)
  * A row that sees no key has o = 0 and lse = -inf, and its gradients are zero.
+ * Scores scale q k are fp32 numbers and may have magnitudes of up to 2^30; past that a row's output may be anything.
+ * The backward's probabilities are off by up to 2^-22 of themselves times their score's and lse's magnitude.
  * Probabilities and their gradients are rounded to bf16 for the matrix products, which
  * sum in fp32.  Rows start 16-byte aligned (strides are multiples of 8).  A hidden key
  * or value does not reach a row's forward output, finite or not; the backward takes finite operands: a
@@ -545,7 +547,7 @@ int32_t gdr_kv_load(const gdr_kv *p, int32_t T, const int32_t *cu_seqlens, const
  * Sequence n takes rows cu_seqlens[n] .. cu_seqlens[n+1] - 1 of q (row n when cu_seqlens is
  * NULL; T == N) and holds lens[n] tokens, the rows' own among them (stored before the call):
  * the last row sees all of them, the one before all but the last, and so on, each within
- * `window` tokens up to its own (0: all).  lens is clipped to [0, max_pages * page], which is at most
+ * `window` tokens up to its own (0: all).  Scores and scale are as in gdr_attn_fwd.  lens is clipped to [0, max_pages * page], which is at most
  * 2^30 here, and cu_seqlens to [0, T].  Keys of a page outside [0, n_pages) are hidden.  A row that sees no key gets 0;
  * rows that no sequence covers are left as they were.  Channels that read as NaN reach the rows that see
  * their token, and no others.  Workspace: gdr_attn_step_workspace_bytes. */

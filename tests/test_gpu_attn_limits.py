@@ -1,6 +1,6 @@
 """The attention layers' operators where a formula's terms cancel or leave the ordinary
 range: rows that see one key, values in the cache that are not finite, long
-documents among many short ones."""
+documents among many short ones, scores far from zero."""
 import pytest
 import torch
 
@@ -133,3 +133,38 @@ def test_shared_workspaces():
     assert gdr.AttnProblem(q[:40], k[:40], v[:40], small, share=one)._fwd_ws is None
     with pytest.raises(gdr.GdrError, match="shared workspace"):
         gdr.AttnProblem(q, k, v, plan, share=tiny)
+
+
+FAR = [(2.0 ** 63, -(2.0 ** 64)), (1.171875 * 2.0 ** 15, -1.5 * 2.0 ** 14), (1.171875 * 2.0 ** 15, 1.5 * 2.0 ** 14),
+       (1.171875 * 2.0 ** 14, -1.5 * 2.0 ** 10), (1.171875 * 2.0 ** 14, 1.5 * 2.0 ** 10), (1.171875 * 2.0 ** 8, 1.5 * 2.0 ** 7)]
+
+
+@pytest.mark.parametrize("a,b", FAR)
+@pytest.mark.parametrize("T", [3, 300, 2600])
+def test_scores_far_from_zero(T, a, b):
+    """Scores of a b, up to 2^30, and one whose product with log2 e rounds nothing off, far below: all keys of a row count the same."""
+    g, cu = gen(T), [0, T]
+    q, k, v = (torch.zeros(T, h, 128, dtype=BF, device="cuda") for h in (2, 1, 1))
+    q[..., 7], k[..., 7] = a, b
+    v.copy_(torch.randint(-8, 9, v.shape, generator=g, device="cuda"))
+    p = gdr.AttnProblem(q, k, v, gdr.AttnPlan(cu), scale=1.0)
+    o, lse = torch.empty_like(q), torch.empty(2, T, device="cuda")
+    gdr.attn_fwd(p, o, lse)
+    count = torch.arange(1, T + 1, device="cuda").double()
+    mean = v.double().cumsum(0) / count[:, None, None]
+
+    def near(got, mean):  # one probability, rounded to bf16 for the products, times whole numbers: sums are exact; the quotient is rounded twice
+        assert ((got.double() - mean).abs() <= (2.0 ** -7 + 2.0 ** -14) * mean.abs()).all()
+
+    near(o, mean)
+    assert ((lse.double() - a * b - count.log()).abs() <= abs(a * b) * 2.0 ** -21 + 2.0 ** -19).all()
+    cache, table = pool(g, [T], 1, 16)
+    every = gdr.KvProblem(cache, table, None, T, ints(cu))
+    gdr.kv_store(every, k, v)
+    K, V = torch.empty_like(k), torch.empty_like(v)
+    gdr.kv_load(every, K, V)
+    assert K.equal(k)
+    s = gdr.AttnStep(q[-1:], cache, table, ints([T]), scale=1.0)
+    one = torch.empty(1, 2, 128, dtype=BF, device="cuda")
+    gdr.attn_step(s, one, s.alloc_workspace())
+    near(one, V.double().mean(0))
