@@ -165,7 +165,12 @@ class AttnPlan:
         import torch
 
         def host(cu):
-            return np.ascontiguousarray(np.asarray(cu.cpu() if hasattr(cu, "cpu") else cu, dtype=np.int32))
+            cu = np.asarray(cu.cpu() if hasattr(cu, "cpu") else cu)
+            if cu.size and cu.dtype.kind not in "iu":
+                _bad("cu_q and cu_k must be ints, not %s" % cu.dtype)
+            if cu.size:
+                _sizes(int(cu.min()), int(cu.max()))
+            return np.ascontiguousarray(cu, dtype=np.int32)
 
         cu_q = host(cu_q)
         cu_k = cu_q if cu_k is None else host(cu_k)

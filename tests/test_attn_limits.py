@@ -3,7 +3,9 @@ refusal here stands for sizes that the kernels' 32-bit arithmetic would not hold
 import ctypes
 import random
 
+import numpy as np
 import pytest
+import torch
 
 import chunked_gated_delta_14_amd as gdr
 from test_attn_host import BIG, OUT, kv, plan, problem, refused, step
@@ -65,3 +67,20 @@ def test_lists_of_parts():
                 assert len(seen) == (count if m else 0)
                 assert last <= (2 * sum(steps)) // (1 << level)
         assert at == p.table_len
+
+
+@pytest.mark.parametrize("cu", [
+    torch.tensor([0, (1 << 32) + 5, (1 << 32) + 9]), np.array([0, 5, (1 << 33) + 9]), [0, 5, 1 << 40], np.array([0, -(1 << 32), 9]), [0, 2.5, 9.9],
+    torch.tensor([0.0, 5.0, 9.0]),
+])
+def test_plan_takes_ints_of_32_bits(cu):
+    """Wider ones would be cut to their low bits, and parts of tokens to whole ones, without a word."""
+    for args in ((cu, None), ([0, 5, 9], cu)):
+        with pytest.raises(gdr.GdrError, match="32 bits|ints"):
+            gdr.AttnPlan(*args, device="cpu")
+
+
+@pytest.mark.parametrize("cu", [[0, 5, 9], (0, 5, 9), np.array([0, 5, 9], np.uint8), torch.tensor([0, 5, 9]), torch.tensor([0, 5, 9], dtype=torch.int32)])
+def test_plan_takes_ints_of_any_kind(cu):
+    p = gdr.AttnPlan(cu, device="cpu")
+    assert (p.N, p.T_q, p.T_k) == (2, 9, 9)
