@@ -4,9 +4,9 @@
 //
 // Bound by the rows' bytes.  All heads of a token share their angles, so a block first
 // forms the sines and cosines of its few tokens in LDS and then streams the heads.
-// An angle is kept in turns: p f_i is one fp64 product (p below 2^31 leaves 22 bits
-// behind the point to a turn), its fraction goes to fp32, and the sine and cosine of that are
-// good to an ulp or two at any position.  A thread of the second part owns up to 16
+// An angle is kept in turns: an fp64 fma takes the whole turns off p f_i before it rounds, and the fraction goes to
+// fp32.  So sine and cosine are those of the frequency given, to a few roundings, at any position; that frequency's own
+// rounding to fp64 grows with the position (2^-25 turn at p f = 2^28).  A thread of the second part owns up to 16
 // bytes of a row's each side of the pairs: 8 (bf16) or 4 (fp32) pairs of half
 // layout, half as many neighbouring pairs; what is left of R and of the channels that
 // pass goes by single pairs and channels.  [261392, 16 + 4 heads] bf16 492 us, 5.4 TB/s, above what a large
@@ -88,9 +88,9 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
   if (n <= 0) return;
   for (int e = threadIdx.x; e < n * half; e += 256) {
     const int t = e / half, i = e - t * half;
-    const double x = (double)(a.pos ? a.pos[t0 + t] : first + t) * a.freqs[i];
+    const double p = (double)(a.pos ? a.pos[t0 + t] : first + t), f = a.freqs[i];
     float s, c;
-    sincospif((float)(2.0 * (x - rint(x))), &s, &c);
+    sincospif((float)(2.0 * fma(p, f, -rint(p * f))), &s, &c);
     cs[e] = make_float2(c * a.magnitude, s * a.magnitude * a.sign);
   }
   __syncthreads();

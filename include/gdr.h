@@ -424,8 +424,8 @@ int32_t gdr_norm_bwd(const gdr_norm *p, const void *dy, const void *ds, void *dx
  * angle p f_i of the token's position p, with f_i = freqs[i] turns a token:
  *     (a, b) -> magnitude (a cos - b sin, b cos + a sin)
  * GDR_ROPE_HALF pairs channels (i, i + rot/2), GDR_ROPE_PAIRS (2i, 2i + 1); channels
- * from rot on pass unchanged.  Angles are reduced in fp64, so far positions keep
- * their precision.  An output may have its input's address and stride (in place:
+ * from rot on pass unchanged.  Angles are reduced in fp64 without rounding the product, so at far
+ * positions they are off by no more than p times what the frequency given is.  An output may have its input's address and stride (in place:
  * only the rotated channels are then touched); other overlaps are the caller's. */
 enum gdr_rope_layout { GDR_ROPE_HALF = 0, GDR_ROPE_PAIRS = 1 };
 typedef struct gdr_rope {

@@ -1,6 +1,10 @@
 """The attention layers' operators where a formula's terms cancel or leave the ordinary
 range: rows that see one key, values in the cache that are not finite, long
-documents among many short ones, scores far from zero."""
+documents among many short ones, scores far from zero, positions
+whose angles come back to nearly nothing."""
+import math
+from fractions import Fraction
+
 import pytest
 import torch
 
@@ -168,3 +172,35 @@ def test_scores_far_from_zero(T, a, b):
     one = torch.empty(1, 2, 128, dtype=BF, device="cuda")
     gdr.attn_step(s, one, s.alloc_workspace())
     near(one, V.double().mean(0))
+
+
+def test_far_positions_keep_small_angles():
+    """Angles by whole-number arithmetic from the frequencies given: far positions chosen so that p f_i comes within 2^-20 to 2^-30
+    turns of a whole number, whose sine is then the angle, to a few roundings of itself."""
+    freqs = gdr.rope_freqs(16, 10.0)
+    exact = [Fraction(x) for x in freqs.tolist()]
+    pos, g = [], torch.Generator().manual_seed(3)
+    for f in exact:  # denominators of f's continued fraction: p f is nearly whole
+        a, b, p0, p1 = f.numerator, f.denominator, 1, 0
+        while b:
+            a, b, p0, p1 = b, a % b, p1, (a // b) * p1 + p0
+            if p1 >= 1 << 31:
+                break
+            pos += [p1] if p1 > 1 << 12 else []
+    pos += torch.randint(0, 2 ** 31 - 1, (200,), generator=g).tolist() + [2 ** 31 - 1, -(2 ** 31)]
+    T = len(pos)
+    x = torch.zeros(T, 1, 16, device="cuda")
+    x[..., :8] = 1.0  # (1, 0) becomes (cos, sin)
+    y = torch.empty_like(x)
+    gdr.rope_fwd(gdr.RopeProblem(x, None, freqs, positions=torch.tensor(pos, dtype=torch.int32, device="cuda")), y)
+    small = 0
+    for t, row in enumerate(y[:, 0].double().tolist()):
+        for i, f in enumerate(exact):
+            turns = pos[t] * f
+            turns = float(turns - round(turns))
+            small += abs(turns) < 2.0 ** -24
+            # the fraction of a turn is rounded to fp32, which is relative to it (2 pi |turns| 2^-24 of angle, at most pi 2^-24), and sine and
+            # cosine are good to 4 ulp; near zero turns the angle's error is the sine's, relative, and none of the cosine's
+            for got, want in ((row[i], math.cos(2 * math.pi * turns)), (row[8 + i], math.sin(2 * math.pi * turns))):
+                assert abs(got - want) <= 2.0 ** -21 * abs(want) + (math.pi * 2.0 ** -24 if abs(turns) > 0.125 else 0.0), (pos[t], i)
+    assert small > 20, small
