@@ -130,6 +130,7 @@ int32_t attn_fwd(const gdr_attn *p, uint16_t *o, float *lse, void *ws, int64_t w
   const gdr::AttnWorkspace w = gdr::attn_workspace(*p);
   if (ws && (rc = check_workspace(ws, ws_bytes, w.fwd))) return rc;
   if (aliases({o, lse}, {p->q, p->k, p->v, p->tile_table})) return invalid("o or lse is an input");
+  if (aliases({o}, {lse})) return invalid("o and lse are the same memory");
   if ((rc = gdr::host_check_device())) return rc;
   if ((rc = launch(gdr::TK_ATTN_FWD, stream, "attention launch",
                    [&](hipStream_t s) { return gdr::launch_attn_fwd(*p, o, lse, ws, s); })))

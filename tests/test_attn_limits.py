@@ -84,3 +84,8 @@ def test_plan_takes_ints_of_32_bits(cu):
 def test_plan_takes_ints_of_any_kind(cu):
     p = gdr.AttnPlan(cu, device="cpu")
     assert (p.N, p.T_q, p.T_k) == (2, 9, 9)
+
+
+def test_forward_outputs_are_two():
+    L, p = gdr.lib(), problem()
+    refused(L.gdr_attn_fwd(ctypes.byref(p), OUT, OUT, None, 0, None), 1, "same memory")
