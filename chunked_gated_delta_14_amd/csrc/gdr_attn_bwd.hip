@@ -11,8 +11,8 @@
 //   attn_dkv: 32 keys a wavefront, query rows and output gradients of all of the kv head's
 //             query heads through LDS.
 // Each forms S and dP as 32 x 32 tiles whose registers, rounded to bf16, are the next
-// product's operand as they stand.  P and dS carry a relative 2^-9 from that, of either
-// sign, into sums that are rounded by 2^-9 at their end.
+// product's operand as they stand.  P and dS carry up to a relative 2^-8 from that, of either
+// sign where scores differ, into sums that are rounded by up to 2^-8 at their end.
 //
 // Bound by the matrix units at the clock that their power leaves: 32674 causal rows of 16 heads on 4 take
 // 5.55 ms (attn_dq: three products, 1.18 PFLOP/s, matrix units 0.66 of the cycles busy) and 8.1 ms (attn_dkv:

@@ -9,8 +9,9 @@
 // O^T += V^T P^T as they stand, V^T read from LDS by transposing reads.
 // The running maximum is only moved, and the sums rescaled, when a row's grows by more
 // than 2^8: until then the probabilities are up to 2^8 instead of 1, which costs neither
-// fp32 nor bf16 any precision.  Probabilities go to bf16 for the second product (a
-// relative 2^-9 each, of either sign, where the output is rounded by 2^-9 anyway); their sum is taken in fp32 before.
+// fp32 nor bf16 any precision.  Probabilities go to bf16 for the second product, off by
+// up to a relative 2^-8 each as the output is by its own rounding; their sum is taken in fp32 before.  Between different
+// scores these errors have either sign; a row of equal ones has the same one throughout, and carries it to its output.
 //
 // Bound by the matrix units at the clock that their power leaves: 32674 causal rows of 16
 // heads on 4 take 4.04 ms, 1.08 PFLOP/s, where a bf16 product of 8192^3 reaches 1.23-1.29 on the same cards;

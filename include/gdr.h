@@ -547,10 +547,11 @@ int32_t gdr_kv_load(const gdr_kv *p, int32_t T, const int32_t *cu_seqlens, const
  * Sequence n takes rows cu_seqlens[n] .. cu_seqlens[n+1] - 1 of q (row n when cu_seqlens is
  * NULL; T == N) and holds lens[n] tokens, the rows' own among them (stored before the call):
  * the last row sees all of them, the one before all but the last, and so on, each within
- * `window` tokens up to its own (0: all).  Scores and scale are as in gdr_attn_fwd.  lens is clipped to [0, max_pages * page], which is at most
- * 2^30 here, and cu_seqlens to [0, T].  Keys of a page outside [0, n_pages) are hidden.  A row that sees no key gets 0;
- * rows that no sequence covers are left as they were.  Channels that read as NaN reach the rows that see
- * their token, and no others.  Workspace: gdr_attn_step_workspace_bytes. */
+ * `window` tokens up to its own (0: all).  Scores and scale are as in gdr_attn_fwd.  lens is clipped to
+ * [0, max_pages * page], which is at most 2^30 here, and cu_seqlens to [0, T].  Keys of a page outside
+ * [0, n_pages) are hidden.  A row that sees no key gets 0; rows that no sequence covers are left as they were.
+ * What reads as NaN reaches the rows that see its token (a key all their channels, a value its 32), and no
+ * others.  Workspace: gdr_attn_step_workspace_bytes. */
 typedef struct gdr_attn_step {
   int32_t T, H_q, window;
   float scale;
@@ -575,7 +576,7 @@ int32_t gdr_attn_step_fwd(const gdr_kv *cache, const gdr_attn_step *p, uint16_t 
  * "conv_step", "gate_fwd", "gate_bwd", "step", "norm_fwd", "norm_bwd",
  * "param_sum" (the sums of the parameter gradients' partials), "rope", "attn_fwd",
  * "attn_dq", "attn_dkv", "kv_store", "kv_load", "attn_step" and "attn_join" (partial results
- * of attn_dkv and attn_step).  Not thread-safe with
+ * of attn_fwd, attn_dq, attn_dkv and attn_step).  Not thread-safe with
  * respect to concurrent calls that are being timed. */
 int32_t gdr_timing_enable(int32_t on);
 int32_t gdr_timing_read(const char **names, double *total_ms, int64_t *launches, int32_t capacity,
