@@ -6,9 +6,9 @@
 //
 // Bound by the bytes, 256 + 68 a token, head and side.  16 lanes take a row of 128 channels,
 // 8 each: 16 bytes of bf16 and 4 of codes, so both sides' accesses are whole lines; four
-// lanes share a block, whose maximum they find by two lane swaps.  32674 tokens of 4 heads: stored in
-// 21 us, 4.0 TB/s, read back in 17 us, 5.2 TB/s (the same tokens again; both calls 36 us, 43 on tokens that are not in the caches).  (Codes by comparing with every border instead of the hardware's
-// conversion: 35 us, the vector units' time.)
+// lanes share a block, whose maximum they find by two lane swaps.  32674 tokens of 4 heads: stored in 21 us, 4.0 TB/s,
+// read back in 17 us, 5.2 TB/s (the same tokens again; both calls 36 us, 43 on tokens that the caches do not hold).  (Codes
+// by comparing with every border instead of the hardware's conversion: 35 us, the vector units' time.)
 #include "gdr_attn.h"
 #include "gdr_vec.h"
 
